@@ -182,10 +182,12 @@ def plain_codes(v):
     v = v.to(F32)
     amax = v.abs().amax(-1, keepdim=True)
     a = amax.clamp_min(TINY)
-    codes = torch.round(v * (127.0 / a))
+    # quotients of two tensors: one with a plain number is taken by way of a reciprocal, which is rounded twice
+    most = torch.full_like(a, 127.0)
+    codes = torch.round(v * (most / a))
     fine = torch.isfinite(amax)
     codes = torch.where(fine, codes, torch.zeros_like(codes)).to(torch.int8)
-    return codes, torch.where(fine, a / 127.0, torch.full_like(a, math.nan)).squeeze(-1)
+    return codes, torch.where(fine, a / most, torch.full_like(a, math.nan)).squeeze(-1)
 
 
 def plain_norm(s):
