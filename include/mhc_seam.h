@@ -330,6 +330,165 @@ int mhc_mxfp8_gemm(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
 int mhc_mxfp8_gemm_blocks(int64_t T, int32_t N, int32_t cu_count, int32_t *tm, int32_t *tn,
                           int32_t *stages);
 
+/* ------------------------------------------------ one-stream block boundary
+ *
+ * The operators below serve models with one residual stream, int8 products
+ * and experts.  They need no handle, hold no state and no workspace, allocate
+ * nothing and enqueue one launch on `stream` (NULL for the default stream) of
+ * the current device; calls on any number of streams may overlap and may be
+ * captured into graphs.  Tensors are dense, row-major and on the current
+ * device; pointers are 16-byte aligned unless said otherwise.  INVALID_ARG or
+ * HIP_ERROR on failure.
+ */
+typedef enum mhc_dtype {
+    MHC_BF16 = 0,
+    MHC_F16 = 1,
+    MHC_F32 = 2
+} mhc_dtype;
+
+typedef enum mhc_gate {
+    MHC_GATE_NONE = 0,
+    MHC_GATE_TOKEN = 1,    /* f32 [T]     one factor for each token */
+    MHC_GATE_CHANNEL = 2,  /* f32 [H]     one for each channel */
+    MHC_GATE_ELEMENT = 3   /* dtype [T][H] */
+} mhc_gate;
+
+/*
+ * Norms before and after a sub-layer with its gate and residual scale, the
+ * one-stream counterpart of the seam: per token t
+ *   p    = y rstd(y) gamma_post                     (p = y without gamma_post)
+ *   r    = residual_scale x + branch_scale (p gate)   rounded to x_dtype
+ *   norm = r rstd(r) gamma                            rounded to dtype
+ *   rstd(v) = f32(1 / sqrt(mean_h(v^2) + eps))
+ * and, with codes, the rounded norm's int8 form (mhc_int8_quantize).
+ * Elementwise steps are binary32, each rounded on its own in the order
+ * ((y rstd) gamma_post) gate, (residual_scale x) + (branch_scale p), (r rstd)
+ * gamma; the sums of squares are binary64, so results do not depend on how a
+ * row is split and the codes are those mhc_int8_quantize gives for norm.
+ * Without y (the first block): r = x, no residual_out.  Without gamma (after
+ * the last block): residual_out only.
+ * A pointer must be set exactly when the call uses it, and be NULL otherwise:
+ *   x             x_dtype [T][H]   always; x_dtype is dtype or MHC_F32
+ *   y             dtype [T][H]     optional; gamma_post and gate only with it
+ *   gamma_post    dtype [H]        optional
+ *   gate          see mhc_gate     exactly when gate_kind is not NONE
+ *   gamma         dtype [H]        optional; at least one of y and gamma
+ *   residual_out  x_dtype [T][H]   exactly with y; may be x itself (in place)
+ *   norm          dtype [T][H]     with gamma; optional when codes are given
+ *   codes         int8 [T][H]      optional, with gamma
+ *   scales        f32 [T]          exactly with codes; 4-byte aligned
+ * Without y both scales must be 1.  dtype is MHC_BF16 or MHC_F16; 1 <= H <=
+ * 32768, any H; T * H < 2^40, T < 2^31.  eps in [0, 1], 0 selects 1e-6.
+ * Outputs overlap no input and no other output, but for residual_out == x.
+ * Infinities and NaN go through the arithmetic; int8 rows holding one get
+ * codes 0 and scale NaN.  T == 0 does nothing.
+ */
+typedef struct mhc_block_norm_args {
+    int64_t T;
+    int32_t H;
+    int32_t dtype;          /* mhc_dtype of y, element gates, gammas and norm */
+    int32_t x_dtype;        /* mhc_dtype of x and residual_out */
+    int32_t gate_kind;      /* mhc_gate */
+    float eps;
+    float residual_scale;
+    float branch_scale;
+    int32_t reserved;       /* 0 */
+    const void *x;
+    const void *y;
+    const void *gamma_post;
+    const void *gate;
+    const void *gamma;
+    void *residual_out;
+    void *norm;
+    int8_t *codes;
+    float *scales;
+} mhc_block_norm_args;
+
+int mhc_block_norm(const mhc_block_norm_args *args, void *stream);
+
+/*
+ * int8 form of the rows of any [rows][H] tensor (dtype MHC_BF16 or MHC_F16),
+ * one scale a row: the operand of mhc_int8_gemm.  In binary32
+ *   a = max(max_h |v|, 2^-119),  scales = a / 127,
+ *   codes = v (127 / a) rounded to the nearest whole number, ties to even
+ * (-127 .. 127).  A zero row has codes 0 and the scale of a = 2^-119.  A row
+ * holding an infinity or NaN has codes 0 and scale NaN.
+ * 1 <= H <= 32768, any H; rows * H < 2^40, rows < 2^31; src and codes 16-byte
+ * aligned, scales 4-byte; no overlap.  rows == 0 does nothing.
+ */
+int mhc_int8_quantize(const void *src, int32_t dtype, int64_t rows, int32_t H, int8_t *codes,
+                      float *scales, void *stream);
+
+/*
+ * Matrix product of int8 codes with a scale for each token and each channel:
+ *   out[t][n] = f32(sum_k a[t][k] b[n][k]) a_scales[t] b_scales[n] (+ bias[n])
+ * The sum is exact (int32); its conversion, the two products and the sum
+ * with the bias are binary32, in that order; the result is rounded once to
+ * out_dtype.
+ *   a        int8 [T][K]   a_scales f32 [T]     (activations)
+ *   b        int8 [N][K]   b_scales f32 [N]     (weights, K contiguous)
+ *   bias     f32 [N] or NULL
+ *   out      out_dtype [T][N]: MHC_BF16, MHC_F16 or MHC_F32; overlaps no input
+ * K a multiple of 16, 16 .. 131056 (every sum of codes -128 .. 127 fits);
+ * N > 0, any N; T < 2^31; T * N, T * K and N * K below 2^40.  a, b and out
+ * 16-byte aligned, scales and bias 4-byte.  Codes -128 .. 127 are all valid.
+ * A NaN scale makes its row or column NaN, over zero codes too.  T == 0 does
+ * nothing.
+ */
+int mhc_int8_gemm(const int8_t *a, const float *a_scales, const int8_t *b, const float *b_scales,
+                  const float *bias, int64_t T, int32_t N, int32_t K, int32_t out_dtype, void *out,
+                  void *stream);
+
+typedef enum mhc_scoring {
+    MHC_SOFTMAX = 0,
+    MHC_SIGMOID = 1
+} mhc_scoring;
+
+/*
+ * Routing of tokens to experts, the gates of an experts' sub-layer.  Per
+ * token, from its logits l:
+ *   s   = softmax(l) or 1 / (1 + exp(-l))
+ *   key = s + bias
+ *   groups > 1: of the groups of E / groups consecutive experts those
+ *   topk_groups stay open whose best `group_top` (1 or 2) keys sum highest
+ *   ids     = the k experts of the highest keys in open groups, highest first
+ *   weights = s[ids], divided by their sum if renormalize, times scale
+ * Equal keys and equal sums go to the lowest index.  Scores and keys are
+ * binary64, weights are rounded once to f32.
+ * A logit or a bias of -inf takes its expert out (a group's missing keys
+ * count as -1e30); where fewer than k experts are left, the other slots hold
+ * id -1 and weight 0, all of them in a row with none.  A NaN logit, or +inf
+ * under softmax, is taken out too and makes the row's weights NaN; a bias
+ * must not be NaN.  Ids are distinct and in range whatever the logits are.
+ * A renormalized row whose chosen scores sum to 0 has weights 0.
+ *   logits   dtype [T][E]  (MHC_BF16, MHC_F16 or MHC_F32); element aligned
+ *   bias     f32 [E] or NULL
+ *   weights  f32 [T][k]    ids int32 [T][k]; 4-byte aligned, no overlap
+ * 1 <= E <= 1024; groups divides E, 1 <= groups <= 64; 1 <= topk_groups <=
+ * groups; group_top 1 or 2 and at most E / groups; 1 <= k <= 64 and at most
+ * topk_groups * E / groups; without groups (groups == 1) topk_groups and
+ * group_top are 1.  T * E < 2^40, T < 2^31; T == 0 does nothing.
+ */
+typedef struct mhc_route_args {
+    int64_t T;
+    int32_t E;
+    int32_t k;
+    int32_t dtype;          /* mhc_dtype of logits */
+    int32_t scoring;        /* mhc_scoring */
+    int32_t groups;
+    int32_t topk_groups;
+    int32_t group_top;
+    int32_t renormalize;    /* 0 or 1 */
+    float scale;
+    int32_t reserved;       /* 0 */
+    const void *logits;
+    const float *bias;
+    float *weights;
+    int32_t *ids;
+} mhc_route_args;
+
+int mhc_route(const mhc_route_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

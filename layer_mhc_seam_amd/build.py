@@ -14,7 +14,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmhc_seam.so")
 SOURCES = [os.path.join(CSRC, "seam_kernels.hip"), os.path.join(CSRC, "head_kernels.hip"),
            os.path.join(CSRC, "gemm_kernels.hip"), os.path.join(CSRC, "measure_kernels.hip"),
-           os.path.join(CSRC, "seam_runtime.cpp")]
+           os.path.join(CSRC, "block_kernels.hip"), os.path.join(CSRC, "int8_kernels.hip"),
+           os.path.join(CSRC, "route_kernels.hip"),
+           os.path.join(CSRC, "seam_runtime.cpp"), os.path.join(CSRC, "block_runtime.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 

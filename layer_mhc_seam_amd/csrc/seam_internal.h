@@ -6,7 +6,15 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/mhc_seam.h"
+
 namespace mhc {
+
+// Set the calling thread's error message and return the status
+// (seam_runtime.cpp).
+int fail(int status, const char *fmt, ...) __attribute__((visibility("hidden")));
+int hip_fail(hipError_t e, const char *what) __attribute__((visibility("hidden")));
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr int kBlockTokens = 16;   // tokens per block: the MFMA M dimension
 constexpr int kWaves = 8;          // waves per workgroup
@@ -80,6 +88,53 @@ hipError_t launch_mxfp8_gemm(const uint8_t *a, const uint8_t *sa, const uint8_t 
                              hipStream_t s);
 hipError_t launch_head_reduce(const uint16_t *x, const float *w, int64_t T, int H, uint16_t *out,
                               int cus, hipStream_t s);
+
+// The one-stream block norm (block_kernels.hip); P.y, gamma_post, gate,
+// gamma, norm and codes are null where the call has none
+struct BlockNormParams {
+    int H;
+    int gate_kind;            // mhc_gate
+    float eps, residual_scale, branch_scale;
+    const void *x;
+    const void *y;
+    const void *gamma_post;
+    const void *gate;
+    const void *gamma;
+    void *residual_out;
+    void *norm;
+    int8_t *codes;
+    float *scales;
+};
+hipError_t launch_block_norm(const BlockNormParams &p, int64_t T, int dtype, int x_dtype,
+                             hipStream_t s);
+hipError_t launch_int8_quantize(const void *src, int dtype, int64_t rows, int H, int8_t *codes,
+                                float *scales, hipStream_t s);
+
+// int8 product (int8_kernels.hip)
+struct Int8GemmParams {
+    const int8_t *a;
+    const float *sa;
+    const int8_t *b;
+    const float *sb;
+    const float *bias;        // null without one
+    void *out;
+    int T, N, K;
+};
+GemmBlocks int8_gemm_blocks(int64_t T, int N, int cus);
+hipError_t launch_int8_gemm(const Int8GemmParams &p, int out_dtype, int cus, hipStream_t s);
+
+// Expert routing (route_kernels.hip)
+struct RouteParams {
+    const void *logits;
+    const float *bias;        // null without one
+    float *weights;
+    int32_t *ids;
+    int E, k, groups, keep, top;
+    int sigmoid, renorm;
+    float scale;
+};
+hipError_t launch_route(const RouteParams &p, int64_t tokens, int dtype, hipStream_t s);
+
 hipError_t launch_quantize(const uint16_t *src, int rows, int H, int group, uint8_t *codes,
                            uint8_t *scales, uint16_t *grid, hipStream_t s);
 

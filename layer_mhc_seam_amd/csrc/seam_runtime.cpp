@@ -21,12 +21,15 @@
 #include <unordered_map>
 #include <vector>
 
-#include "../../include/mhc_seam.h"
 #include "seam_internal.h"
 
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace mhc {
 
 int fail(int status, const char *fmt, ...)
 {
@@ -45,6 +48,14 @@ int hip_fail(hipError_t e, const char *what)
         return fail(MHC_SEAM_OUT_OF_MEMORY, "%s: %s", what, hipGetErrorString(e));
     return fail(MHC_SEAM_HIP_ERROR, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace mhc
+
+using mhc::aligned16;
+using mhc::fail;
+using mhc::hip_fail;
+
+namespace {
 
 struct Scratch {
     void *base = nullptr;
@@ -127,8 +138,6 @@ int check_desc(const mhc_seam_desc *d)
             return fail(MHC_SEAM_INVALID_ARG, "reserved desc fields must be zero");
     return MHC_SEAM_OK;
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_args(int H, int64_t max_tokens, const mhc_seam_args *a)
 {

@@ -17,6 +17,10 @@ OK, INVALID_ARG, UNSUPPORTED_DEVICE, OUT_OF_MEMORY, HIP_ERROR, CAPTURE_ALLOC = r
 FORMS = {"post": 0, "no_post": 1}
 OUT_DTYPES = {"bf16": 0, "fp8_grid": 1, "mxfp8": 2, "mxfp8_g128": 3}
 
+DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_ELEMENT = range(4)
+SCORINGS = {"softmax": 0, "sigmoid": 1}
+
 _P = ctypes.c_void_p
 
 
@@ -44,11 +48,30 @@ class Plan(ctypes.Structure):
                 ("reserved", ctypes.c_int32 * 2)]
 
 
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("x", _P), ("y", _P), ("gamma_post", _P), ("gate", _P), ("gamma", _P),
+                ("residual_out", _P), ("norm", _P), ("codes", _P), ("scales", _P)]
+
+
+class RouteArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scoring", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("logits", _P), ("bias", _P), ("weights", _P), ("ids", _P)]
+
+
 EXPORTS = ("mhc_seam_create", "mhc_seam_run", "mhc_seam_run_noalloc", "mhc_seam_destroy",
            "mhc_seam_validate",
            "mhc_seam_plan_for", "mhc_seam_status_string", "mhc_seam_last_error",
            "mhc_seam_copy", "mhc_stream_mix", "mhc_seam_quantize", "mhc_head_reduce",
-           "mhc_mxfp8_gemm", "mhc_mxfp8_gemm_blocks")
+           "mhc_mxfp8_gemm", "mhc_mxfp8_gemm_blocks", "mhc_block_norm", "mhc_int8_quantize",
+           "mhc_int8_gemm", "mhc_route")
 
 _lib = None
 
@@ -89,6 +112,13 @@ def lib():
                                         ctypes.POINTER(ctypes.c_int32),
                                         ctypes.POINTER(ctypes.c_int32),
                                         ctypes.POINTER(ctypes.c_int32)]
+    L.mhc_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), _P]
+    L.mhc_int8_quantize.argtypes = [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P, _P, _P]
+    L.mhc_int8_gemm.argtypes = [_P, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int32,
+                                ctypes.c_int32, ctypes.c_int32, _P, _P]
+    L.mhc_route.argtypes = [ctypes.POINTER(RouteArgs), _P]
+    for name in ("mhc_block_norm", "mhc_int8_quantize", "mhc_int8_gemm", "mhc_route"):
+        getattr(L, name).restype = ctypes.c_int
     for name in ("mhc_seam_create", "mhc_seam_run", "mhc_seam_run_noalloc", "mhc_seam_destroy",
                  "mhc_seam_validate",
                  "mhc_seam_plan_for", "mhc_seam_copy", "mhc_stream_mix", "mhc_seam_quantize",
@@ -318,3 +348,202 @@ def mxfp8_gemm(a, a_scales, b, b_scales, *, out=None, stream=None):
     _check(lib().mhc_mxfp8_gemm(_ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), T, N, K,
                                 _ptr(out), _stream_handle(stream)))
     return out
+
+
+# ------------------------------------------------ one-stream block boundary --
+#
+# Unlike the calls above, these run on the device their tensors are on,
+# whichever is current, and on that device's current stream.
+
+def _codes_of(dtypes):
+    import torch
+    names = {torch.bfloat16: "bf16", torch.float16: "f16", torch.float32: "f32"}
+    return {t: DTYPES[n] for t, n in names.items() if n in dtypes}
+
+
+def _need(name, t, dtype, shape, device):
+    """t is a dense tensor of that type and shape on that device."""
+    if t.device != device or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a tensor on {device}" if device.type == "cuda"
+                         else f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _enqueue(device, stream, call, *args):
+    """call(*args, stream) on `device`: its current stream unless one of its
+    streams is given."""
+    import torch
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(call(*args, handle))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, handle))
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_scale=1.0,
+               branch_scale=1.0, eps=1e-6, norm=True, int8=False, out=None, stream=None):
+    """Norms before and after a sub-layer with its gate and residual scale:
+    r = residual_scale x + branch_scale gate p with p = rmsnorm(y) gamma_post
+    (or y), stored as residual_out, and norm = rmsnorm(r) gamma.
+
+    x [T, H] (bf16 or f16, or f32 beside either), y [T, H], gamma and
+    gamma_post [H] bf16 or f16.  gate: f32 [T, 1] (token), f32 [H] (channel)
+    or y's type [T, H] (element).  Without y: the norm of x alone.  Without
+    gamma: residual_out alone.  int8: also the norm's codes (int8 [T, H]) and
+    scales (f32 [T]), the operand of int8_gemm; norm=False then leaves the
+    norm itself out.
+    Returns a dict of outputs (allocated unless given in `out`; residual_out
+    may be x)."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    dev = x.device
+    like = gamma if gamma is not None else y
+    if like is None:
+        raise ValueError("block_norm needs y, gamma or both")
+    dt = like.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"gamma and y must be bfloat16 or float16, got {dt}")
+    _need("x", x, torch.float32 if x.dtype == torch.float32 else dt, (T, H), dev)
+    for name, t, shape in (("gamma", gamma, (H,)), ("y", y, (T, H)), ("gamma_post", gamma_post, (H,))):
+        if t is not None:
+            _need(name, t, dt, shape, dev)
+    kind = GATE_NONE
+    if gate is not None:
+        if gate.dtype == torch.float32:
+            kind = GATE_CHANNEL if gate.dim() == 1 else GATE_TOKEN
+            _need("gate", gate, torch.float32, (H,) if kind == GATE_CHANNEL else (T, 1), dev)
+        else:
+            kind = GATE_ELEMENT
+            _need("gate", gate, dt, (T, H), dev)
+    if gamma is None and int8:
+        raise ValueError("int8 codes are those of the norm: give gamma")
+    o = dict(out) if out else {}
+    used = []
+    for name, wanted, dtype, shape in (
+            ("residual_out", y is not None, x.dtype, (T, H)),
+            ("norm", gamma is not None and norm, dt, (T, H)),
+            ("codes", int8, torch.int8, (T, H)), ("scales", int8, torch.float32, (T,))):
+        if not wanted:
+            if name in o:
+                raise ValueError(f"this call writes no {name}")
+            used.append(None)
+            continue
+        if name in o:
+            _need(name, o[name], dtype, shape, dev)
+        else:
+            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        used.append(o[name].data_ptr())
+    for name in o:
+        if name not in ("residual_out", "norm", "codes", "scales"):
+            raise ValueError(f"block_norm has no output {name}")
+    codes = _codes_of(DTYPES)
+    a = BlockNormArgs(T, H, codes[dt], codes[x.dtype], kind, eps, residual_scale, branch_scale, 0,
+                      x.data_ptr(), _address(y), _address(gamma_post), _address(gate),
+                      _address(gamma), *used)
+    _enqueue(dev, stream, lib().mhc_block_norm, ctypes.byref(a))
+    return o
+
+
+def int8_quantize(src, *, out=None, stream=None):
+    """int8 codes [rows, H] and f32 scales [rows] of a bf16 or f16 [rows, H]
+    device tensor, one scale a row: the operands of int8_gemm.  out: the pair
+    to write to."""
+    import torch
+    if src.dim() != 2:
+        raise ValueError("src must be [rows, H]")
+    if src.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"src must be bfloat16 or float16, got {src.dtype}")
+    rows, H = src.shape
+    dev = src.device
+    _need("src", src, src.dtype, (rows, H), dev)
+    if out is None:
+        codes = torch.empty((rows, H), dtype=torch.int8, device=dev)
+        scales = torch.empty((rows,), dtype=torch.float32, device=dev)
+    else:
+        codes, scales = out
+        _need("codes", codes, torch.int8, (rows, H), dev)
+        _need("scales", scales, torch.float32, (rows,), dev)
+    _enqueue(dev, stream, lib().mhc_int8_quantize, src.data_ptr(), _codes_of(DTYPES)[src.dtype],
+             rows, H, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None, stream=None):
+    """Product of int8 codes with a scale for each token and channel:
+    out[t, n] = sum_k a[t, k] b[n, k] * a_scales[t] * b_scales[n] (+ bias[n]).
+    a int8 [T, K], a_scales f32 [T] (block_norm's or int8_quantize's), b int8
+    [N, K], b_scales and bias f32 [N]; out_dtype bf16, f16 or f32."""
+    import torch
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a must be [T, K] and b [N, K]")
+    T, K = a.shape
+    N = b.shape[0]
+    dev = a.device
+    if out_dtype not in DTYPES:
+        raise ValueError(f"out_dtype must be one of {', '.join(DTYPES)}")
+    dt = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[out_dtype]
+    _need("a", a, torch.int8, (T, K), dev)
+    _need("a_scales", a_scales, torch.float32, (T,), dev)
+    _need("b", b, torch.int8, (N, K), dev)
+    _need("b_scales", b_scales, torch.float32, (N,), dev)
+    if bias is not None:
+        _need("bias", bias, torch.float32, (N,), dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=dt, device=dev)
+    else:
+        _need("out", out, dt, (T, N), dev)
+    _enqueue(dev, stream, lib().mhc_int8_gemm, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
+             b_scales.data_ptr(), _address(bias), T, N, K, DTYPES[out_dtype], out.data_ptr())
+    return out
+
+
+def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, group_top=1,
+          renormalize=True, scale=1.0, out=None, stream=None):
+    """Routing of tokens to experts: of logits [T, E] (f32, bf16 or f16) the k
+    experts of the highest score + bias in the topk_groups best groups, and
+    their scores (softmax or sigmoid), renormalized and times scale.  bias f32
+    [E].  A group's score is the sum of its group_top (1 or 2) highest keys.
+    Returns (weights f32 [T, k], ids int32 [T, k]), highest first; id -1 and
+    weight 0 where masks (-inf) leave fewer than k experts.  out: the pair to
+    write to."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if logits.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    if scoring not in SCORINGS:
+        raise ValueError(f"scoring must be one of {', '.join(SCORINGS)}")
+    T, E = logits.shape
+    dev = logits.device
+    _need("logits", logits, logits.dtype, (T, E), dev)
+    if bias is not None:
+        _need("bias", bias, torch.float32, (E,), dev)
+    if out is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    else:
+        weights, ids = out
+        _need("weights", weights, torch.float32, (T, k), dev)
+        _need("ids", ids, torch.int32, (T, k), dev)
+    a = RouteArgs(T, E, k, _codes_of(DTYPES)[logits.dtype], SCORINGS[scoring], groups, topk_groups,
+                  group_top, int(bool(renormalize)), scale, 0, logits.data_ptr(), _address(bias),
+                  weights.data_ptr(), ids.data_ptr())
+    _enqueue(dev, stream, lib().mhc_route, ctypes.byref(a))
+    return weights, ids

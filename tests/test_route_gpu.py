@@ -1,0 +1,198 @@
+"""Expert routing on the GPU against the plain definition in binary64.
+
+Ids are equal: both sides choose by binary64 keys, and inputs whose keys
+differ by less than a few of its last places are exact ties (equal logits).
+Weights are binary64 until their one rounding: 2^-24 relative, and 2^-40 for
+the difference of two binary64 evaluations."""
+import math
+
+import pytest
+import torch
+
+import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def check(logits, k, scoring="softmax", bias=None, groups=1, keep=1, top=1, renorm=True, scale=1.0):
+    from layer_mhc_seam_amd.seam import route
+    w, ids = route(logits.cuda(), k, scoring=scoring, bias=None if bias is None else bias.cuda(), groups=groups,
+                   topk_groups=keep, group_top=top, renormalize=renorm, scale=scale)
+    w, ids = w.cpu().double(), ids.cpu()
+    want_w, want = ref.route(logits, k, scoring, bias, groups, keep, top, renorm, scale)
+    bad = (ids != want).any(1).nonzero()
+    assert not len(bad), f"{len(bad)} rows differ, first {bad[0].item()}: {ids[bad[0]]} for {want[bad[0]]}"
+    nan = want_w.isnan()
+    assert torch.equal(w.isnan(), nan)
+    err = (w - want_w).abs()[~nan]
+    assert (err <= (2.0 ** -24 + 2.0 ** -40) * want_w.abs()[~nan] + 2.0 ** -149).all()
+    return w, ids
+
+
+# experts: one, below, at and past a wave's and every change of the
+# kernel's; groups of one, odd and even sizes, as many as there may be
+@pytest.mark.parametrize("E,k,groups,keep,top", [
+    (1, 1, 1, 1, 1), (2, 2, 1, 1, 1), (8, 2, 1, 1, 1), (8, 2, 4, 2, 1), (63, 5, 1, 1, 1), (64, 6, 8, 3, 1),
+    (64, 64, 1, 1, 1), (64, 64, 64, 64, 1), (65, 8, 5, 2, 2), (100, 7, 4, 1, 2), (127, 3, 1, 1, 1),
+    (128, 8, 8, 4, 2), (129, 8, 3, 2, 2), (160, 6, 8, 3, 1), (160, 6, 1, 1, 1), (256, 8, 8, 4, 2),
+    (256, 8, 1, 1, 1), (257, 9, 1, 1, 1), (384, 8, 1, 1, 1), (384, 8, 8, 4, 2), (512, 10, 16, 5, 2),
+    (513, 4, 27, 9, 2), (700, 33, 7, 3, 2), (1000, 1, 1, 1, 1), (1024, 64, 64, 13, 2), (1024, 8, 1, 1, 1)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_matches_definition(E, k, groups, keep, top, scoring):
+    g = torch.Generator().manual_seed(E + k)
+    for i, dt in enumerate(DTYPES):
+        T = (1, 5, 67)[i]
+        logits = (1.5 * torch.randn(T, E, generator=g)).to(dt)
+        bias = 0.1 * torch.randn(E, generator=g)
+        check(logits, k, scoring, None, groups, keep, top)
+        check(logits, k, scoring, bias, groups, keep, top, renorm=i != 1, scale=2.5)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep,top", [(1, 1, 1), (8, 3, 1), (8, 3, 2)])
+def test_route_ties_go_to_the_lowest_index(scoring, groups, keep, top):
+    """All equal; few distinct values; equal rows but one."""
+    g = torch.Generator().manual_seed(1)
+    l = torch.randint(-2, 3, (40, 128), generator=g).float()
+    l[0] = 0.25
+    l[1] = 0.25
+    l[1, 77] = 0.5
+    w, ids = check(l, 6, scoring, None, groups, keep, top)
+    assert ids[0].tolist() == [0, 1, 2, 3, 4, 5]
+    check(l, 6, scoring, torch.zeros(128), groups, keep, top)
+    check(l, 6, scoring, torch.randint(-1, 2, (128,), generator=g).float() * 0.25, groups, keep, top)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_near_ties(scoring, bias):
+    """Logits one or two units of the last place apart, in a shuffled order:
+    scores that binary32 cannot tell from each other."""
+    g = torch.Generator().manual_seed(2)
+    base = torch.tensor([0.7, 1.3, -2.1, 5.5]).repeat_interleave(10)[:, None]
+    bits = base.expand(40, 96).contiguous().view(torch.int32) + torch.stack(
+        [torch.randperm(96, generator=g) for _ in range(40)]).int()
+    check(bits.view(torch.float32), 8, scoring, 0.01 * torch.ones(96) if bias else None)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep,top", [(1, 1, 1), (8, 2, 1), (8, 2, 2)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_masks(scoring, groups, keep, top, bias):
+    """Experts out by -inf logits and by -inf bias: fewer than k left, one,
+    none; whole groups out; groups with a single expert left."""
+    g = torch.Generator().manual_seed(3)
+    E = 64
+    l = torch.randn(60, E, generator=g)
+    share = torch.linspace(0, 1, 60)[:, None]
+    l = l.masked_fill(torch.rand(60, E, generator=g) < share, -math.inf)
+    l[0] = -math.inf
+    l[1] = -math.inf
+    l[1, 63] = -3.0
+    l[2, :56] = -math.inf
+    b = 0.1 * torch.randn(E, generator=g) if bias else None
+    if bias:
+        b[5] = -math.inf
+        b[40:48] = -math.inf
+    w, ids = check(l, 5, scoring, b, groups, keep, top)
+    assert (ids[0] == -1).all() and (w[0] == 0).all()
+    assert ids[1].tolist() == [63, -1, -1, -1, -1]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_lowest_values_infinities_and_nan(scoring):
+    """The types' lowest and largest values, infinities and NaN: ids distinct
+    and in range always."""
+    for dt in DTYPES:
+        f = torch.finfo(dt)
+        l = torch.randn(12, 40).to(dt)
+        l[0] = f.min
+        l[1, 3:] = f.min
+        l[2, 7] = f.max
+        l[3] = f.max
+        l[4, 9] = math.inf
+        l[5, 9] = math.nan
+        l[6] = math.nan
+        l[7] = math.inf
+        l[8, 0], l[8, 1], l[8, 2] = math.nan, math.inf, -math.inf
+        l[9] = 60000.0
+        l[10] = -60000.0
+        w, ids = check(l, 6, scoring)
+        assert w[5].isnan().all() and (ids[6] == -1).all()
+        check(l, 6, scoring, torch.randn(40), 4, 2, 2)
+    b = torch.zeros(40)
+    b[3] = math.inf
+    _, ids = check(torch.randn(3, 40), 4, scoring, b)
+    assert (ids[:, 0] == 3).all()
+
+
+def test_route_vanishing_scores():
+    """Sigmoid scores that vanish in binary64: their sum is 0, weights are 0
+    and ids stay those of the lowest indices."""
+    w, ids = check(torch.full((2, 16), -800.0), 3, "sigmoid")
+    assert ids[0].tolist() == [0, 1, 2] and (w == 0).all()
+
+
+def test_route_unaligned_rows_and_given_outputs():
+    from layer_mhc_seam_amd.seam import route
+    for dt in DTYPES:
+        buf = torch.randn(7 * 37 + 3).to(dt).cuda()
+        l = buf[3:].view(7, 37)
+        w, ids = (torch.full((7 * 5 + 16,), 9, dtype=t, device="cuda") for t in (torch.float32, torch.int32))
+        route(l, 5, out=(w[:35].view(7, 5), ids[:35].view(7, 5)))
+        want = ref.route(l.cpu(), 5, "softmax", None, 1, 1, 1, True, 1.0)
+        assert torch.equal(ids[:35].view(7, 5).cpu(), want[1])
+        assert (w[35:] == 9).all() and (ids[35:] == 9).all()
+
+
+def test_route_many_tokens():
+    g = torch.Generator().manual_seed(4)
+    l = torch.randn(4160, 256, generator=g)
+    check(l, 8, "sigmoid", 0.05 * torch.randn(256, generator=g), 8, 4, 2, scale=2.5)
+
+
+def test_route_stream_graph_and_empty():
+    from layer_mhc_seam_amd.seam import route
+    l = torch.randn(65, 256, device="cuda")
+    b = 0.1 * torch.randn(256, device="cuda")
+    kw = dict(scoring="sigmoid", bias=b, groups=8, topk_groups=4, group_top=2)
+    want = route(l, 8, **kw)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    out = tuple(torch.empty_like(t) for t in want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        route(l, 8, **kw, out=out, stream=s)
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        route(l, 8, **kw)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    w, ids = route(torch.empty(0, 8, device="cuda"), 2)
+    assert w.shape == (0, 2) and ids.shape == (0, 2)
+
+
+def test_route_refusals():
+    from layer_mhc_seam_amd.seam import SeamError, route
+    l = torch.randn(4, 16, device="cuda")
+    for call in (lambda: route(l.t(), 2), lambda: route(l.double(), 2), lambda: route(l[0], 2),
+                 lambda: route(l, 2, bias=torch.zeros(8, device="cuda")),
+                 lambda: route(l, 2, bias=torch.zeros(16)), lambda: route(l, 2, scoring="tanh"),
+                 lambda: route(l, 2, out=(torch.empty(4, 2, device="cuda"),) * 2)):
+        with pytest.raises(ValueError):
+            call()
+    for kw in (dict(k=17), dict(k=0), dict(k=2, groups=3), dict(k=2, groups=4, topk_groups=5),
+               dict(k=2, groups=16, group_top=2), dict(k=9, groups=4, topk_groups=2)):
+        with pytest.raises(SeamError):
+            route(l, **kw)
