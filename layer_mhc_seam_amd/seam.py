@@ -8,6 +8,7 @@ anything another way.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -355,40 +356,47 @@ def mxfp8_gemm(a, a_scales, b, b_scales, *, out=None, stream=None):
 # Unlike the calls above, these run on the device their tensors are on,
 # whichever is current, and on that device's current stream.
 
-def _codes_of(dtypes):
+@functools.lru_cache(maxsize=None)
+def _types():
+    """torch's types by the names of DTYPES, and their codes by type."""
     import torch
-    names = {torch.bfloat16: "bf16", torch.float16: "f16", torch.float32: "f32"}
-    return {t: DTYPES[n] for t, n in names.items() if n in dtypes}
+    types = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+    return types, {t: DTYPES[n] for n, t in types.items()}
 
 
 def _need(name, t, dtype, shape, device):
     """t is a dense tensor of that type and shape on that device."""
-    if t.device != device or t.device.type != "cuda":
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda \
+            and t.is_contiguous():
+        return
+    if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a tensor on {device}" if device.type == "cuda"
                          else f"{name} must be a device tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _enqueue(device, stream, call, *args):
     """call(*args, stream) on `device`: its current stream unless one of its
-    streams is given."""
+    streams is given.  (The handle is asked for as it is: a Stream object
+    around it takes 2 us, as long as a small kernel's whole launch.)"""
     import torch
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     else:
         handle = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        _check(call(*args, handle))
+        status = call(*args, handle)
     else:
         with torch.cuda.device(device):
-            _check(call(*args, handle))
+            status = call(*args, handle)
+    if status != OK:
+        _check(status)
 
 
 def _address(t):
@@ -412,51 +420,56 @@ def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_sc
     import torch
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
-    T, H = x.shape
+    T, H = shape = x.shape
     dev = x.device
-    like = gamma if gamma is not None else y
-    if like is None:
+    codes = _types()[1]
+    dt = gamma.dtype if gamma is not None else None if y is None else y.dtype
+    if dt is None:
         raise ValueError("block_norm needs y, gamma or both")
-    dt = like.dtype
-    if dt not in (torch.bfloat16, torch.float16):
+    if dt is not torch.bfloat16 and dt is not torch.float16:
         raise ValueError(f"gamma and y must be bfloat16 or float16, got {dt}")
-    _need("x", x, torch.float32 if x.dtype == torch.float32 else dt, (T, H), dev)
-    for name, t, shape in (("gamma", gamma, (H,)), ("y", y, (T, H)), ("gamma_post", gamma_post, (H,))):
-        if t is not None:
-            _need(name, t, dt, shape, dev)
+    x_dt = torch.float32 if x.dtype is torch.float32 else dt
+    _need("x", x, x_dt, shape, dev)
+    if gamma is not None:
+        _need("gamma", gamma, dt, (H,), dev)
+    elif int8:
+        raise ValueError("int8 codes are those of the norm: give gamma")
+    if y is not None:
+        _need("y", y, dt, shape, dev)
+    if gamma_post is not None:
+        _need("gamma_post", gamma_post, dt, (H,), dev)
     kind = GATE_NONE
     if gate is not None:
-        if gate.dtype == torch.float32:
-            kind = GATE_CHANNEL if gate.dim() == 1 else GATE_TOKEN
-            _need("gate", gate, torch.float32, (H,) if kind == GATE_CHANNEL else (T, 1), dev)
-        else:
+        if gate.dtype is not torch.float32:
             kind = GATE_ELEMENT
-            _need("gate", gate, dt, (T, H), dev)
-    if gamma is None and int8:
-        raise ValueError("int8 codes are those of the norm: give gamma")
-    o = dict(out) if out else {}
-    used = []
-    for name, wanted, dtype, shape in (
-            ("residual_out", y is not None, x.dtype, (T, H)),
-            ("norm", gamma is not None and norm, dt, (T, H)),
-            ("codes", int8, torch.int8, (T, H)), ("scales", int8, torch.float32, (T,))):
-        if not wanted:
-            if name in o:
-                raise ValueError(f"this call writes no {name}")
-            used.append(None)
-            continue
-        if name in o:
-            _need(name, o[name], dtype, shape, dev)
+            _need("gate", gate, dt, shape, dev)
+        elif gate.dim() == 1:
+            kind = GATE_CHANNEL
+            _need("gate", gate, torch.float32, (H,), dev)
         else:
-            o[name] = torch.empty(shape, dtype=dtype, device=dev)
-        used.append(o[name].data_ptr())
+            kind = GATE_TOKEN
+            _need("gate", gate, torch.float32, (T, 1), dev)
+    want = {}
+    if y is not None:
+        want["residual_out"] = (x_dt, shape)
+    if gamma is not None and norm:
+        want["norm"] = (dt, shape)
+    if int8:
+        want["codes"] = (torch.int8, shape)
+        want["scales"] = (torch.float32, (T,))
+    o = dict(out) if out else {}
     for name in o:
-        if name not in ("residual_out", "norm", "codes", "scales"):
-            raise ValueError(f"block_norm has no output {name}")
-    codes = _codes_of(DTYPES)
-    a = BlockNormArgs(T, H, codes[dt], codes[x.dtype], kind, eps, residual_scale, branch_scale, 0,
+        if name not in want:
+            raise ValueError(f"this call writes no {name}")
+    for name, (dtype, size) in want.items():
+        if name in o:
+            _need(name, o[name], dtype, size, dev)
+        else:
+            o[name] = torch.empty(size, dtype=dtype, device=dev)
+    a = BlockNormArgs(T, H, codes[dt], codes[x_dt], kind, eps, residual_scale, branch_scale, 0,
                       x.data_ptr(), _address(y), _address(gamma_post), _address(gate),
-                      _address(gamma), *used)
+                      _address(gamma), _address(o.get("residual_out")), _address(o.get("norm")),
+                      _address(o.get("codes")), _address(o.get("scales")))
     _enqueue(dev, stream, lib().mhc_block_norm, ctypes.byref(a))
     return o
 
@@ -468,7 +481,7 @@ def int8_quantize(src, *, out=None, stream=None):
     import torch
     if src.dim() != 2:
         raise ValueError("src must be [rows, H]")
-    if src.dtype not in (torch.bfloat16, torch.float16):
+    if src.dtype is not torch.bfloat16 and src.dtype is not torch.float16:
         raise ValueError(f"src must be bfloat16 or float16, got {src.dtype}")
     rows, H = src.shape
     dev = src.device
@@ -480,7 +493,7 @@ def int8_quantize(src, *, out=None, stream=None):
         codes, scales = out
         _need("codes", codes, torch.int8, (rows, H), dev)
         _need("scales", scales, torch.float32, (rows,), dev)
-    _enqueue(dev, stream, lib().mhc_int8_quantize, src.data_ptr(), _codes_of(DTYPES)[src.dtype],
+    _enqueue(dev, stream, lib().mhc_int8_quantize, src.data_ptr(), _types()[1][src.dtype],
              rows, H, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
@@ -498,7 +511,7 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None
     dev = a.device
     if out_dtype not in DTYPES:
         raise ValueError(f"out_dtype must be one of {', '.join(DTYPES)}")
-    dt = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[out_dtype]
+    dt = _types()[0][out_dtype]
     _need("a", a, torch.int8, (T, K), dev)
     _need("a_scales", a_scales, torch.float32, (T,), dev)
     _need("b", b, torch.int8, (N, K), dev)
@@ -526,7 +539,7 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
     import torch
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
-    if logits.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+    if logits.dtype not in _types()[1]:
         raise ValueError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
     if scoring not in SCORINGS:
         raise ValueError(f"scoring must be one of {', '.join(SCORINGS)}")
@@ -542,7 +555,7 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
         weights, ids = out
         _need("weights", weights, torch.float32, (T, k), dev)
         _need("ids", ids, torch.int32, (T, k), dev)
-    a = RouteArgs(T, E, k, _codes_of(DTYPES)[logits.dtype], SCORINGS[scoring], groups, topk_groups,
+    a = RouteArgs(T, E, k, _types()[1][logits.dtype], SCORINGS[scoring], groups, topk_groups,
                   group_top, int(bool(renormalize)), scale, 0, logits.data_ptr(), _address(bias),
                   weights.data_ptr(), ids.data_ptr())
     _enqueue(dev, stream, lib().mhc_route, ctypes.byref(a))
