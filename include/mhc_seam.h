@@ -448,15 +448,17 @@ typedef enum mhc_scoring {
  * Routing of tokens to experts, the gates of an experts' sub-layer.  Per
  * token, from its logits l:
  *   s   = softmax(l) or 1 / (1 + exp(-l))
- *   key = s + bias
+ *   key = s + bias, or l itself without a bias (the scores' order, also
+ *         where binary64 holds no difference between the scores)
  *   groups > 1: of the groups of E / groups consecutive experts those
- *   topk_groups stay open whose best `group_top` (1 or 2) keys sum highest
+ *   topk_groups stay open whose best key is highest (group_top 1), or whose
+ *   two best s + bias sum highest (group_top 2)
  *   ids     = the k experts of the highest keys in open groups, highest first
  *   weights = s[ids], divided by their sum if renormalize, times scale
  * Equal keys and equal sums go to the lowest index.  Scores and keys are
  * binary64, weights are rounded once to f32.
- * A logit or a bias of -inf takes its expert out (a group's missing keys
- * count as -1e30); where fewer than k experts are left, the other slots hold
+ * A logit or a bias of -inf takes its expert out (what a group then lacks
+ * counts as -1e30 in its sum of two); where fewer than k experts are left, the other slots hold
  * id -1 and weight 0, all of them in a row with none.  A NaN logit, or +inf
  * under softmax, is taken out too and makes the row's weights NaN; a bias
  * must not be NaN.  Ids are distinct and in range whatever the logits are.

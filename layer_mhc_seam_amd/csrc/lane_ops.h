@@ -44,6 +44,55 @@ __device__ __forceinline__ double read_lane(double v, int l)
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// Reductions over a row of 16 lanes (all active), the same value in each.
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    v = max(v, row_ror<8>(v));
+    v = max(v, row_ror<4>(v));
+    v = max(v, row_ror<2>(v));
+    return max(v, row_ror<1>(v));
+}
+
+template <int N>
+__device__ __forceinline__ float row_ror(float v)
+{
+    return __uint_as_float(row_ror<N>(__float_as_uint(v)));
+}
+
+__device__ __forceinline__ float row_max(float v)
+{
+    v = fmaxf(v, row_ror<8>(v));
+    v = fmaxf(v, row_ror<4>(v));
+    v = fmaxf(v, row_ror<2>(v));
+    return fmaxf(v, row_ror<1>(v));
+}
+
+__device__ __forceinline__ float row_sum(float v)
+{
+    v += row_ror<8>(v);
+    v += row_ror<4>(v);
+    v += row_ror<2>(v);
+    return v + row_ror<1>(v);
+}
+
+__device__ __forceinline__ double row_sum(double v)
+{
+    v += row_ror<8>(v);
+    v += row_ror<4>(v);
+    v += row_ror<2>(v);
+    return v + row_ror<1>(v);
+}
+
+// Value of lane l ^ 1, l ^ 2; of lane l ^ 7 and l ^ 15, which stand for
+// l ^ 4 and l ^ 8 once the lanes of each four, or eight, hold one value.
+enum { kXor1 = 0xb1, kXor2 = 0x4e, kXor4 = 0x141, kXor8 = 0x140 };
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_swap(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+
 // Reductions over the wave's 64 lanes (all active), the same value in every
 // lane: four rotations inside the rows of 16, then the four rows.
 __device__ __forceinline__ double wave_sum(double v)

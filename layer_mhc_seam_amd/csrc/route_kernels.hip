@@ -3,9 +3,10 @@
 // For each token, with logits l [E], an optional bias b [E] that balances
 // the experts' load, and G groups of E / G consecutive experts:
 //   s   = softmax(l)  or  1 / (1 + exp(-l))
-//   key = s + b                        (s without a bias)
-//   the `keep` groups whose sums of their best `top` (1 or 2) keys are the
-//   largest stay open; of their experts the k of the largest keys are chosen,
+//   key = s + b, or l without a bias (the scores' order, told apart also
+//   where scores are equal in binary64)
+//   the `keep` groups whose best key (top 1), or whose two best s + b together
+//   (top 2), are the largest stay open; of their experts the k of the largest keys are chosen,
 //   largest first
 //   w   = s of the chosen, divided by their sum (renorm), times scale
 // Equal keys, and equal sums of groups, go to the lowest index.  The bias
@@ -17,8 +18,9 @@
 // would then hang on the rounding of exp and on the order of the softmax's
 // sum.  In binary64 it is the definition's for all but bit-equal scores.
 //
-// Masks: a logit of -inf, or a bias of -inf, takes an expert out.  A group's
-// missing keys count as -1e30, so groups with more experts left come first.
+// Masks: a logit of -inf, or a bias of -inf, takes an expert out.  A key
+// missing from a sum of two counts as -1e30: groups with more experts left
+// come first.
 // Where fewer than k experts are left the other slots hold id -1, weight 0; a
 // row with none left has nothing else.  A NaN logit (and +inf under softmax)
 // is taken out likewise and turns the row's weights to NaN, so ids always lie
@@ -42,13 +44,22 @@ __device__ __forceinline__ float logit(const void *p, int64_t i)
     return (float)static_cast<const T *>(p)[i];
 }
 
-// One wave a token; lane l holds experts EPL l .. EPL l + EPL - 1.
-template <class T, int EPL>
-__global__ __launch_bounds__(64) void route_kernel(RouteParams P)
+// LDS writes of the wave's lanes before its reads that follow
+__device__ __forceinline__ void wave_fence()
 {
-    __shared__ double keys[EPL * 64];
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x, E = P.E;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// ---------------------------------------------------------- in binary64 --
+//
+// One wave a token; lane l holds experts EPL l .. EPL l + EPL - 1.  Groups of
+// any size go through LDS (`keys`, the wave's own).
+template <class T, int EPL>
+__device__ __forceinline__ void route_token(const RouteParams &P, int64_t t, int lane,
+                                            double *keys)
+{
+    const int E = P.E;
     const double inf = __builtin_inf();
     double l[EPL], s[EPL], key[EPL];
     bool bad = false;
@@ -83,7 +94,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams P)
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = EPL * lane + j;
-        key[j] = s[j] + (P.bias && e < E ? (double)P.bias[e] : 0.0);
+        key[j] = !P.bias ? l[j] : e < E ? s[j] + (double)P.bias[e] : -inf;
         if (l[j] == -inf || key[j] != key[j])
             key[j] = -inf;
     }
@@ -91,8 +102,8 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams P)
         const int size = E / P.groups;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            keys[EPL * lane + j] = key[j];
-        __syncthreads();
+            keys[EPL * lane + j] = P.bias || P.top == 1 || l[j] == -inf ? key[j] : s[j];
+        wave_fence();
         double first = -inf, second = -inf;
         if (lane < P.groups)
             for (int i = 0; i < size; ++i) {
@@ -100,12 +111,12 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams P)
                 second = fmax(second, fmin(first, v));
                 first = fmax(first, v);
             }
-        double sum = first == -inf ? kMissing : first;
-        if (P.top == 2)
-            sum += second == -inf ? kMissing : second;
-        __syncthreads();
+        const double sum = P.top == 1 ? first
+                                      : (first == -inf ? kMissing : first) +
+                                            (second == -inf ? kMissing : second);
+        wave_fence();
         keys[lane] = sum;
-        __syncthreads();
+        wave_fence();
         int rank = 0;
         for (int g = 0; g < P.groups; ++g)
             rank += keys[g] > sum || (keys[g] == sum && g < lane);
@@ -157,10 +168,281 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams P)
     }
 }
 
+template <class T, int EPL>
+__global__ __launch_bounds__(64) void route_kernel(RouteParams P)
+{
+    __shared__ double keys[EPL * 64];
+    route_token<T, EPL>(P, blockIdx.x, threadIdx.x, keys);
+}
+
+// ----------------------------------------------------- four tokens a wave --
+//
+// The choice from binary32 keys wherever they prove it right.  A row of 16
+// lanes takes a token, up to EPL experts a lane; with G groups 16 / G lanes
+// hold each group.  A key is a whole number: the score's place between the
+// row's lowest and highest in B bits above the expert's index (inverted, so
+// that the lowest of equal keys is the largest number).  Then one maximum
+// gives value and index at once, and the next largest is the maximum of
+// key - best modulo 2^32, where only smaller keys wrap around: a subtraction
+// and half a three-way maximum a key, and nothing to take out or look up.
+//
+// Scores are binary32 with an error of at most `delta` (below), so two keys
+// further apart than `need` units are in the order of the binary64 ones.  A
+// row in which two neighbours among the k + 1 largest, or the groups on both
+// sides of the border, are nearer than that goes through route_token
+// afterwards, and so does one that has too few experts left, infinities or
+// NaN.  At 256 experts that is about one row in 200.  Without a bias the
+// order is the logits' own: bf16 and fp16 logits fit a key whole, and no row
+// is too close to call (equal logits are common there and are ties).
+//
+// Weights are binary64 of the k chosen.
+constexpr int kIndexBits = 9;
+constexpr u32 kIndexMask = (1u << kIndexBits) - 1;
+constexpr int kValueBits = 30 - kIndexBits;   // keys stay below 2^31
+
+template <class T>
+struct Exact {   // bits of a binary32 value that T's do not use
+    static constexpr int kShift = 0;
+};
+template <>
+struct Exact<__bf16> {
+    static constexpr int kShift = 16;
+};
+template <>
+struct Exact<_Float16> {
+    static constexpr int kShift = 13;
+};
+
+// binary32 bits in the order of the values, -0 with +0
+__device__ __forceinline__ u32 in_order(float v)
+{
+    const u32 b = __float_as_uint(v + 0.0f);
+    return b ^ ((u32)((int)b >> 31) | 0x80000000u);
+}
+
+template <class T, int EPL>
+__device__ __forceinline__ void load_logits(const T *p, int count, float (&v)[EPL])
+{
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    typedef T4 T4_any __attribute__((aligned(sizeof(T))));
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4) {
+        if (j + 4 <= count) {
+            const T4 q = *reinterpret_cast<const T4_any *>(p + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[j + i] = (float)q[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[j + i] = j + i < count ? (float)p[j + i] : -__builtin_inff();
+        }
+    }
+}
+
+template <class T, int EPL>
+__global__ __launch_bounds__(64) void route_rows_kernel(RouteParams P, int64_t tokens)
+{
+    static_assert(EPL % 4 == 0 && 16 * EPL <= (int)kIndexMask + 1, "indexes fit a key");
+    __shared__ double keys[EPL / 4 * 64];
+    const int lane = threadIdx.x, c = lane & 15;
+    const int64_t own = (int64_t)blockIdx.x * 4 + (lane >> 4);
+    const int64_t t = own < tokens ? own : tokens - 1;
+    const T *row = static_cast<const T *>(P.logits) + t * P.E;
+    const int lanes = 16 / P.groups, size = P.E / P.groups;   // of a group
+    const int per = (size + lanes - 1) / lanes, sub = (c % lanes) * per;
+    const int start = c / lanes * size + sub, count = max(0, min(per, size - sub));
+    const float ninf = -__builtin_inff();
+    float v[EPL];
+    load_logits<T, EPL>(row + start, count, v);
+    bool odd = false;   // the row is for route_token
+    float top = ninf;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        odd |= !(v[j] < __builtin_inff());
+        top = fmaxf(top, v[j]);
+    }
+    top = row_max(top);
+    odd |= top == ninf;
+    const bool by_group = P.groups > P.keep;
+    u32 key[EPL];
+    u32 need = 0;
+    if (Exact<T>::kShift > 0 && !P.bias && (!by_group || P.top == 1)) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const u32 index = kIndexMask - (u32)(start + j);
+            key[j] = v[j] == ninf ? 0u
+                                  : (in_order(v[j]) >> Exact<T>::kShift) << kIndexBits | index;
+        }
+    } else {
+        // scores with their error, then their places between lowest and highest
+        float delta = 0.0f;
+        if (P.bias || (by_group && P.top == 2)) {
+            const float log2e = 1.44269504f;
+            float most = 1.0f;
+            if (P.sigmoid) {
+#pragma unroll
+                for (int j = 0; j < EPL; ++j)
+                    v[j] = v[j] == ninf
+                               ? ninf
+                               : __builtin_amdgcn_rcpf(
+                                     1.0f + __builtin_amdgcn_exp2f(fminf(-v[j] * log2e, 126.0f)));
+            } else {
+                float total = 0.0f;
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) {
+                    const float e = __builtin_amdgcn_exp2f((v[j] - top) * log2e);
+                    v[j] = v[j] == ninf ? ninf : e;
+                    total += e;
+                }
+                most = __builtin_amdgcn_rcpf(row_sum(total));
+#pragma unroll
+                for (int j = 0; j < EPL; ++j)
+                    v[j] *= most;
+            }
+            float size_of = 0.0f;
+            if (P.bias)
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) {
+                    const float b = j < count ? P.bias[start + j] : 0.0f;
+                    v[j] += b;
+                    size_of = fmaxf(size_of, b == ninf ? 0.0f : fabsf(b));
+                }
+            // In units of 2^-24: a sigmoid's exponent, exp2, sum and
+            // reciprocal, weighted with s (1 - s) or s, come to less than 8;
+            // a softmax's exponent, exp2, sum of 36 terms, reciprocal and
+            // product to less than 48 of its largest score.  Then the rounding
+            // of score + bias.
+            delta = (P.sigmoid ? 0x1p-21f : 0x1p-18f * most) +
+                    0x1p-23f * (most + row_max(size_of));
+        }
+        float hi = ninf, lo = __builtin_inff();
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            hi = fmaxf(hi, v[j]);
+            lo = fminf(lo, v[j] == ninf ? __builtin_inff() : v[j]);
+        }
+        hi = row_max(hi);
+        lo = -row_max(-lo);
+        const float scale = (float)(1 << kValueBits) / (hi - lo);
+        odd |= !(hi - lo > 0.0f) || !(scale < 0x1p100f) || !(delta * scale < 0x1p16f);
+        need = 2 + (u32)(2.0f * fminf(delta * scale, 0x1p16f) + 1.0f);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const u32 place = 1u + (u32)fminf((v[j] - lo) * scale, (float)(1 << kValueBits));
+            key[j] = v[j] == ninf ? 0u : place << kIndexBits | (kIndexMask - (u32)(start + j));
+        }
+    }
+    if (by_group) {
+        u32 first = 0, second = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            second = max(second, min(first, key[j]));
+            first = max(first, key[j]);
+        }
+        auto join = [&](u32 f, u32 s) {
+            second = max(max(second, s), min(first, f));
+            first = max(first, f);
+        };
+        if (lanes >= 2)
+            join(row_swap<kXor1>(first), row_swap<kXor1>(second));
+        if (lanes >= 4)
+            join(row_swap<kXor2>(first), row_swap<kXor2>(second));
+        if (lanes >= 8)
+            join(row_swap<kXor4>(first), row_swap<kXor4>(second));
+        u32 mine = first;
+        if (P.top == 2) {
+            odd |= second == 0;
+            mine = (first >> kIndexBits) + (second >> kIndexBits);
+        }
+        // lanes of groups that come before this lane's
+        int before = 0;
+#define COUNT(N) before += row_ror<N>(mine) > mine;
+        COUNT(1) COUNT(2) COUNT(3) COUNT(4) COUNT(5) COUNT(6) COUNT(7) COUNT(8)
+        COUNT(9) COUNT(10) COUNT(11) COUNT(12) COUNT(13) COUNT(14) COUNT(15)
+#undef COUNT
+        const bool open = before < P.keep * lanes;
+        const int shift = P.top == 2 ? 0 : kIndexBits;
+        const u32 last = ~row_max(open ? ~(mine >> shift) : 0u);
+        const u32 next = row_max(open ? 0u : mine >> shift);
+        odd |= next > 0 && last - next < need * (u32)P.top;
+        // equal sums: more groups open than there should be
+        odd |= need > 0 &&
+               __builtin_popcountll(__ballot(open) >> (lane & 48) & 0xffff) != P.keep * lanes;
+        if (!open)
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                key[j] = 0;
+    }
+    u32 best = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        best = max(best, key[j]);
+    best = row_max(best);
+    u32 chosen = best;   // lane i of the row keeps the i-th
+    for (int i = 1; i <= P.k; ++i) {
+        odd |= best == 0;
+        u32 step = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            step = max(step, key[j] - best);
+        step = row_max(step);
+        const u32 next = (int)step < 0 ? best + step : 0u;
+        odd |= next > 0 && (best >> kIndexBits) - (next >> kIndexBits) < need;
+        best = next;
+        chosen = c == i ? best : chosen;
+    }
+    const bool has = c < P.k;
+    const int id = (int)(kIndexMask - (chosen & kIndexMask));
+    double w = 0.0;
+    if (has) {
+        const double l = (double)(float)row[min(id, P.E - 1)];
+        w = P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top);
+    }
+    const double sum = row_sum(w);
+    if (P.renorm)
+        w = sum > 0.0 ? w / sum : 0.0;
+    // a row's lanes agree on `odd` once they have all been asked
+    const u64 lanes_odd = __ballot(odd);
+    const bool mine_odd = (lanes_odd >> (lane & 48) & 0xffff) != 0;
+    if (has && own < tokens && !mine_odd) {
+        P.weights[t * P.k + c] = (float)(w * (double)P.scale);
+        P.ids[t * P.k + c] = id;
+    }
+    for (int r = 0; r < 4; ++r) {
+        const int64_t tt = (int64_t)blockIdx.x * 4 + r;
+        if ((lanes_odd >> (16 * r) & 0xffff) && tt < tokens)
+            route_token<T, EPL / 4>(P, tt, lane, keys);
+    }
+}
+
+// Four tokens a wave where a lane's experts, the chosen and the groups fit a
+// row of 16 lanes, and weights need no sum over all experts' scores.
+bool rows_fit(const RouteParams &p)
+{
+    const bool groups = p.groups == 1 || p.groups == 2 || p.groups == 4 || p.groups == 8 ||
+                        p.groups == 16;
+    return groups && p.E <= 512 && p.k <= 16 && (p.sigmoid || p.renorm);
+}
+
 template <class T>
 hipError_t launch(const RouteParams &p, int64_t tokens, hipStream_t s)
 {
-    const dim3 grid((unsigned)tokens), block(64);
+    const dim3 block(64);
+    if (rows_fit(p)) {
+        const int lanes = 16 / p.groups, size = p.E / p.groups, per = (size + lanes - 1) / lanes;
+        const dim3 grid((unsigned)((tokens + 3) / 4));
+        if (per <= 4)
+            hipLaunchKernelGGL((route_rows_kernel<T, 4>), grid, block, 0, s, p, tokens);
+        else if (per <= 8)
+            hipLaunchKernelGGL((route_rows_kernel<T, 8>), grid, block, 0, s, p, tokens);
+        else if (per <= 16)
+            hipLaunchKernelGGL((route_rows_kernel<T, 16>), grid, block, 0, s, p, tokens);
+        else
+            hipLaunchKernelGGL((route_rows_kernel<T, 32>), grid, block, 0, s, p, tokens);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)tokens);
     if (p.E <= 64)
         hipLaunchKernelGGL((route_kernel<T, 1>), grid, block, 0, s, p);
     else if (p.E <= 128)

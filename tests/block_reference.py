@@ -75,14 +75,16 @@ def route(logits, k, scoring, bias, groups, keep, top, renorm, scale):
             else:
                 e = np.exp(l - l.max())
                 s = e / math.fsum(e)
-        key = s + (0.0 if bias is None else bias.to(F64).numpy())
+        score = s + (0.0 if bias is None else bias.to(F64).numpy())
+        key = l.copy() if bias is None else score.copy()
         key[out] = -np.inf
+        score[out] = -np.inf
         if groups > 1:
             size = E // groups
             sums = []
             for g in range(groups):
-                best = sorted(key[g * size:(g + 1) * size], reverse=True)[:top]
-                sums.append(sum(-1e30 if v == -np.inf else v for v in best))
+                best = sorted((key if top == 1 else score)[g * size:(g + 1) * size], reverse=True)[:top]
+                sums.append(best[0] if top == 1 else sum(-1e30 if v == -np.inf else v for v in best))
             order = sorted(range(groups), key=lambda g: (-sums[g], g))
             for g in order[keep:]:
                 key[g * size:(g + 1) * size] = -np.inf

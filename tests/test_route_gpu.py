@@ -196,3 +196,58 @@ def test_route_refusals():
                dict(k=2, groups=16, group_top=2), dict(k=9, groups=4, topk_groups=2)):
         with pytest.raises(SeamError):
             route(l, **kw)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_logits_that_scores_cannot_tell(scoring):
+    """Without a bias the order is the logits': where scores saturate or
+    vanish in binary64, and beside zero."""
+    l = torch.tensor([[40.0, 41, 42, 43, 44, 45, 46, 47], [-800, -801, -900, -790, -795, -1000, -799, -2000],
+                      [0.0, 1e-30, -1e-30, 1e-38, -0.0, 2e-30, 0.0, -5.0]])
+    _, ids = check(l, 4, scoring)
+    assert ids[0].tolist() == [7, 6, 5, 4] and ids[1].tolist() == [3, 4, 6, 0] and ids[2].tolist() == [5, 1, 3, 0]
+    check(l, 4, scoring, None, 2, 1, 1)
+    check(l, 4, scoring, None, 4, 2, 2)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,keep", [(256, 8, 4), (192, 16, 5), (96, 2, 1), (160, 4, 3), (512, 8, 3)])
+def test_route_equal_and_near_group_sums(scoring, E, groups, keep):
+    """Groups that hold the same experts' scores: equal sums on both sides of
+    the border, and sums a few units of binary32's last place apart."""
+    g = torch.Generator().manual_seed(E)
+    base = torch.randn(30, 1, E // groups, generator=g)
+    l = base.expand(30, groups, E // groups).contiguous()
+    l[10:20] = (l[10:20].view(torch.int32) + torch.randint(-2, 3, l[10:20].shape, generator=g).int()).view(torch.float32)
+    l[20:, 1::2] += 1e-6
+    l = l.view(30, E)
+    for dt in DTYPES:
+        for bias in (None, torch.zeros(E), 0.25 * torch.ones(E)):
+            for top in (1, 2):
+                check(l.to(dt), 4, scoring, bias, groups, keep, top)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_biases_of_every_size(scoring):
+    """A bias far above the scores, which they hardly show beside, far below,
+    of both signs, one expert out by -inf, all out."""
+    g = torch.Generator().manual_seed(7)
+    l = torch.randn(20, 256, generator=g)
+    for b in (100 * torch.randn(256, generator=g), 1e6 + torch.zeros(256), 1e-9 * torch.randn(256, generator=g),
+              1e30 * torch.randn(256, generator=g), torch.zeros(256).index_fill(0, torch.arange(0, 256, 3), -math.inf),
+              torch.full((256,), -math.inf)):
+        check(l, 8, scoring, b)
+        check(l, 8, scoring, b, 8, 4, 2)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 4161])
+def test_route_rows_beside_each_other(T):
+    """Rows that need the binary64 choice among rows that do not, at every
+    place of four, and a last wave that is not full."""
+    g = torch.Generator().manual_seed(T)
+    l = torch.randn(T, 64, generator=g)
+    l[::3] = 0.5
+    l[1::7, 5:] = -math.inf
+    for E, k in ((64, 8), (63, 16)):
+        check(l[:, :E].contiguous(), k, "sigmoid", 0.1 * torch.randn(E, generator=g))
+        check(l[:, :E].contiguous(), k, "softmax")
