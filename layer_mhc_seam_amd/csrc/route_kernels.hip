@@ -180,36 +180,43 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams P)
 // The choice from binary32 keys wherever they prove it right.  A row of 16
 // lanes takes a token, up to EPL experts a lane; with G groups 16 / G lanes
 // hold each group.  A key is a whole number: the score's place between the
-// row's lowest and highest in B bits above the expert's index (inverted, so
-// that the lowest of equal keys is the largest number).  Then one maximum
-// gives value and index at once, and the next largest is the maximum of
-// key - best modulo 2^32, where only smaller keys wrap around: a subtraction
-// and half a three-way maximum a key, and nothing to take out or look up.
+// row's lowest and highest, 1 .. 2^22, above the expert's index (inverted, so
+// that the lowest index of a place is the largest number); place 0 is no
+// expert.  One maximum then gives place and index at once.
 //
-// Scores are binary32 with an error of at most `delta` (below), so two keys
-// further apart than `need` units are in the order of the binary64 ones.  A
-// row in which two neighbours among the k + 1 largest, or the groups on both
-// sides of the border, are nearer than that goes through route_token
-// afterwards, and so does one that has too few experts left, infinities or
-// NaN.  At 256 experts that is about one row in 200.  Without a bias the
-// order is the logits' own: bf16 and fp16 logits fit a key whole, and no row
-// is too close to call (equal logits are common there and are ties).
+// Each lane sorts out its four largest keys (76 minima and maxima for 16);
+// its two largest give the groups' sums, and the choice takes the largest
+// head of the row's lanes and moves that lane on, 12 instructions a chosen
+// expert.  Only where a lane runs out of its four does the wave look through
+// all keys again for every next one.
+//
+// Scores are binary32 with an error of at most `delta`, so two keys further
+// apart than `need` places are in the order of the binary64 ones.  Where
+// neighbours among the k largest are nearer than that, or the k-th and the
+// next (then the choice goes on, up to 16, to a gap that is wide enough), the
+// binary64 keys of those chosen are compared.  A row whose groups are too
+// close on both sides of the border, that has too few experts left, or holds
+// infinities or NaN goes through route_token afterwards, one in 4000 at 256
+// experts in 8 groups.  Without a bias the order is the logits' own: bf16 and
+// fp16 logits fit a place whole, and no row is too close to call (equal
+// logits are common there and are ties).
 //
 // Weights are binary64 of the k chosen.
 constexpr int kIndexBits = 9;
 constexpr u32 kIndexMask = (1u << kIndexBits) - 1;
-constexpr int kValueBits = 30 - kIndexBits;   // keys stay below 2^31
+constexpr float kSpan = 0x3p20f, kPlaces = 0x1p22f - 1.0f;   // of the places; the last one
+constexpr int kRowWaves = 4;
 
 template <class T>
-struct Exact {   // bits of a binary32 value that T's do not use
+struct Whole {   // low bits of a binary32 value that T's have zero
     static constexpr int kShift = 0;
 };
 template <>
-struct Exact<__bf16> {
+struct Whole<__bf16> {
     static constexpr int kShift = 16;
 };
 template <>
-struct Exact<_Float16> {
+struct Whole<_Float16> {
     static constexpr int kShift = 13;
 };
 
@@ -220,126 +227,187 @@ __device__ __forceinline__ u32 in_order(float v)
     return b ^ ((u32)((int)b >> 31) | 0x80000000u);
 }
 
+// The first `count` of EPL values, the rest as `none`; four at a time
 template <class T, int EPL>
-__device__ __forceinline__ void load_logits(const T *p, int count, float (&v)[EPL])
+__device__ __forceinline__ void load_row(const T *p, int count, float none, float (&v)[EPL])
 {
     typedef T T4 __attribute__((ext_vector_type(4)));
     typedef T4 T4_any __attribute__((aligned(sizeof(T))));
+    T4 q[EPL / 4];
 #pragma unroll
     for (int j = 0; j < EPL; j += 4) {
         if (j + 4 <= count) {
-            const T4 q = *reinterpret_cast<const T4_any *>(p + j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[j + i] = (float)q[i];
+            q[j / 4] = *reinterpret_cast<const T4_any *>(p + j);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[j + i] = j + i < count ? (float)p[j + i] : -__builtin_inff();
+                if (j + i < count)
+                    q[j / 4][i] = p[j + i];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        v[j] = j < count ? (float)q[j / 4][j % 4] : none;
+}
+
+__device__ __forceinline__ void sort2(u32 &a, u32 &b)
+{
+    const u32 hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+
+// The four largest keys, largest first: sorted fours, joined two at a time
+template <int EPL>
+__device__ __forceinline__ void four_largest(const u32 (&key)[EPL], u32 (&h)[4])
+{
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4) {
+        u32 a = key[j], b = key[j + 1], c = key[j + 2], d = key[j + 3];
+        sort2(a, b);
+        sort2(c, d);
+        sort2(a, c);
+        sort2(b, d);
+        sort2(b, c);
+        if (j == 0) {
+            h[0] = a, h[1] = b, h[2] = c, h[3] = d;
+        } else {
+            h[0] = max(h[0], d), h[1] = max(h[1], c), h[2] = max(h[2], b), h[3] = max(h[3], a);
+            sort2(h[0], h[2]);
+            sort2(h[1], h[3]);
+            sort2(h[0], h[1]);
+            sort2(h[2], h[3]);
         }
     }
 }
 
 template <class T, int EPL>
-__global__ __launch_bounds__(64) void route_rows_kernel(RouteParams P, int64_t tokens)
+__global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams P, int64_t tokens)
 {
     static_assert(EPL % 4 == 0 && 16 * EPL <= (int)kIndexMask + 1, "indexes fit a key");
-    __shared__ double keys[EPL / 4 * 64];
-    const int lane = threadIdx.x, c = lane & 15;
-    const int64_t own = (int64_t)blockIdx.x * 4 + (lane >> 4);
+    __shared__ double keys_of[kRowWaves][EPL / 4 * 64];
+    const int lane = threadIdx.x & 63, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t first_token = ((int64_t)blockIdx.x * kRowWaves + wave) * 4;
+    if (first_token >= tokens)
+        return;
+    const int64_t own = first_token + (lane >> 4);
     const int64_t t = own < tokens ? own : tokens - 1;
     const T *row = static_cast<const T *>(P.logits) + t * P.E;
     const int lanes = 16 / P.groups, size = P.E / P.groups;   // of a group
     const int per = (size + lanes - 1) / lanes, sub = (c % lanes) * per;
     const int start = c / lanes * size + sub, count = max(0, min(per, size - sub));
-    const float ninf = -__builtin_inff();
-    float v[EPL];
-    load_logits<T, EPL>(row + start, count, v);
+    const float inf = __builtin_inff();
+    float v[EPL], b[EPL];
+    load_row<T, EPL>(row + start, count, -inf, v);
+    if (P.bias)
+        load_row<float, EPL>(P.bias + start, count, 0.0f, b);
+    float top = -inf, bottom = inf;
     bool odd = false;   // the row is for route_token
-    float top = ninf;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        odd |= !(v[j] < __builtin_inff());
-        top = fmaxf(top, v[j]);
+    for (int j = 0; j < EPL; j += 2) {
+        top = fmaxf(fmaxf(top, v[j]), v[j + 1]);
+        bottom = fminf(fminf(bottom, v[j]), v[j + 1]);
+        odd |= __builtin_isunordered(v[j], v[j + 1]);
     }
     top = row_max(top);
-    odd |= top == ninf;
+    odd |= !(top < inf && top > -inf);
     const bool by_group = P.groups > P.keep;
     u32 key[EPL];
     u32 need = 0;
-    if (Exact<T>::kShift > 0 && !P.bias && (!by_group || P.top == 1)) {
+    if (Whole<T>::kShift > 0 && !P.bias && (!by_group || P.top == 1)) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const u32 index = kIndexMask - (u32)(start + j);
-            key[j] = v[j] == ninf ? 0u
-                                  : (in_order(v[j]) >> Exact<T>::kShift) << kIndexBits | index;
-        }
+        for (int j = 0; j < EPL; ++j)
+            key[j] = v[j] == -inf ? 0u
+                                  : (in_order(v[j]) >> Whole<T>::kShift) << kIndexBits |
+                                        (kIndexMask - (u32)(start + j));
     } else {
         // scores with their error, then their places between lowest and highest
         float delta = 0.0f;
+        const bool gaps = __ballot(bottom == -inf) != 0;   // absent or masked experts
         if (P.bias || (by_group && P.top == 2)) {
             const float log2e = 1.44269504f;
-            float most = 1.0f;
+            float s[EPL], most = 1.0f;
             if (P.sigmoid) {
 #pragma unroll
                 for (int j = 0; j < EPL; ++j)
-                    v[j] = v[j] == ninf
-                               ? ninf
-                               : __builtin_amdgcn_rcpf(
-                                     1.0f + __builtin_amdgcn_exp2f(fminf(-v[j] * log2e, 126.0f)));
+                    s[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v[j] * log2e));
             } else {
                 float total = 0.0f;
 #pragma unroll
                 for (int j = 0; j < EPL; ++j) {
-                    const float e = __builtin_amdgcn_exp2f((v[j] - top) * log2e);
-                    v[j] = v[j] == ninf ? ninf : e;
-                    total += e;
+                    s[j] = __builtin_amdgcn_exp2f((v[j] - top) * log2e);
+                    total += s[j];
                 }
                 most = __builtin_amdgcn_rcpf(row_sum(total));
 #pragma unroll
                 for (int j = 0; j < EPL; ++j)
-                    v[j] *= most;
+                    s[j] *= most;
             }
-            float size_of = 0.0f;
             if (P.bias)
 #pragma unroll
-                for (int j = 0; j < EPL; ++j) {
-                    const float b = j < count ? P.bias[start + j] : 0.0f;
-                    v[j] += b;
-                    size_of = fmaxf(size_of, b == ninf ? 0.0f : fabsf(b));
-                }
+                for (int j = 0; j < EPL; ++j)
+                    s[j] += b[j];
+            if (gaps)
+#pragma unroll
+                for (int j = 0; j < EPL; ++j)
+                    s[j] = v[j] == -inf ? -inf : s[j];
             // In units of 2^-24: a sigmoid's exponent, exp2, sum and
             // reciprocal, weighted with s (1 - s) or s, come to less than 8;
             // a softmax's exponent, exp2, sum of 36 terms, reciprocal and
-            // product to less than 48 of its largest score.  Then the rounding
-            // of score + bias.
-            delta = (P.sigmoid ? 0x1p-21f : 0x1p-18f * most) +
-                    0x1p-23f * (most + row_max(size_of));
-        }
-        float hi = ninf, lo = __builtin_inff();
+            // product to less than 48 of its largest score.
+            delta = P.sigmoid ? 0x1p-21f : 0x1p-18f * most;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            hi = fmaxf(hi, v[j]);
-            lo = fminf(lo, v[j] == ninf ? __builtin_inff() : v[j]);
+            for (int j = 0; j < EPL; ++j)
+                v[j] = s[j];
         }
+        float hi = -inf, lo = inf;
+        if (gaps) {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                lo = fminf(lo, v[j] == -inf ? inf : v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                lo = fminf(lo, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            hi = fmaxf(hi, v[j]);
         hi = row_max(hi);
         lo = -row_max(-lo);
-        const float scale = (float)(1 << kValueBits) / (hi - lo);
-        odd |= !(hi - lo > 0.0f) || !(scale < 0x1p100f) || !(delta * scale < 0x1p16f);
-        need = 2 + (u32)(2.0f * fminf(delta * scale, 0x1p16f) + 1.0f);
+        if (P.bias) {
+            // a bias of -inf may have left lo at it
+            const bool masked = lo == -inf;
+            if (__ballot(masked)) {
+                lo = inf;
+#pragma unroll
+                for (int j = 0; j < EPL; ++j)
+                    lo = fminf(lo, v[j] == -inf ? inf : v[j]);
+                lo = -row_max(-lo);
+            }
+            // the rounding of score + bias
+            delta += 0x1p-24f * fmaxf(fabsf(hi), fabsf(lo));
+        }
+        // Places to the nearest, from the low bits of a sum with 2^23.  What
+        // is the same for all of them (scale, base) keeps their order; the
+        // product and the sum round each by less than 5 / 8.  The lowest place
+        // is above `need`, so that no expert is as far from every one.
+        const float scale = kSpan / (hi - lo), from = -lo * scale;
+        const float slack = 2.0f * delta * scale + 0x1p-22f * fabsf(from) + 2.0f;
+        odd |= !(hi - lo > 0.0f) || !(scale < 0x1p100f) || !(slack < 0x1p18f);
+        need = (u32)fminf(slack, 0x1p18f) + 1u;
+        const float base = from + (2.0f * slack + 2.0f);
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const u32 place = 1u + (u32)fminf((v[j] - lo) * scale, (float)(1 << kValueBits));
-            key[j] = v[j] == ninf ? 0u : place << kIndexBits | (kIndexMask - (u32)(start + j));
+            const float place = fminf(fmaxf(__builtin_fmaf(v[j], scale, base), 0.0f), kPlaces);
+            key[j] = __float_as_uint(place + 0x1p23f) << kIndexBits | (kIndexMask - (u32)(start + j));
         }
     }
+    u32 h[4];
+    four_largest<EPL>(key, h);
     if (by_group) {
-        u32 first = 0, second = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            second = max(second, min(first, key[j]));
-            first = max(first, key[j]);
-        }
+        u32 first = h[0], second = h[1];
         auto join = [&](u32 f, u32 s) {
             second = max(max(second, s), min(first, f));
             first = max(first, f);
@@ -352,16 +420,24 @@ __global__ __launch_bounds__(64) void route_rows_kernel(RouteParams P, int64_t t
             join(row_swap<kXor4>(first), row_swap<kXor4>(second));
         u32 mine = first;
         if (P.top == 2) {
-            odd |= second == 0;
+            odd |= second <= kIndexMask;
             mine = (first >> kIndexBits) + (second >> kIndexBits);
         }
-        // lanes of groups that come before this lane's
+        // groups that come before this lane's
         int before = 0;
 #define COUNT(N) before += row_ror<N>(mine) > mine;
-        COUNT(1) COUNT(2) COUNT(3) COUNT(4) COUNT(5) COUNT(6) COUNT(7) COUNT(8)
-        COUNT(9) COUNT(10) COUNT(11) COUNT(12) COUNT(13) COUNT(14) COUNT(15)
+        if (lanes == 1) {
+            COUNT(1) COUNT(3) COUNT(5) COUNT(7) COUNT(9) COUNT(11) COUNT(13) COUNT(15)
+        }
+        if (lanes <= 2) {
+            COUNT(2) COUNT(6) COUNT(10) COUNT(14)
+        }
+        if (lanes <= 4) {
+            COUNT(4) COUNT(12)
+        }
+        COUNT(8)
 #undef COUNT
-        const bool open = before < P.keep * lanes;
+        const bool open = before < P.keep;
         const int shift = P.top == 2 ? 0 : kIndexBits;
         const u32 last = ~row_max(open ? ~(mine >> shift) : 0u);
         const u32 next = row_max(open ? 0u : mine >> shift);
@@ -369,50 +445,91 @@ __global__ __launch_bounds__(64) void route_rows_kernel(RouteParams P, int64_t t
         // equal sums: more groups open than there should be
         odd |= need > 0 &&
                __builtin_popcountll(__ballot(open) >> (lane & 48) & 0xffff) != P.keep * lanes;
-        if (!open)
+        if (!open) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
                 key[j] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                h[j] = 0;
+        }
     }
-    u32 best = 0;
+    // `chosen`: the c-th of the row.  `sure`: how many of them are a set that
+    // is certain, k where the gap after the k-th is wide enough.  `close`: some
+    // of them are nearer to each other than `need`.
+    u32 best = row_max(h[0]), chosen = best;
+    int sure = 0, popped = 0;
+    bool close = false, all_keys = false;
+    for (int i = 1; i <= 16; ++i) {
+        odd |= i <= P.k && best <= kIndexMask;
+        const bool here = h[0] == best;
+        popped += here;
+        h[0] = here ? h[1] : h[0];
+        h[1] = here ? h[2] : h[1];
+        h[2] = here ? h[3] : h[2];
+        h[3] = here ? 0u : h[3];
+        u32 next;
+        all_keys |= __ballot(popped >= 4) != 0;
+        if (!all_keys) {
+            next = row_max(h[0]);
+        } else {
+            // the largest key below `best`: modulo 2^32 only those wrap around
+            u32 step = 0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-        best = max(best, key[j]);
-    best = row_max(best);
-    u32 chosen = best;   // lane i of the row keeps the i-th
-    for (int i = 1; i <= P.k; ++i) {
-        odd |= best == 0;
-        u32 step = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            step = max(step, key[j] - best);
-        step = row_max(step);
-        const u32 next = (int)step < 0 ? best + step : 0u;
-        odd |= next > 0 && (best >> kIndexBits) - (next >> kIndexBits) < need;
+            for (int j = 0; j < EPL; ++j)
+                step = max(step, key[j] - best);
+            step = row_max(step);
+            next = (int)step < 0 ? best + step : 0u;
+        }
+        const bool wide = (best >> kIndexBits) - (next >> kIndexBits) >= need;
+        if (i < P.k)
+            close |= !wide;
+        else if (sure == 0) {
+            sure = wide ? i : 0;
+            close |= !wide;
+        }
+        if (i >= P.k && __ballot(sure == 0 && !odd) == 0)
+            break;
         best = next;
         chosen = c == i ? best : chosen;
     }
-    const bool has = c < P.k;
-    const int id = (int)(kIndexMask - (chosen & kIndexMask));
-    double w = 0.0;
-    if (has) {
-        const double l = (double)(float)row[min(id, P.E - 1)];
-        w = P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top);
+    odd |= sure == 0;
+    int id = (int)(kIndexMask - (chosen & kIndexMask)), rank = c;
+    const double l = (double)(float)row[min(id, P.E - 1)];
+    double w = P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top);
+    if (__ballot(close)) {
+        odd |= close && P.bias && !P.sigmoid;   // needs the sum of all scores
+        double mine = l;
+        if (P.bias)
+            mine = w + (double)P.bias[min(id, P.E - 1)];
+        if (c >= sure)
+            mine = -__builtin_inf();
+        int before = 0;
+#define COUNT(N)                                                                            \
+    {                                                                                       \
+        const double other = row_ror<N>(mine);                                              \
+        const int other_id = (int)row_ror<N>((u32)id);                                      \
+        before += other > mine || (other == mine && other_id < id);                         \
     }
-    const double sum = row_sum(w);
+        COUNT(1) COUNT(2) COUNT(3) COUNT(4) COUNT(5) COUNT(6) COUNT(7) COUNT(8)
+        COUNT(9) COUNT(10) COUNT(11) COUNT(12) COUNT(13) COUNT(14) COUNT(15)
+#undef COUNT
+        rank = close && c < sure ? before : c;
+    }
+    const bool has = rank < P.k && c < (close ? sure : P.k);
+    const double sum = row_sum(has ? w : 0.0);
     if (P.renorm)
         w = sum > 0.0 ? w / sum : 0.0;
     // a row's lanes agree on `odd` once they have all been asked
     const u64 lanes_odd = __ballot(odd);
-    const bool mine_odd = (lanes_odd >> (lane & 48) & 0xffff) != 0;
-    if (has && own < tokens && !mine_odd) {
-        P.weights[t * P.k + c] = (float)(w * (double)P.scale);
-        P.ids[t * P.k + c] = id;
+    if (has && own < tokens && (lanes_odd >> (lane & 48) & 0xffff) == 0) {
+        P.weights[t * P.k + rank] = (float)(w * (double)P.scale);
+        P.ids[t * P.k + rank] = id;
     }
     for (int r = 0; r < 4; ++r) {
-        const int64_t tt = (int64_t)blockIdx.x * 4 + r;
+        const int64_t tt = first_token + r;
         if ((lanes_odd >> (16 * r) & 0xffff) && tt < tokens)
-            route_token<T, EPL / 4>(P, tt, lane, keys);
+            route_token<T, EPL / 4>(P, tt, lane, keys_of[wave]);
     }
 }
 
@@ -428,10 +545,10 @@ bool rows_fit(const RouteParams &p)
 template <class T>
 hipError_t launch(const RouteParams &p, int64_t tokens, hipStream_t s)
 {
-    const dim3 block(64);
     if (rows_fit(p)) {
         const int lanes = 16 / p.groups, size = p.E / p.groups, per = (size + lanes - 1) / lanes;
-        const dim3 grid((unsigned)((tokens + 3) / 4));
+        const int a_block = 4 * kRowWaves;
+        const dim3 grid((unsigned)((tokens + a_block - 1) / a_block)), block(64 * kRowWaves);
         if (per <= 4)
             hipLaunchKernelGGL((route_rows_kernel<T, 4>), grid, block, 0, s, p, tokens);
         else if (per <= 8)
@@ -442,7 +559,7 @@ hipError_t launch(const RouteParams &p, int64_t tokens, hipStream_t s)
             hipLaunchKernelGGL((route_rows_kernel<T, 32>), grid, block, 0, s, p, tokens);
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)tokens);
+    const dim3 grid((unsigned)tokens), block(64);
     if (p.E <= 64)
         hipLaunchKernelGGL((route_kernel<T, 1>), grid, block, 0, s, p);
     else if (p.E <= 128)
