@@ -439,6 +439,14 @@ int mhc_int8_gemm(const int8_t *a, const float *a_scales, const int8_t *b, const
                   const float *bias, int64_t T, int32_t N, int32_t K, int32_t out_dtype, void *out,
                   void *stream);
 
+/*
+ * The output blocks mhc_int8_gemm launches for T x N on a device with
+ * cu_count compute units: *tm x *tn outputs per workgroup.  Host only; the
+ * same choice the launch makes.  INVALID_ARG unless T is in 1 .. 2^31 - 1,
+ * N > 0, cu_count > 0 and both outputs are non-null.
+ */
+int mhc_int8_gemm_blocks(int64_t T, int32_t N, int32_t cu_count, int32_t *tm, int32_t *tn);
+
 typedef enum mhc_scoring {
     MHC_SOFTMAX = 0,
     MHC_SIGMOID = 1

@@ -204,6 +204,17 @@ int mhc_int8_gemm(const int8_t *a, const float *a_scales, const int8_t *b, const
     return MHC_SEAM_OK;
 }
 
+int mhc_int8_gemm_blocks(int64_t T, int32_t N, int32_t cu_count, int32_t *tm, int32_t *tn)
+{
+    if (T <= 0 || T > INT32_MAX || N <= 0 || cu_count <= 0 || !tm || !tn)
+        return fail(MHC_SEAM_INVALID_ARG,
+                    "gemm blocks need T in 1..2^31-1, N > 0, cu_count > 0 and two outputs");
+    const mhc::GemmBlocks g = mhc::int8_gemm_blocks(T, N, cu_count);
+    *tm = g.tm;
+    *tn = g.tn;
+    return MHC_SEAM_OK;
+}
+
 int mhc_route(const mhc_route_args *a, void *stream)
 {
     if (!a)

@@ -27,8 +27,6 @@ typedef uint32_t u32;
 typedef u32 u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kStep = 128;   // K per step of the tiled kernels
-
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 typedef __attribute__((address_space(3))) void *lds_ptr;
 
@@ -66,33 +64,52 @@ __device__ __forceinline__ void block_barrier()
 // ------------------------------------------------------------ tiled kernel --
 //
 // A workgroup of (TM / WM)(TN / WN) waves computes a TM x TN block, each wave
-// WM x WN of it, in 128-wide K steps.  A step's rows go from memory straight
-// into LDS (16 bytes a lane, 1 KB a wave and instruction: 8 rows of 128
-// bytes); S stages keep S - 1 steps' loads in flight.  Piece c of row R lies
-// in slot c ^ ((R >> 1) & 7) of its row, which puts the 16 lanes of a read
-// phase on different banks.
-template <int TM_, int TN_, int WM_, int WN_, int S_>
+// WM x WN of it, in steps of KS = 128, 256 or 512 of K.  A step's rows go from
+// memory straight into LDS (16 bytes a lane, 1 KB a wave and instruction:
+// 1024 / KS rows of KS bytes); S stages keep S - 1 steps' loads in flight.
+// Piece c of row R lies in slot c ^ turn(R) of its row, which puts the 16
+// lanes of a read phase (16 rows, one piece each) on different banks: two
+// rows of 128 bytes, or 256 of a row, cover the banks once.
+template <int TM_, int TN_, int WM_, int WN_, int S_, int KS_ = 128>
 struct Tile {
-    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, S = S_;
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, S = S_, KS = KS_;
     static constexpr int NW = (TM / WM) * (TN / WN);
     static constexpr int kThreads = 64 * NW;
-    static constexpr int kRunsA = TM / 8 / NW, kRunsB = TN / 8 / NW;   // 1 KB runs per wave and step
+    static constexpr int kPieces = KS / 16, kRunRows = 1024 / KS;   // of a row; of a 1 KB run
+    static constexpr int kRunsA = TM / kRunRows / NW, kRunsB = TN / kRunRows / NW;   // a wave's
     static constexpr int kLoads = kRunsA + kRunsB;
-    static_assert(kRunsA * 8 * NW == TM && kRunsB * 8 * NW == TN, "whole runs per wave");
-    static_assert(S >= 2 && (S - 1) * kLoads < 64, "the loads in flight fit the vmcnt counter");
+    static constexpr int kFactors = (TM + 2 * TN + kThreads - 1) / kThreads;   // a thread's
+    static_assert(KS == 128 || KS == 256 || KS == 512, "turn() is for these");
+    static_assert(kRunsA * kRunRows * NW == TM && kRunsB * kRunRows * NW == TN,
+                  "whole runs per wave");
+    static_assert(S >= 2 && (S - 1) * kLoads + kFactors < 64,
+                  "the loads in flight fit the vmcnt counter");
+    static_assert(S * (TM + TN) * KS >= TM * TN * 2, "16-bit results fit the stages");
+    static __device__ __forceinline__ int turn(int row)
+    {
+        return KS == 128 ? row >> 1 & 7 : row & 15;
+    }
 };
 
 template <class C>
 struct StageT {
-    int8_t a[C::TM * kStep];
-    int8_t b[C::TN * kStep];
+    alignas(16) int8_t a[C::TM * C::KS];
+    alignas(16) int8_t b[C::TN * C::KS];
+};
+
+// A workgroup's LDS.  (One object: beside a second one the compiler waits for
+// every load in flight before it reads the first.)
+template <class C>
+struct TileLds {
+    StageT<C> st[C::S];
+    float factor[C::TM + 2 * C::TN];   // the block's sa, sb and bias
 };
 
 // Buffer resources based at the block's first rows, so that offsets fit 32
 // bits whatever T K and N K, and this lane's offsets in them.  Rows past the
 // end re-read the last.  In a last step that K does not fill, a row's pieces
 // past K hold the next row's bytes (past the last row the resource ends and
-// nothing outside is read); the products leave them out.
+// nothing outside is read); zero_tail leaves them out.
 template <class C>
 struct SrcT {
     rsrc_t a, b;
@@ -107,16 +124,16 @@ __device__ __forceinline__ SrcT<C> src_tile(const Int8GemmParams &P, int m_blk, 
     SrcT<C> s;
     s.a = make_rsrc(P.a + (size_t)m_blk * P.K, (uint32_t)(ra * P.K));
     s.b = make_rsrc(P.b + (size_t)n_blk * P.K, (uint32_t)(rb * P.K));
-    const int slot = lane & 7;
+    const int slot = lane % C::kPieces, sub = lane / C::kPieces;
 #pragma unroll
     for (int i = 0; i < C::kRunsA; ++i) {
-        const int row = 8 * (wave * C::kRunsA + i) + (lane >> 3);
-        s.oa[i] = min(row, ra - 1) * P.K + 16 * (slot ^ ((row >> 1) & 7));
+        const int row = C::kRunRows * (wave * C::kRunsA + i) + sub;
+        s.oa[i] = min(row, ra - 1) * P.K + 16 * (slot ^ C::turn(row));
     }
 #pragma unroll
     for (int i = 0; i < C::kRunsB; ++i) {
-        const int row = 8 * (wave * C::kRunsB + i) + (lane >> 3);
-        s.ob[i] = min(row, rb - 1) * P.K + 16 * (slot ^ ((row >> 1) & 7));
+        const int row = C::kRunRows * (wave * C::kRunsB + i) + sub;
+        s.ob[i] = min(row, rb - 1) * P.K + 16 * (slot ^ C::turn(row));
     }
     return s;
 }
@@ -126,10 +143,10 @@ __device__ __forceinline__ void fetch_step(const SrcT<C> &s, int ks, StageT<C> &
 {
 #pragma unroll
     for (int i = 0; i < C::kRunsA; ++i)
-        load_lds(s.a, st.a + 1024 * (wave * C::kRunsA + i), s.oa[i], ks * kStep);
+        load_lds(s.a, st.a + 1024 * (wave * C::kRunsA + i), s.oa[i], ks * C::KS);
 #pragma unroll
     for (int i = 0; i < C::kRunsB; ++i)
-        load_lds(s.b, st.b + 1024 * (wave * C::kRunsB + i), s.ob[i], ks * kStep);
+        load_lds(s.b, st.b + 1024 * (wave * C::kRunsB + i), s.ob[i], ks * C::KS);
 }
 
 // Block order: consecutive workgroups go to the 8 XCDs in turn, and XCD x
@@ -157,11 +174,94 @@ __device__ __forceinline__ O finish(int acc, float sa, float sb, float bias, boo
     return (O)rounded(has_bias ? v + bias : v);
 }
 
+// The block's results from a wave's sums: binary32 straight to memory (16
+// lanes store 64 consecutive bytes), 16-bit types by way of LDS (`ot`, free by
+// now) to 16-byte pieces of rows, or single elements, 64 in a row, where rows
+// do not start on 16 bytes.  factor: the block's sa, sb and bias.
+template <class C, class O>
+__device__ __forceinline__ void store_block(const Int8GemmParams &P, int m_blk, int n_blk, int wm,
+                                            int wn, const i32x4 (&acc)[C::WM / 16][C::WN / 16],
+                                            const float *factor, O *ot)
+{
+    constexpr int MI = C::WM / 16, NJ = C::WN / 16;
+    const int tid = threadIdx.x, g = tid >> 4 & 3, r = tid & 15;
+    const int T = P.T, N = P.N;
+    O *out = static_cast<O *>(P.out);
+    float sb[NJ], bias[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        sb[j] = factor[C::TM + wn + 16 * j + r];
+        bias[j] = factor[C::TM + C::TN + wn + 16 * j + r];
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = wm + 16 * i + 4 * g + e;
+            const float sa = factor[row];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int col = wn + 16 * j + r;
+                const O v = finish<O>(acc[i][j][e], sa, sb[j], bias[j], P.bias != nullptr);
+                if constexpr (sizeof(O) == 2)
+                    ot[row * C::TN + col] = v;
+                else if (m_blk + row < T && n_blk + col < N)
+                    out[(size_t)(m_blk + row) * N + n_blk + col] = v;
+            }
+        }
+    if constexpr (sizeof(O) == 2) {
+        __syncthreads();
+        const int rows = min(C::TM, T - m_blk), cols = min(C::TN, N - n_blk);
+        O *to = out + (size_t)m_blk * N + n_blk;
+        if (N % 8 == 0) {
+            for (int c = tid; c < C::TM * C::TN / 8; c += C::kThreads) {
+                const int row = c / (C::TN / 8), col = c % (C::TN / 8) * 8;
+                if (row < rows && col < cols)
+                    *reinterpret_cast<u32x4 *>(to + (size_t)row * N + col) =
+                        *reinterpret_cast<const u32x4 *>(ot + row * C::TN + col);
+            }
+        } else {
+            for (int c = tid; c < C::TM * C::TN; c += C::kThreads) {
+                const int row = c / C::TN, col = c % C::TN;
+                if (row < rows && col < cols)
+                    to[(size_t)row * N + col] = ot[c];
+            }
+        }
+    }
+}
+
+// sa, sb or bias of the block's i-th factor
+template <class C>
+__device__ __forceinline__ float factor_of(const Int8GemmParams &P, int m_blk, int n_blk, int i)
+{
+    const int col = i - C::TM;
+    return i < C::TM           ? P.sa[min(m_blk + i, P.T - 1)]
+           : col < C::TN       ? P.sb[min(n_blk + col, P.N - 1)]
+           : P.bias != nullptr ? P.bias[min(n_blk + col - C::TN, P.N - 1)]
+                               : 0.0f;
+}
+
+// A last step that K does not fill: zeros in B's pieces past K leave the
+// products out, whatever A's rows hold there.
+template <class C>
+__device__ __forceinline__ void zero_tail(int8_t *b, int pieces)
+{
+    const int rest = C::kPieces - pieces;
+    for (int i = threadIdx.x; i < C::TN * rest; i += C::kThreads) {
+        const int row = i / rest, piece = pieces + i % rest;
+        *reinterpret_cast<i32x4 *>(b + row * C::KS + 16 * (piece ^ C::turn(row))) =
+            i32x4{0, 0, 0, 0};
+    }
+    __syncthreads();
+}
+
 template <class C, class O>
 __global__ __launch_bounds__(C::kThreads, 1) void int8_gemm_tile_kernel(Int8GemmParams P)
 {
     constexpr int MI = C::WM / 16, NJ = C::WN / 16, S = C::S;
-    __shared__ StageT<C> st[S];
+    __shared__ TileLds<C> lds;
+    StageT<C>(&st)[S] = lds.st;
+    float(&factor)[C::TM + 2 * C::TN] = lds.factor;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int T = P.T, N = P.N;
@@ -171,21 +271,37 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_gemm_tile_kernel(Int8Gemm
     const int m_blk = mi * C::TM, n_blk = ni * C::TN;
     const int wm = (wave / (C::TN / C::WN)) * C::WM, wn = (wave % (C::TN / C::WN)) * C::WN;
     const int g = lane >> 4, r = lane & 15;
-    const int p0 = 16 * (g ^ (r >> 1)), p1 = p0 ^ 64;   // slots of pieces g and g + 4 of row r
+    constexpr int Q = C::KS / 64;   // products of a step: pieces g + 4 q of row r
+    int at[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        at[q] = r * C::KS + 16 * ((g + 4 * q) ^ C::turn(r));
     i32x4 acc[MI][NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
             acc[i][j] = i32x4{0, 0, 0, 0};
-    const int steps = (P.K + kStep - 1) / kStep;
-    const int pieces = (P.K - (steps - 1) * kStep) / 16;   // of the last step
+    // The factors are asked for first: their way from memory is as long as
+    // several steps, and the first rows' follows on its heels.
+    float f[C::kFactors];
+#pragma unroll
+    for (int i = 0; i < C::kFactors; ++i)
+        f[i] = factor_of<C>(P, m_blk, n_blk, min(tid + i * C::kThreads, C::TM + 2 * C::TN - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    const int steps = (P.K + C::KS - 1) / C::KS;
+    const int pieces = (P.K - (steps - 1) * C::KS) / 16;   // of the last step
     const SrcT<C> src = src_tile<C>(P, m_blk, n_blk, wave, lane);
     // Steps past the end re-read the last into a free stage: every step has
     // the same loads in flight, so the waits are constants.
 #pragma unroll
     for (int p = 0; p < S - 1; ++p)
         fetch_step<C>(src, min(p, steps - 1), st[p], wave);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < C::kFactors; ++i)
+        if (tid + i * C::kThreads < C::TM + 2 * C::TN)
+            factor[tid + i * C::kThreads] = f[i];
     int cur_s = 0, next_s = S - 1;
     for (int ks = 0; ks < steps; ++ks) {
         wait_vm<(S - 2) * C::kLoads>();   // this wave's loads of step ks are in LDS
@@ -193,32 +309,27 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_gemm_tile_kernel(Int8Gemm
         fetch_step<C>(src, min(ks + S - 1, steps - 1), st[next_s], wave);
         __builtin_amdgcn_sched_barrier(0);
         const StageT<C> &cur = st[cur_s];
-        const bool ragged = ks == steps - 1 && pieces < 8;
-        i32x4 b0[NJ], b1[NJ];
+        if (ks == steps - 1 && pieces < C::kPieces)
+            zero_tail<C>(st[cur_s].b, pieces);
+        i32x4 b[NJ][Q];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int8_t *p = cur.b + (wn + 16 * j + r) * kStep;
-            b0[j] = *reinterpret_cast<const i32x4 *>(p + p0);
-            b1[j] = *reinterpret_cast<const i32x4 *>(p + p1);
-            if (ragged) {   // integers: a zero on one side leaves the product out
-                if (g >= pieces)
-                    b0[j] = i32x4{0, 0, 0, 0};
-                if (g + 4 >= pieces)
-                    b1[j] = i32x4{0, 0, 0, 0};
-            }
-        }
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                b[j][q] = *reinterpret_cast<const i32x4 *>(cur.b + (wn + 16 * j) * C::KS + at[q]);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            const int8_t *p = cur.a + (wm + 16 * i + r) * kStep;
-            const i32x4 a0 = *reinterpret_cast<const i32x4 *>(p + p0);
-            const i32x4 a1 = *reinterpret_cast<const i32x4 *>(p + p1);
+            i32x4 a[Q];
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, b0[j], acc[i][j], 0, 0, 0);
+            for (int q = 0; q < Q; ++q)
+                a[q] = *reinterpret_cast<const i32x4 *>(cur.a + (wm + 16 * i) * C::KS + at[q]);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, b1[j], acc[i][j], 0, 0, 0);
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[q], b[j][q], acc[i][j], 0,
+                                                                      0, 0);
         }
         __builtin_amdgcn_s_setprio(0);
         cur_s = cur_s == S - 1 ? 0 : cur_s + 1;
@@ -226,71 +337,157 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_gemm_tile_kernel(Int8Gemm
     }
     wait_vm<0>();      // the re-reads past the end have landed
     __syncthreads();   // and every wave is done with the stages
-    O *out = static_cast<O *>(P.out);
-    float sb[NJ], bias[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int col = min(n_blk + wn + 16 * j + r, N - 1);
-        sb[j] = P.sb[col];
-        bias[j] = P.bias ? P.bias[col] : 0.0f;
-    }
-    if constexpr (sizeof(O) == 4) {
-        // 16 lanes store 64 consecutive bytes
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = m_blk + wm + 16 * i + 4 * g + e;
-                if (row >= T)
-                    continue;
-                const float sa = P.sa[row];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const int col = n_blk + wn + 16 * j + r;
-                    if (col < N)
-                        out[(size_t)row * N + col] =
-                            finish<O>(acc[i][j][e], sa, sb[j], bias[j], P.bias != nullptr);
-                }
-            }
-    } else {
-        // the block in LDS, then 16-byte row pieces to memory
-        static_assert(sizeof(O) == 4 || S * sizeof(StageT<C>) >= C::TM * C::TN * sizeof(O),
-                      "the output block fits the stages");
-        O *ot = reinterpret_cast<O *>(&st[0]);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = wm + 16 * i + 4 * g + e;
-                const float sa = P.sa[min(m_blk + row, T - 1)];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    ot[row * C::TN + wn + 16 * j + r] =
-                        finish<O>(acc[i][j][e], sa, sb[j], bias[j], P.bias != nullptr);
-            }
-        __syncthreads();
-        const bool whole = N % 8 == 0;
-        for (int c = tid; c < C::TM * C::TN / 8; c += C::kThreads) {
-            const int row = c / (C::TN / 8), col = (c % (C::TN / 8)) * 8;
-            const int gr = m_blk + row, gc = n_blk + col;
-            if (gr >= T || gc >= N)
-                continue;
-            O *dst = out + (size_t)gr * N + gc;
-            const O *e8 = ot + row * C::TN + col;
-            if (whole) {
-                *reinterpret_cast<u32x4 *>(dst) = *reinterpret_cast<const u32x4 *>(e8);
-            } else {
-                for (int e = 0; e < 8 && gc + e < N; ++e)
-                    dst[e] = e8[e];
-            }
-        }
-    }
+    store_block<C, O>(P, m_blk, n_blk, wm, wn, acc, factor, reinterpret_cast<O *>(&st[0]));
 }
 
-using BigTile = Tile<256, 256, 64, 128, 2>;
-using MidTile = Tile<128, 128, 64, 64, 3>;
-using SmallTile = Tile<64, 64, 32, 32, 3>;
-using Tile32 = Tile<32, 32, 16, 16, 6>;
+// --------------------------------------------------------- 256 x 256 blocks --
+//
+// The largest block, for many rows: 8 waves of 64 x 128 and 128-wide steps,
+// whose loads, LDS reads and products overlap in each wave.  A step's products
+// take two halves of 64 of K.  While one half's are issued, the other half's
+// fragments (or the next step's first) come from LDS into registers, one read
+// for two products.  In the middle of a step all of its rows are in
+// registers; after a barrier there the loads of later steps overwrite them.
+// LDS holds five half steps (A or B rows, 32 KB each, 160 KB in all) in a
+// ring: when a step's rows have to be there, the A rows of the one after it
+// are still on their way, so loads never run dry.
+using RingTile = Tile<256, 256, 64, 128, 2>;
+
+template <class O>
+__global__ __launch_bounds__(RingTile::kThreads, 1) void int8_gemm_ring_kernel(Int8GemmParams P)
+{
+    using C = RingTile;
+    constexpr int MI = C::WM / 16, NJ = C::WN / 16, kSlots = 5, kSlot = C::TM * C::KS;
+    constexpr int kHalf = C::kRunsA;   // loads of a half step, a wave's
+    static_assert(C::TM == C::TN, "A and B rows share the slots");
+    static_assert(kSlots * kSlot >= C::TM * C::TN * 2 + 4 * (C::TM + 2 * C::TN),
+                  "16-bit results and the factors fit");
+    __shared__ alignas(16) int8_t lds[kSlots * kSlot];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int mi, ni;
+    if (!block_of(blockIdx.x, (P.T + C::TM - 1) / C::TM, (P.N + C::TN - 1) / C::TN, mi, ni))
+        return;
+    const int m_blk = mi * C::TM, n_blk = ni * C::TN;
+    const int wm = (wave / (C::TN / C::WN)) * C::WM, wn = (wave % (C::TN / C::WN)) * C::WN;
+    const int g = lane >> 4, r = lane & 15;
+    const int at[2] = {r * C::KS + 16 * (g ^ C::turn(r)), r * C::KS + 16 * ((g + 4) ^ C::turn(r))};
+    i32x4 acc[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            acc[i][j] = i32x4{0, 0, 0, 0};
+    const int steps = (P.K + C::KS - 1) / C::KS;
+    const int pieces = (P.K - (steps - 1) * C::KS) / 16;   // of the last step
+    const bool ragged = pieces < C::kPieces;
+    const SrcT<C> src = src_tile<C>(P, m_blk, n_blk, wave, lane);
+    // steps past the end re-read the last, so that waits are constants
+    auto fetch_a = [&](int ks, int slot) {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+            load_lds(src.a, lds + slot * kSlot + 1024 * (wave * kHalf + i), src.oa[i],
+                     min(ks, steps - 1) * C::KS);
+    };
+    auto fetch_b = [&](int ks, int slot) {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+            load_lds(src.b, lds + slot * kSlot + 1024 * (wave * kHalf + i), src.ob[i],
+                     min(ks, steps - 1) * C::KS);
+    };
+    i32x4 a0[MI], b0[NJ], a1[MI], b1[NJ];   // fragments of a step's halves
+    auto read = [&](i32x4(&a)[MI], i32x4(&b)[NJ], int slot_a, int slot_b, int half) {
+        const int8_t *pa = lds + slot_a * kSlot + wm * C::KS + at[half];
+        const int8_t *pb = lds + slot_b * kSlot + wn * C::KS + at[half];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            b[j] = *reinterpret_cast<const i32x4 *>(pb + 16 * C::KS * j);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            a[i] = *reinterpret_cast<const i32x4 *>(pa + 16 * C::KS * i);
+    };
+    // the products, two for each of the reads asked for before them
+    auto multiply = [&](const i32x4(&a)[MI], const i32x4(&b)[NJ]) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < MI + NJ; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, MI * NJ - 2 * (MI + NJ), 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    fetch_a(0, 0);
+    fetch_b(0, 1);
+    fetch_a(1, 2);
+    fetch_b(1, 3);
+    fetch_a(2, 4);
+    wait_vm<3 * kHalf>();
+    block_barrier();
+    if (ragged && steps == 1)
+        zero_tail<C>(lds + kSlot, pieces);
+    int slot_a = 0, slot_b = 1;
+    float f[C::kFactors] = {};
+    read(a0, b0, slot_a, slot_b, 0);
+    for (int ks = 0; ks < steps; ++ks) {
+        const int next_a = slot_a >= kSlots - 2 ? slot_a - (kSlots - 2) : slot_a + 2;
+        const int next_b = slot_b >= kSlots - 2 ? slot_b - (kSlots - 2) : slot_b + 2;
+        read(a1, b1, slot_a, slot_b, 1);
+        multiply(a0, b0);
+        wait_vm<kHalf>();   // the next step's rows are in LDS, the A rows after them may not be
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and this step's in registers
+        block_barrier();
+        if (ragged && ks + 1 == steps - 1)
+            zero_tail<C>(lds + next_b * kSlot, pieces);
+        fetch_b(ks + 2, slot_a);
+        fetch_a(ks + 3, slot_b);
+        if (ks == steps - 1)
+#pragma unroll
+            for (int i = 0; i < C::kFactors; ++i)
+                f[i] = factor_of<C>(P, m_blk, n_blk, min(tid + i * C::kThreads,
+                                                         C::TM + 2 * C::TN - 1));
+        __builtin_amdgcn_sched_barrier(0);
+        read(a0, b0, next_a, next_b, 0);
+        multiply(a1, b1);
+        slot_a = next_a;
+        slot_b = next_b;
+    }
+    wait_vm<0>();      // the re-reads past the end have landed
+    __syncthreads();   // and every wave is done with the slots
+    float *factor = reinterpret_cast<float *>(lds + C::TM * C::TN * 2);
+#pragma unroll
+    for (int i = 0; i < C::kFactors; ++i)
+        if (tid + i * C::kThreads < C::TM + 2 * C::TN)
+            factor[tid + i * C::kThreads] = f[i];
+    __syncthreads();
+    store_block<C, O>(P, m_blk, n_blk, wm, wn, acc, factor, reinterpret_cast<O *>(lds));
+}
+
+// The shapes a launch chooses from, smallest first, with what a round of the
+// CUs costs: measured times of one workgroup a CU at K = 5120 less the
+// launch's 2 us, in units of half a microsecond.  Few rows of K a step leave
+// the small blocks waiting at barriers (16 x 32 in steps of 128, 256 and 512:
+// 8.1, 7.0 and 6.8 us at T = 1, N = K = 5120); from 128 x 128 on LDS has no
+// room for more than 128.
+template <class F>
+void int8_shapes(F &&f)
+{
+    f(Tile<16, 32, 16, 16, 3, 512>(), 10);
+    f(Tile<32, 32, 16, 16, 4, 256>(), 12);
+    f(Tile<32, 64, 16, 32, 4, 256>(), 16);
+    f(Tile<64, 64, 16, 32, 3, 256>(), 21);
+    f(Tile<96, 64, 48, 16, 3, 256>(), 28);
+    f(Tile<128, 64, 32, 32, 3, 256>(), 32);
+    f(Tile<128, 128, 32, 32, 4, 128>(), 45);
+    f(Tile<128, 192, 32, 96, 3, 128>(), 62);
+    f(Tile<128, 256, 64, 64, 3, 128>(), 75);
+    f(Tile<192, 256, 96, 64, 2, 128>(), 100);
+    f(RingTile(), 122);
+}
 
 template <class C, class O>
 hipError_t launch_tile(const Int8GemmParams &p, hipStream_t s)
@@ -298,39 +495,43 @@ hipError_t launch_tile(const Int8GemmParams &p, hipStream_t s)
     const int64_t total = (int64_t)((p.T + C::TM - 1) / C::TM) * ((p.N + C::TN - 1) / C::TN);
     if (total > INT32_MAX / 2)
         return hipErrorInvalidValue;
-    const int grid = (int)((total + 7) / 8 * 8);   // whole rounds of the 8 XCDs
-    hipLaunchKernelGGL((int8_gemm_tile_kernel<C, O>), dim3(grid), dim3(C::kThreads), 0, s, p);
+    const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(C::kThreads);   // rounds of the XCDs
+    if constexpr (C::TM == RingTile::TM)
+        hipLaunchKernelGGL(int8_gemm_ring_kernel<O>, grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((int8_gemm_tile_kernel<C, O>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
 template <class O>
 hipError_t launch_shape(const Int8GemmParams &p, const GemmBlocks &g, hipStream_t s)
 {
-#define SHAPE(C)                                                                            \
-    if (g.tm == C::TM && g.tn == C::TN)                                                     \
-        return launch_tile<C, O>(p, s);
-    SHAPE(BigTile)
-    SHAPE(MidTile)
-    SHAPE(SmallTile)
-    SHAPE(Tile32)
-#undef SHAPE
-    return hipErrorInvalidValue;
+    hipError_t e = hipErrorInvalidValue;
+    int8_shapes([&](auto shape, int) {
+        using C = decltype(shape);
+        if (g.tm == C::TM && g.tn == C::TN)
+            e = launch_tile<C, O>(p, s);
+    });
+    return e;
 }
 
 }  // namespace
 
+// The shape whose rounds of the CUs cost least, the larger on a tie.
 GemmBlocks int8_gemm_blocks(int64_t T, int N, int cus)
 {
-    auto blocks = [&](int tm, int tn) {
-        return ((T + tm - 1) / tm) * (int64_t)((N + tn - 1) / tn);
-    };
-    if (blocks(256, 256) >= cus)
-        return {256, 256, 2};
-    if (blocks(128, 128) >= cus)
-        return {128, 128, 3};
-    if (blocks(64, 64) >= cus)
-        return {64, 64, 3};
-    return {32, 32, 6};
+    GemmBlocks best{};
+    int64_t least = INT64_MAX;
+    int8_shapes([&](auto shape, int cost) {
+        using C = decltype(shape);
+        const int64_t blocks = ((T + C::TM - 1) / C::TM) * (int64_t)((N + C::TN - 1) / C::TN);
+        const int64_t total = (blocks + cus - 1) / cus * cost;
+        if (total <= least) {
+            least = total;
+            best = {C::TM, C::TN, C::S};
+        }
+    });
+    return best;
 }
 
 hipError_t launch_int8_gemm(const Int8GemmParams &p, int out_dtype, int cus, hipStream_t s)

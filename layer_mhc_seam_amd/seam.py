@@ -72,7 +72,7 @@ EXPORTS = ("mhc_seam_create", "mhc_seam_run", "mhc_seam_run_noalloc", "mhc_seam_
            "mhc_seam_plan_for", "mhc_seam_status_string", "mhc_seam_last_error",
            "mhc_seam_copy", "mhc_stream_mix", "mhc_seam_quantize", "mhc_head_reduce",
            "mhc_mxfp8_gemm", "mhc_mxfp8_gemm_blocks", "mhc_block_norm", "mhc_int8_quantize",
-           "mhc_int8_gemm", "mhc_route")
+           "mhc_int8_gemm", "mhc_int8_gemm_blocks", "mhc_route")
 
 _lib = None
 
@@ -118,7 +118,11 @@ def lib():
     L.mhc_int8_gemm.argtypes = [_P, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int32,
                                 ctypes.c_int32, ctypes.c_int32, _P, _P]
     L.mhc_route.argtypes = [ctypes.POINTER(RouteArgs), _P]
-    for name in ("mhc_block_norm", "mhc_int8_quantize", "mhc_int8_gemm", "mhc_route"):
+    L.mhc_int8_gemm_blocks.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.POINTER(ctypes.c_int32),
+                                       ctypes.POINTER(ctypes.c_int32)]
+    for name in ("mhc_block_norm", "mhc_int8_quantize", "mhc_int8_gemm", "mhc_int8_gemm_blocks",
+                 "mhc_route"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("mhc_seam_create", "mhc_seam_run", "mhc_seam_run_noalloc", "mhc_seam_destroy",
                  "mhc_seam_validate",
@@ -525,6 +529,14 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None
     _enqueue(dev, stream, lib().mhc_int8_gemm, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
              b_scales.data_ptr(), _address(bias), T, N, K, DTYPES[out_dtype], out.data_ptr())
     return out
+
+
+def int8_gemm_blocks(T, N, cu_count=256):
+    """Output blocks (TM, TN) int8_gemm launches for T x N on cu_count CUs
+    (host only)."""
+    tm, tn = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().mhc_int8_gemm_blocks(T, N, cu_count, ctypes.byref(tm), ctypes.byref(tn)))
+    return tm.value, tn.value
 
 
 def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, group_top=1,

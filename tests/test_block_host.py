@@ -200,3 +200,26 @@ def test_route_definition():
                        None, 1, 1, 1, True, 1.0)
     assert ids.tolist() == [[1, -1], [-1, -1], [1, -1]]
     assert w[:2].tolist() == [[1.0, 0.0], [0.0, 0.0]] and w[2].isnan().all()
+
+
+# ------------------------------------------- blocks of the int8 product --
+
+def test_int8_gemm_blocks_by_token_count():
+    """The launch's blocks at N = 5120 on 256 CUs over every change of shape
+    (the shapes measured fastest there), and where one is chosen for filling
+    the last round."""
+    want = {1: (16, 32), 16: (16, 32), 17: (32, 32), 32: (32, 32), 33: (32, 64), 96: (32, 64),
+            97: (64, 64), 192: (64, 64), 193: (96, 64), 288: (96, 64), 289: (128, 64), 384: (128, 64),
+            385: (128, 128), 768: (128, 128), 769: (128, 192), 1024: (128, 192), 1280: (128, 256),
+            1536: (128, 256), 2048: (192, 256), 2560: (256, 256), 4160: (192, 256), 6144: (256, 256),
+            16384: (256, 256)}
+    for T, shape in want.items():
+        assert S.int8_gemm_blocks(T, 5120, 256) == shape, T
+    assert S.int8_gemm_blocks(4160, 256, 256) == (96, 64)
+    assert S.int8_gemm_blocks(128, 5120, 128) != S.int8_gemm_blocks(128, 5120, 256)
+
+
+@pytest.mark.parametrize("T,N,cus", [(0, 5120, 256), (4, 0, 256), (4, 5120, 0), (1 << 31, 5120, 256)])
+def test_int8_gemm_blocks_refuses(T, N, cus):
+    with pytest.raises(S.SeamError):
+        S.int8_gemm_blocks(T, N, cus)

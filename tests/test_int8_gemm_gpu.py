@@ -197,3 +197,33 @@ def test_int8_gemm_refusals():
             call()
     with pytest.raises(SeamError):
         int8_gemm(a[:, :24].contiguous(), sa, b[:, :24].contiguous(), sb)
+
+
+# one shape, or more, for each of the launch's blocks: whole and ragged rows
+# and columns, K of one step, of several, and ending inside one
+BLOCK_SHAPES = [(16, 320, 512), (9, 333, 1040), (30, 5120, 256), (27, 5100, 784), (90, 4000, 512),
+                (70, 5099, 1296), (180, 5120, 256), (150, 4001, 528), (250, 5120, 768), (270, 4999, 272),
+                (380, 5120, 512), (300, 5111, 800), (700, 5120, 256), (600, 5117, 400), (1000, 5120, 128),
+                (900, 5101, 656), (1500, 5120, 384), (1300, 5110, 144), (2000, 5120, 256), (1900, 5109, 304),
+                (2500, 5120, 128), (2400, 5103, 272), (5000, 5120, 640), (6100, 5099, 16)]
+
+
+def test_block_shapes_cover_every_block():
+    from layer_mhc_seam_amd.seam import int8_gemm_blocks
+    seen = {}
+    for T, N, _ in BLOCK_SHAPES:
+        seen.setdefault(int8_gemm_blocks(T, N, 256), []).append((T, N))
+    assert len(seen) == 11 and all(len(v) >= 2 for v in seen.values()), seen
+
+
+@pytest.mark.parametrize("T,N,K", BLOCK_SHAPES)
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_int8_gemm_blocks_match_definition(T, N, K, dt):
+    c = operands(T, N, K, seed=T + K)
+    got = gemm(*c, out_dtype=dt)
+    if T * N * K > 1 << 31:
+        g = torch.Generator().manual_seed(K)
+        at = torch.cat([torch.arange(3), torch.arange(T - 3, T), torch.randint(0, T, (200,), generator=g)])
+        check(got[at], c[0][at], c[1][at], *c[2:], dt)
+    else:
+        check(got, *c, dt)
