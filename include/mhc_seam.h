@@ -378,7 +378,8 @@ typedef enum mhc_gate {
  *   codes         int8 [T][H]      optional, with gamma
  *   scales        f32 [T]          exactly with codes; 4-byte aligned
  * Without y both scales must be 1.  dtype is MHC_BF16 or MHC_F16; 1 <= H <=
- * 32768, any H; T * H < 2^40, T < 2^31.  eps in [0, 1], 0 selects 1e-6.
+ * 32768, or 32752 where H is no multiple of 8; T * H < 2^40, T < 2^31.  eps in
+ * [0, 1], 0 selects 1e-6.
  * Outputs overlap no input and no other output, but for residual_out == x.
  * Infinities and NaN go through the arithmetic; int8 rows holding one get
  * codes 0 and scale NaN.  T == 0 does nothing.
@@ -413,7 +414,8 @@ int mhc_block_norm(const mhc_block_norm_args *args, void *stream);
  *   codes = v (127 / a) rounded to the nearest whole number, ties to even
  * (-127 .. 127).  A zero row has codes 0 and the scale of a = 2^-119.  A row
  * holding an infinity or NaN has codes 0 and scale NaN.
- * 1 <= H <= 32768, any H; rows * H < 2^40, rows < 2^31; src and codes 16-byte
+ * 1 <= H <= 32768, or 32752 where H is no multiple of 8; rows * H < 2^40, rows
+ * < 2^31; src and codes 16-byte
  * aligned, scales 4-byte; no overlap.  rows == 0 does nothing.
  */
 int mhc_int8_quantize(const void *src, int32_t dtype, int64_t rows, int32_t H, int8_t *codes,

@@ -26,6 +26,8 @@
 // output written once.  The row's bytes bound it.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "lane_ops.h"
 #include "seam_internal.h"
 
@@ -36,9 +38,7 @@ typedef uint32_t u32;
 typedef uint64_t u64;
 typedef u32 u32x4 __attribute__((ext_vector_type(4)));
 typedef u32 u32x2 __attribute__((ext_vector_type(2)));
-// rows of a width that is no multiple of 8 start at any element
-typedef u32 u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef u32 u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef u32 u32x4_any __attribute__((ext_vector_type(4), aligned(2)));   // at any element
 
 constexpr float kTinyMax = 0x1p-119f;
 
@@ -52,8 +52,34 @@ struct F32 {
     typedef float type;
 };
 
-// 8 consecutive elements of a row as binary32.  `n` of them exist: 8, or
-// fewer in the last chunk of a ragged row (the rest read as zero).
+// Eight consecutive elements of a row, `at` .. at + 7, of which those from
+// `from` to `to` - 1 exist (the rest read as zero).  Chunks end where memory
+// has a multiple of 8 elements, so that whole ones are aligned in every tensor
+// of the row's layout whatever the width; the first and last of a row may be
+// partial.  (At H = 5117 chunks counted from the row's first element, at any
+// alignment, took 201 us where these take 149: T = 16384, bf16, int8.)
+template <bool RAGGED>
+struct Span {
+    int at, from, to;
+    bool inside;   // all eight lie inside the tensor, in this row or its neighbours
+    __device__ __forceinline__ bool whole() const { return to - from == 8; }
+    // some of the eight exist, or, in a row of whole chunks, none
+    __device__ __forceinline__ bool part() const { return RAGGED && !whole(); }
+    __device__ __forceinline__ bool has(int i) const { return i >= from && i < to; }
+};
+
+template <bool RAGGED>
+__device__ __forceinline__ Span<RAGGED> span_of(int64_t row, int64_t rows, int H, int chunk)
+{
+    if (!RAGGED) {
+        const bool whole = 8 * chunk < H;
+        return {8 * chunk, 0, whole ? 8 : 0, whole};
+    }
+    const int at = 8 * chunk - (int)(row * H & 7), from = max(0, -at);
+    const int to = max(from, min(8, H - at));
+    return {at, from, to, to > from && row * H + at + 8 <= rows * H};
+}
+
 template <class E>
 __device__ __forceinline__ void unpack8(const u32x4 &v, float (&f)[8])
 {
@@ -85,22 +111,63 @@ struct Chunk<F32> {
     u32x4 v, w;
 };
 
-template <class E>
-__device__ __forceinline__ void load_chunk(Chunk<E> &c, const void *row, int at, int n)
+// The span's elements of a row of a tensor.  A partial chunk is read whole
+// too, and what belongs to the rows beside it dropped, but for one that ends
+// past the tensor.
+template <class E, bool RAGGED>
+__device__ __forceinline__ void load_chunk(Chunk<E> &c, const void *row, const Span<RAGGED> &s)
 {
     typedef typename E::type T;
-    const T *p = static_cast<const T *>(row) + at;
-    if (n == 8) {
-        c.v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+    const T *p = static_cast<const T *>(row) + s.at;
+    if (s.inside) {
+        c.v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
         if constexpr (sizeof(T) == 4)
-            c.w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p) + 1);
-    } else {
+            c.w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p) + 1);
+    } else if (RAGGED) {
         T e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            e[i] = i < n ? p[i] : (T)0.0f;
+            e[i] = s.has(i) ? p[i] : (T)0.0f;
         __builtin_memcpy(&c, e, sizeof c);
+    } else {
+        __builtin_memset(&c, 0, sizeof c);
     }
+}
+
+// The span's elements of a vector over the channels
+template <class E, bool RAGGED>
+__device__ __forceinline__ void load_channels(Chunk<E> &c, const void *v, const Span<RAGGED> &s)
+{
+    typedef typename E::type T;
+    const T *p = static_cast<const T *>(v) + s.at;
+    if (s.whole()) {
+        c.v = *reinterpret_cast<const u32x4_any *>(p);
+        if constexpr (sizeof(T) == 4)
+            c.w = reinterpret_cast<const u32x4_any *>(p)[1];
+    } else if (RAGGED) {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            e[i] = s.has(i) ? p[i] : (T)0.0f;
+        __builtin_memcpy(&c, e, sizeof c);
+    } else {
+        __builtin_memset(&c, 0, sizeof c);
+    }
+}
+
+// zeros for the elements of c that do not exist
+template <class E, bool RAGGED>
+__device__ __forceinline__ void keep_own(Chunk<E> &c, const Span<RAGGED> &s)
+{
+    typedef typename E::type T;
+    if (!s.part())
+        return;
+    T e[8];
+    __builtin_memcpy(e, &c, sizeof c);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        e[k] = s.has(k) ? e[k] : (T)0.0f;
+    __builtin_memcpy(&c, e, sizeof c);
 }
 
 template <class E>
@@ -118,11 +185,11 @@ __device__ __forceinline__ void unpack(const Chunk<E> &c, float (&f)[8])
 }
 
 // f rounded to E, in memory and back in f
-template <class E>
-__device__ __forceinline__ void store_round(void *row, int at, int n, float (&f)[8])
+template <class E, bool RAGGED>
+__device__ __forceinline__ Chunk<E> store_round(void *row, const Span<RAGGED> &s, float (&f)[8])
 {
     typedef typename E::type T;
-    T *p = static_cast<T *>(row) + at;
+    T *p = static_cast<T *>(row) + s.at;
     Chunk<E> c;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -135,35 +202,66 @@ __device__ __forceinline__ void store_round(void *row, int at, int n, float (&f)
         unpack8<E>(c.v, f);
     }
     if (!row)
-        return;
-    if (n == 8) {
-        __builtin_nontemporal_store(c.v, reinterpret_cast<u32x4_any *>(p));
+        return c;
+    if (s.whole()) {
+        __builtin_nontemporal_store(c.v, reinterpret_cast<u32x4 *>(p));
         if constexpr (sizeof(T) == 4)
-            __builtin_nontemporal_store(c.w, reinterpret_cast<u32x4_any *>(p) + 1);
-    } else {
+            __builtin_nontemporal_store(c.w, reinterpret_cast<u32x4 *>(p) + 1);
+    } else if (RAGGED) {
         T e[8];
         __builtin_memcpy(e, &c, sizeof c);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n)
+            if (s.has(i))
                 p[i] = e[i];
+    }
+    return c;
+}
+
+// Codes of eight values, four to a word: in the low byte of the product's sum
+// with 1.5 x 2^23, which rounds it to a whole number, ties to even.
+template <bool RAGGED>
+__device__ __forceinline__ void store_codes(int8_t *row, const Span<RAGGED> &s, const float (&f)[8],
+                                            float inv)
+{
+    int8_t *p = row + s.at;
+    u32 b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        b[i] = __float_as_uint(f[i] * inv + 0x1.8p23f);
+    u32x2 c;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const u32 lo = __builtin_amdgcn_perm(b[4 * w + 1], b[4 * w], 0x0c0c0400u);
+        const u32 hi = __builtin_amdgcn_perm(b[4 * w + 3], b[4 * w + 2], 0x04000c0cu);
+        c[w] = lo | hi;
+    }
+    if (s.whole()) {
+        __builtin_nontemporal_store(c, reinterpret_cast<u32x2 *>(p));
+    } else if (RAGGED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s.has(i))
+                p[i] = (int8_t)(c[i / 4] >> (8 * (i % 4)));
     }
 }
 
-__device__ __forceinline__ void store_codes(int8_t *p, int n, const float (&f)[8], float inv)
+// Largest magnitudes of a chunk's even and odd elements, joined to `m`: bit
+// patterns without their sign, of which any NaN's is above infinity's.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void join_max(u16x2 &m, const u32x4 &v)
 {
-    u32x2 c = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        c[i / 4] |= ((u32)(int)__builtin_rintf(f[i] * inv) & 0xffu) << (8 * (i % 4));
-    if (n == 8) {
-        __builtin_nontemporal_store(c, reinterpret_cast<u32x2_any *>(p));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                p[i] = (int8_t)(c[i / 4] >> (8 * (i % 4)));
-    }
+    for (int i = 0; i < 4; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu));
+}
+
+// the larger of both as binary32 bits
+template <class E>
+__device__ __forceinline__ u32 max_bits(const u16x2 &m)
+{
+    const unsigned short v = m[0] > m[1] ? m[0] : m[1];
+    return __float_as_uint((float)__builtin_bit_cast(typename E::type, v));
 }
 
 // Workgroup reductions: each wave's value in LDS, one barrier, every thread
@@ -196,9 +294,19 @@ __device__ __forceinline__ u32 block_max(u32 v, u32 *slot, int waves)
     return m;
 }
 
-__device__ __forceinline__ float rstd_of(double sum, int H, float eps)
+// 1 / sqrt(sum / H + eps), rounded once to binary32: the hardware's estimate
+// (24 bits or more) and two steps of Newton's iteration, each of which squares
+// the error, in a tenth of the instructions of a square root and a quotient.
+__device__ __forceinline__ float rstd_of(double sum, double inv_H, float eps)
 {
-    return (float)(1.0 / __builtin_sqrt(sum / (double)H + (double)eps));
+    const double x = __builtin_fma(sum, inv_H, (double)eps);
+    double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const double h = 0.5 * y;
+        y = __builtin_fma(h, __builtin_fma(-x * y, y, 1.0), y);
+    }
+    return x == __builtin_inf() ? 0.0f : (float)y;
 }
 
 // The row's scale and the factor its codes are made with.  amax: the largest
@@ -211,41 +319,74 @@ __device__ __forceinline__ void int8_scale(u32 amax, float &scale, float &inv)
     inv = fine ? 127.0f / a : 0.0f;
 }
 
-constexpr int kMaxWaves = 16;
+constexpr int kMaxWaves = 16, kWaveRows = 4;
 
-// NC chunks of 8 elements a thread, thread t holds chunks t, t + threads, ...
-template <class E, class X, int NC>
-__global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormParams P)
+// Who works on a row: a workgroup, or (WAVE) one of its kWaveRows waves.
+// Thread i holds the row's chunks i, i + stride, ...
+template <bool WAVE>
+struct RowPlace {
+    int64_t row;
+    int index, stride, waves;
+    __device__ __forceinline__ RowPlace()
+    {
+        if (WAVE) {
+            const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            row = (int64_t)blockIdx.x * kWaveRows + wave;
+            index = threadIdx.x & 63;
+            stride = 64;
+            waves = 1;
+        } else {
+            row = blockIdx.x;
+            index = threadIdx.x;
+            stride = blockDim.x;
+            waves = blockDim.x >> 6;
+        }
+    }
+};
+
+template <int NC, bool WAVE>
+constexpr int max_threads()
+{
+    return WAVE ? 64 * kWaveRows : NC == 4 ? 1024 : 512;
+}
+
+template <class E, class X, int NC, bool WAVE, bool RAGGED>
+__global__ __launch_bounds__((max_threads<NC, WAVE>())) void block_norm_kernel(BlockNormParams P)
 {
     __shared__ double sum_y[kMaxWaves], sum_r[kMaxWaves];
     __shared__ u32 max_n[kMaxWaves];
     typedef typename E::type T;
     typedef typename X::type TX;
-    const int64_t t = blockIdx.x;
-    const int H = P.H, waves = blockDim.x >> 6;
-    const TX *x = static_cast<const TX *>(P.x) + t * H;
-    int at[NC], n[NC];
+    const RowPlace<WAVE> me;
+    const int64_t t = me.row;
+    if (WAVE && t >= P.T)
+        return;
+    const int H = P.H, waves = me.waves;
+    Span<RAGGED> span[NC];
     Chunk<X> cx[NC];
     Chunk<E> cy[NC], cg[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        at[i] = 8 * (threadIdx.x + i * blockDim.x);
-        n[i] = max(0, min(8, H - at[i]));
-        load_chunk<X>(cx[i], x, at[i], n[i]);
+        span[i] = span_of<RAGGED>(t, P.T, H, me.index + i * me.stride);
+        load_chunk<X>(cx[i], static_cast<const TX *>(P.x) + t * H, span[i]);
         if (P.y)
-            load_chunk<E>(cy[i], static_cast<const T *>(P.y) + t * H, at[i], n[i]);
+            load_chunk<E>(cy[i], static_cast<const T *>(P.y) + t * H, span[i]);
         if (P.gate_kind == MHC_GATE_ELEMENT)
-            load_chunk<E>(cg[i], static_cast<const T *>(P.gate) + t * H, at[i], n[i]);
+            load_chunk<E>(cg[i], static_cast<const T *>(P.gate) + t * H, span[i]);
     }
     float r[NC][8];
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i) {
+        keep_own<X>(cx[i], span[i]);
         unpack<X>(cx[i], r[i]);
+    }
     if (P.y) {
         float p[NC][8];
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i) {
+            keep_own<E>(cy[i], span[i]);
             unpack<E>(cy[i], p[i]);
+        }
         if (P.gamma_post) {
             double s = 0.0;
 #pragma unroll
@@ -253,12 +394,12 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormParams P)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     s = __builtin_fma((double)p[i][e], (double)p[i][e], s);
-            const float rs = rstd_of(block_sum(s, sum_y, waves), H, P.eps);
+            const float rs = rstd_of(block_sum(s, sum_y, waves), P.inv_H, P.eps);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 Chunk<E> c;
                 float g[8];
-                load_chunk<E>(c, P.gamma_post, at[i], n[i]);
+                load_channels<E>(c, P.gamma_post, span[i]);
                 unpack<E>(c, g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -275,7 +416,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormParams P)
                     unpack<E>(cg[i], g);
                 } else if (P.gate_kind == MHC_GATE_CHANNEL) {
                     Chunk<F32> c;
-                    load_chunk<F32>(c, P.gate, at[i], n[i]);
+                    load_channels<F32>(c, P.gate, span[i]);
                     unpack<F32>(c, g);
                 } else {
 #pragma unroll
@@ -292,8 +433,15 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormParams P)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 r[i][e] = P.residual_scale * r[i][e] + P.branch_scale * p[i][e];
-            store_round<X>(static_cast<TX *>(P.residual_out) + t * H, at[i], n[i], r[i]);
+            store_round<X>(static_cast<TX *>(P.residual_out) + t * H, span[i], r[i]);
         }
+        // what does not exist adds nothing, whatever rstd made of its zeros
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            if (!span[i].whole())
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    r[i][e] = span[i].has(e) ? r[i][e] : 0.0f;
     }
     if (!P.gamma)
         return;
@@ -302,27 +450,27 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormParams P)
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            s = e < n[i] ? __builtin_fma((double)r[i][e], (double)r[i][e], s) : s;
-    const float rs = rstd_of(block_sum(s, sum_r, waves), H, P.eps);
-    u32 amax = 0;
+            s = __builtin_fma((double)r[i][e], (double)r[i][e], s);
+    const float rs = rstd_of(block_sum(s, sum_r, waves), P.inv_H, P.eps);
+    u16x2 amax = {0, 0};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         Chunk<E> c;
         float g[8];
-        load_chunk<E>(c, P.gamma, at[i], n[i]);
+        load_channels<E>(c, P.gamma, span[i]);
         unpack<E>(c, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             r[i][e] = (r[i][e] * rs) * g[e];
-        store_round<E>(P.norm ? static_cast<T *>(P.norm) + t * H : nullptr, at[i], n[i], r[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            amax = max(amax, e < n[i] ? __float_as_uint(r[i][e]) & 0x7fffffffu : 0u);
+        c = store_round<E>(P.norm ? static_cast<T *>(P.norm) + t * H : nullptr, span[i], r[i]);
+        keep_own<E>(c, span[i]);   // a NaN rstd makes NaN of zeros
+        if (RAGGED || span[i].whole())
+            join_max(amax, c.v);
     }
     if (!P.codes)
         return;
     float scale, inv;
-    int8_scale(block_max(amax, max_n, waves), scale, inv);
+    int8_scale(block_max(max_bits<E>(amax), max_n, waves), scale, inv);
     const bool fine = inv != 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -330,106 +478,113 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormParams P)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 r[i][e] = 0.0f;
-        store_codes(P.codes + t * H + at[i], n[i], r[i], inv);
+        store_codes(P.codes + t * H, span[i], r[i], inv);
     }
-    if (threadIdx.x == 0)
+    if (me.index == 0)
         P.scales[t] = scale;
 }
 
-template <class E, int NC>
-__global__ __launch_bounds__(1024) void int8_quantize_kernel(const void *src, int H, int8_t *codes,
-                                                             float *scales)
+template <class E, int NC, bool WAVE, bool RAGGED>
+__global__ __launch_bounds__((max_threads<NC, WAVE>())) void int8_quantize_kernel(
+    const void *src, int64_t rows, int H, int8_t *codes, float *scales)
 {
     __shared__ u32 max_n[kMaxWaves];
     typedef typename E::type T;
-    const int64_t t = blockIdx.x;
-    const int waves = blockDim.x >> 6;
-    const T *row = static_cast<const T *>(src) + t * H;
-    int at[NC], n[NC];
+    const RowPlace<WAVE> me;
+    const int64_t t = me.row;
+    if (WAVE && t >= rows)
+        return;
+    Span<RAGGED> span[NC];
     Chunk<E> c[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        at[i] = 8 * (threadIdx.x + i * blockDim.x);
-        n[i] = max(0, min(8, H - at[i]));
-        load_chunk<E>(c[i], row, at[i], n[i]);
+        span[i] = span_of<RAGGED>(t, rows, H, me.index + i * me.stride);
+        load_chunk<E>(c[i], static_cast<const T *>(src) + t * H, span[i]);
     }
-    float v[NC][8];
-    u32 amax = 0;
+    u16x2 amax = {0, 0};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        unpack<E>(c[i], v[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            amax = max(amax, __float_as_uint(v[i][e]) & 0x7fffffffu);
+        keep_own<E>(c[i], span[i]);
+        join_max(amax, c[i].v);
     }
     float scale, inv;
-    int8_scale(block_max(amax, max_n, waves), scale, inv);
+    int8_scale(block_max(max_bits<E>(amax), max_n, me.waves), scale, inv);
     const bool fine = inv != 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
+        float v[8];
+        unpack<E>(c[i], v);
         if (!fine)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[i][e] = 0.0f;
-        store_codes(codes + t * H + at[i], n[i], v[i], inv);
+                v[e] = 0.0f;
+        store_codes(codes + t * H, span[i], v, inv);
     }
-    if (threadIdx.x == 0)
+    if (me.index == 0)
         scales[t] = scale;
 }
 
-// Chunks a thread holds and threads a row: whole rows in registers, 64 to
-// 1024 threads.
-struct RowShape {
-    int nc, threads;
-};
-
-RowShape row_shape(int H)
+// Rows of up to 128 chunks (H = 1024) take a wave each, four in a workgroup,
+// without barriers (H = 2048 in a wave and in a workgroup: 57.9 and 56.7 us at
+// T = 16384, 4.8 and 3.7 at T = 4).  Longer ones take a workgroup of up to 512
+// threads with two chunks each (H = 5120 with one, two and four a thread: 193,
+// 162 and 167 us at T = 16384), the longest up to 1024 with four.
+template <class F>
+hipError_t with_shape(int64_t rows, int H, F &&f)
 {
-    const int chunks = (H + 7) / 8;
-    const int nc = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
-    return {nc, ((chunks + nc - 1) / nc + 63) / 64 * 64};
+    const bool ragged = H % 8 != 0;
+    const int chunks = ragged ? H / 8 + 2 : H / 8;   // the most a row spans
+    auto go = [&](auto nc, auto wave, dim3 grid, dim3 block) {
+        return ragged ? f(nc, wave, std::true_type{}, grid, block)
+                      : f(nc, wave, std::false_type{}, grid, block);
+    };
+    auto wave = [&](auto nc) {
+        return go(nc, std::true_type{}, dim3((unsigned)((rows + kWaveRows - 1) / kWaveRows)),
+                  dim3(64 * kWaveRows));
+    };
+    auto block = [&](auto nc) {
+        const int threads = ((chunks + nc() - 1) / nc() + 63) / 64 * 64;
+        return go(nc, std::false_type{}, dim3((unsigned)rows), dim3(threads));
+    };
+    if (chunks <= 64)
+        return wave(std::integral_constant<int, 1>{});
+    if (chunks <= 128)
+        return wave(std::integral_constant<int, 2>{});
+    if (chunks <= 1024)
+        return block(std::integral_constant<int, 2>{});
+    return block(std::integral_constant<int, 4>{});
 }
 
 template <class E, class X>
-hipError_t launch_norm(const BlockNormParams &p, int64_t T, hipStream_t s)
+hipError_t launch_norm(const BlockNormParams &p, hipStream_t s)
 {
-    const RowShape g = row_shape(p.H);
-    const dim3 grid((unsigned)T), block(g.threads);
-    if (g.nc == 1)
-        hipLaunchKernelGGL((block_norm_kernel<E, X, 1>), grid, block, 0, s, p);
-    else if (g.nc == 2)
-        hipLaunchKernelGGL((block_norm_kernel<E, X, 2>), grid, block, 0, s, p);
-    else
-        hipLaunchKernelGGL((block_norm_kernel<E, X, 4>), grid, block, 0, s, p);
-    return hipGetLastError();
+    return with_shape(p.T, p.H, [&](auto nc, auto wave, auto ragged, dim3 grid, dim3 block) {
+        hipLaunchKernelGGL((block_norm_kernel<E, X, nc(), wave(), ragged()>), grid, block, 0, s, p);
+        return hipGetLastError();
+    });
 }
 
 template <class E>
 hipError_t launch_quant(const void *src, int64_t rows, int H, int8_t *codes, float *scales,
                         hipStream_t s)
 {
-    const RowShape g = row_shape(H);
-    const dim3 grid((unsigned)rows), block(g.threads);
-    if (g.nc == 1)
-        hipLaunchKernelGGL((int8_quantize_kernel<E, 1>), grid, block, 0, s, src, H, codes, scales);
-    else if (g.nc == 2)
-        hipLaunchKernelGGL((int8_quantize_kernel<E, 2>), grid, block, 0, s, src, H, codes, scales);
-    else
-        hipLaunchKernelGGL((int8_quantize_kernel<E, 4>), grid, block, 0, s, src, H, codes, scales);
-    return hipGetLastError();
+    return with_shape(rows, H, [&](auto nc, auto wave, auto ragged, dim3 grid, dim3 block) {
+        hipLaunchKernelGGL((int8_quantize_kernel<E, nc(), wave(), ragged()>), grid, block, 0, s,
+                           src, rows, H, codes, scales);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace
 
-hipError_t launch_block_norm(const BlockNormParams &p, int64_t T, int dtype, int x_dtype,
-                             hipStream_t s)
+hipError_t launch_block_norm(const BlockNormParams &p, int dtype, int x_dtype, hipStream_t s)
 {
-    if (T == 0)
+    if (p.T == 0)
         return hipSuccess;
     const bool wide = x_dtype == MHC_F32;
     if (dtype == MHC_BF16)
-        return wide ? launch_norm<Bf16, F32>(p, T, s) : launch_norm<Bf16, Bf16>(p, T, s);
-    return wide ? launch_norm<F16, F32>(p, T, s) : launch_norm<F16, F16>(p, T, s);
+        return wide ? launch_norm<Bf16, F32>(p, s) : launch_norm<Bf16, Bf16>(p, s);
+    return wide ? launch_norm<F16, F32>(p, s) : launch_norm<F16, F16>(p, s);
 }
 
 hipError_t launch_int8_quantize(const void *src, int dtype, int64_t rows, int H, int8_t *codes,

@@ -2,6 +2,7 @@
 // norm, the int8 quantiser and product, and expert routing.  Argument rules
 // only; each call is checked in full before any device call is made.
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -15,7 +16,9 @@ using mhc::hip_fail;
 namespace {
 
 constexpr int64_t kMaxElements = int64_t(1) << 40;
-constexpr int kMaxWidth = 32768;     // a row fits a workgroup's registers
+// Widths whose rows fit a workgroup's registers: 4096 chunks of 8, of which a
+// row that starts and ends inside one spans two more than it fills
+bool width_fits(int64_t H) { return H >= 1 && H <= (H % 8 ? 32752 : 32768); }
 constexpr int kMaxDepth = 131056;    // 128 * 128 * K < 2^31
 constexpr int kMaxRoute = 1024, kMaxGroups = 64, kMaxChosen = 64;
 
@@ -52,12 +55,19 @@ bool clash(std::initializer_list<Range> outs, std::initializer_list<Range> ins)
     return false;
 }
 
+// Compute units of the current device, asked for once per device
 hipError_t compute_units(int *cus)
 {
+    static std::atomic<int> known[64];
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
-    if (e == hipSuccess)
-        e = hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess)
+        return e;
+    if (dev >= 0 && dev < 64 && (*cus = known[dev].load(std::memory_order_relaxed)) > 0)
+        return hipSuccess;
+    e = hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e == hipSuccess && dev >= 0 && dev < 64)
+        known[dev].store(*cus, std::memory_order_relaxed);
     return e;
 }
 
@@ -70,9 +80,10 @@ int mhc_block_norm(const mhc_block_norm_args *a, void *stream)
     if (!a)
         return fail(MHC_SEAM_INVALID_ARG, "args is NULL");
     const int64_t T = a->T, H = a->H;
-    if (T < 0 || T > INT32_MAX || H < 1 || H > kMaxWidth || T * H >= kMaxElements)
+    if (T < 0 || T > INT32_MAX || !width_fits(H) || T * H >= kMaxElements)
         return fail(MHC_SEAM_INVALID_ARG,
-                    "block norm needs 0 <= T < 2^31, 1 <= H <= %d and T*H < 2^40", kMaxWidth);
+                    "block norm needs 0 <= T < 2^31, 1 <= H <= 32768 (32752 if no multiple of 8) "
+                    "and T*H < 2^40");
     if (!half_type(a->dtype) || (a->x_dtype != a->dtype && a->x_dtype != MHC_F32))
         return fail(MHC_SEAM_INVALID_ARG,
                     "block norm: dtype is bf16 or f16, x_dtype the same or f32");
@@ -123,7 +134,9 @@ int mhc_block_norm(const mhc_block_norm_args *a, void *stream)
         (!in_place && overlap(r, x)))
         return fail(MHC_SEAM_INVALID_ARG, "an output overlaps an input or another output");
     mhc::BlockNormParams p;
+    p.T = T;
     p.H = a->H;
+    p.inv_H = 1.0 / (double)a->H;
     p.gate_kind = a->gate_kind;
     p.eps = a->eps > 0.0f ? a->eps : 1e-6f;
     p.residual_scale = a->residual_scale;
@@ -137,7 +150,7 @@ int mhc_block_norm(const mhc_block_norm_args *a, void *stream)
     p.norm = a->norm;
     p.codes = a->codes;
     p.scales = a->scales;
-    hipError_t err = mhc::launch_block_norm(p, T, a->dtype, a->x_dtype,
+    hipError_t err = mhc::launch_block_norm(p, a->dtype, a->x_dtype,
                                             reinterpret_cast<hipStream_t>(stream));
     if (err != hipSuccess)
         return hip_fail(err, "block norm launch");
@@ -147,10 +160,10 @@ int mhc_block_norm(const mhc_block_norm_args *a, void *stream)
 int mhc_int8_quantize(const void *src, int32_t dtype, int64_t rows, int32_t H, int8_t *codes,
                       float *scales, void *stream)
 {
-    if (rows < 0 || rows > INT32_MAX || H < 1 || H > kMaxWidth || rows * H >= kMaxElements)
+    if (rows < 0 || rows > INT32_MAX || !width_fits(H) || rows * H >= kMaxElements)
         return fail(MHC_SEAM_INVALID_ARG,
-                    "int8 quantize needs 0 <= rows < 2^31, 1 <= H <= %d and rows*H < 2^40",
-                    kMaxWidth);
+                    "int8 quantize needs 0 <= rows < 2^31, 1 <= H <= 32768 (32752 if no multiple "
+                    "of 8) and rows*H < 2^40");
     if (!half_type(dtype))
         return fail(MHC_SEAM_INVALID_ARG, "int8 quantize takes bf16 or f16");
     if (rows == 0)

@@ -92,9 +92,11 @@ hipError_t launch_head_reduce(const uint16_t *x, const float *w, int64_t T, int 
 // The one-stream block norm (block_kernels.hip); P.y, gamma_post, gate,
 // gamma, norm and codes are null where the call has none
 struct BlockNormParams {
+    int64_t T;
     int H;
     int gate_kind;            // mhc_gate
     float eps, residual_scale, branch_scale;
+    double inv_H;             // 1 / H
     const void *x;
     const void *y;
     const void *gamma_post;
@@ -105,8 +107,7 @@ struct BlockNormParams {
     int8_t *codes;
     float *scales;
 };
-hipError_t launch_block_norm(const BlockNormParams &p, int64_t T, int dtype, int x_dtype,
-                             hipStream_t s);
+hipError_t launch_block_norm(const BlockNormParams &p, int dtype, int x_dtype, hipStream_t s);
 hipError_t launch_int8_quantize(const void *src, int dtype, int64_t rows, int H, int8_t *codes,
                                 float *scales, hipStream_t s);
 

@@ -453,23 +453,22 @@ def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_sc
         else:
             kind = GATE_TOKEN
             _need("gate", gate, torch.float32, (T, 1), dev)
-    want = {}
-    if y is not None:
-        want["residual_out"] = (x_dt, shape)
-    if gamma is not None and norm:
-        want["norm"] = (dt, shape)
-    if int8:
-        want["codes"] = (torch.int8, shape)
-        want["scales"] = (torch.float32, (T,))
     o = dict(out) if out else {}
-    for name in o:
-        if name not in want:
-            raise ValueError(f"this call writes no {name}")
-    for name, (dtype, size) in want.items():
+    writes = 0
+    for name, wanted, dtype in (("residual_out", y is not None, x_dt),
+                                ("norm", norm and gamma is not None, dt),
+                                ("codes", int8, torch.int8), ("scales", int8, torch.float32)):
+        if not wanted:
+            continue
+        writes += 1
         if name in o:
-            _need(name, o[name], dtype, size, dev)
+            _need(name, o[name], dtype, (T,) if name == "scales" else shape, dev)
+        elif name == "scales":
+            o[name] = torch.empty((T,), dtype=dtype, device=dev)
         else:
-            o[name] = torch.empty(size, dtype=dtype, device=dev)
+            o[name] = torch.empty_like(x, dtype=dtype)   # x is dense
+    if len(o) != writes:
+        raise ValueError(f"out holds more than this call writes: {', '.join(out)}")
     a = BlockNormArgs(T, H, codes[dt], codes[x_dt], kind, eps, residual_scale, branch_scale, 0,
                       x.data_ptr(), _address(y), _address(gamma_post), _address(gate),
                       _address(gamma), _address(o.get("residual_out")), _address(o.get("norm")),
@@ -491,7 +490,7 @@ def int8_quantize(src, *, out=None, stream=None):
     dev = src.device
     _need("src", src, src.dtype, (rows, H), dev)
     if out is None:
-        codes = torch.empty((rows, H), dtype=torch.int8, device=dev)
+        codes = torch.empty_like(src, dtype=torch.int8)
         scales = torch.empty((rows,), dtype=torch.float32, device=dev)
     else:
         codes, scales = out

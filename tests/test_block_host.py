@@ -41,7 +41,7 @@ def test_struct_layouts():
 
 
 @pytest.mark.parametrize("kw", [
-    dict(T=-1), dict(T=1 << 31), dict(H=0), dict(H=32769), dict(T=1 << 30, H=1024),
+    dict(T=-1), dict(T=1 << 31), dict(H=0), dict(H=32769), dict(H=32753), dict(H=32767), dict(T=1 << 30, H=1024),
     dict(dtype=2), dict(dtype=-1), dict(x_dtype=1), dict(x_dtype=3), dict(gate_kind=4),
     dict(gate_kind=-1), dict(eps=-1e-6), dict(eps=math.nan), dict(eps=2.0),
     dict(residual_scale=math.inf), dict(branch_scale=math.nan), dict(reserved=1),
@@ -68,7 +68,7 @@ def test_block_norm_without_a_branch_takes_no_branch_arguments():
 
 
 @pytest.mark.parametrize("rows,H,dtype,off", [(-1, 64, 0, 0), (1 << 31, 64, 0, 0), (4, 0, 0, 0),
-                                              (4, 40000, 0, 0), (4, 64, 2, 0), (4, 64, 0, 8),
+                                              (4, 40000, 0, 0), (4, 32759, 0, 0), (4, 64, 2, 0), (4, 64, 0, 8),
                                               (1 << 30, 1024, 0, 0)])
 def test_int8_quantize_refuses(rows, H, dtype, off):
     assert S.lib().mhc_int8_quantize(slot(0) + off, dtype, rows, H, slot(1), slot(2), None) == 1

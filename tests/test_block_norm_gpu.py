@@ -82,7 +82,8 @@ def near_formula(o, c, rs, bs, eps=1e-6):
 
 # widths: below a vector, ragged on either side of a wave's and of every
 # change of the launch's shape, the package's own, the widest
-WIDTHS = [1, 7, 8, 64, 100, 509, 512, 1027, 2040, 2048, 2056, 5120, 7168, 8185, 8192, 8200, 32768]
+WIDTHS = [1, 7, 8, 64, 100, 505, 509, 512, 1017, 1027, 2040, 2041, 2042, 2048, 2056, 5120, 7168, 8185, 8192, 8200,
+          20481, 32751, 32768]
 
 
 @pytest.mark.parametrize("H", WIDTHS)
