@@ -383,10 +383,17 @@ def _need(name, t, dtype, shape, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _new(rows, cols, dtype, device):
+    """An uninitialised dense [rows, cols] (the cheapest way to one: 1.3 us
+    against torch.empty's 1.7)."""
+    import torch
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _enqueue(device, stream, call, *args):
     """call(*args, stream) on `device`: its current stream unless one of its
-    streams is given.  (The handle is asked for as it is: a Stream object
-    around it takes 2 us, as long as a small kernel's whole launch.)"""
+    streams is given.  (Stream handle and device are asked for as they are: a
+    Stream object takes 2 us, as long as a small kernel's whole launch.)"""
     import torch
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(device.index)
@@ -394,7 +401,7 @@ def _enqueue(device, stream, call, *args):
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         status = call(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -522,7 +529,7 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None
     if bias is not None:
         _need("bias", bias, torch.float32, (N,), dev)
     if out is None:
-        out = torch.empty((T, N), dtype=dt, device=dev)
+        out = _new(T, N, dt, dev)
     else:
         _need("out", out, dt, (T, N), dev)
     _enqueue(dev, stream, lib().mhc_int8_gemm, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
@@ -560,8 +567,8 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
     if bias is not None:
         _need("bias", bias, torch.float32, (E,), dev)
     if out is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = _new(T, k, torch.float32, dev)
+        ids = _new(T, k, torch.int32, dev)
     else:
         weights, ids = out
         _need("weights", weights, torch.float32, (T, k), dev)
