@@ -331,12 +331,12 @@ struct RowPlace {
     {
         if (WAVE) {
             const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-            row = (int64_t)blockIdx.x * kWaveRows + wave;
+            row = block_id() * kWaveRows + wave;
             index = threadIdx.x & 63;
             stride = 64;
             waves = 1;
         } else {
-            row = blockIdx.x;
+            row = block_id();
             index = threadIdx.x;
             stride = blockDim.x;
             waves = blockDim.x >> 6;
@@ -359,7 +359,7 @@ __global__ __launch_bounds__((max_threads<NC, WAVE>())) void block_norm_kernel(B
     typedef typename X::type TX;
     const RowPlace<WAVE> me;
     const int64_t t = me.row;
-    if (WAVE && t >= P.T)
+    if (t >= P.T)
         return;
     const int H = P.H, waves = me.waves;
     Span<RAGGED> span[NC];
@@ -492,7 +492,7 @@ __global__ __launch_bounds__((max_threads<NC, WAVE>())) void int8_quantize_kerne
     typedef typename E::type T;
     const RowPlace<WAVE> me;
     const int64_t t = me.row;
-    if (WAVE && t >= rows)
+    if (t >= rows)
         return;
     Span<RAGGED> span[NC];
     Chunk<E> c[NC];
@@ -539,12 +539,12 @@ hipError_t with_shape(int64_t rows, int H, F &&f)
                       : f(nc, wave, std::false_type{}, grid, block);
     };
     auto wave = [&](auto nc) {
-        return go(nc, std::true_type{}, dim3((unsigned)((rows + kWaveRows - 1) / kWaveRows)),
+        return go(nc, std::true_type{}, grid_of((rows + kWaveRows - 1) / kWaveRows),
                   dim3(64 * kWaveRows));
     };
     auto block = [&](auto nc) {
         const int threads = ((chunks + nc() - 1) / nc() + 63) / 64 * 64;
-        return go(nc, std::false_type{}, dim3((unsigned)rows), dim3(threads));
+        return go(nc, std::false_type{}, grid_of(rows), dim3(threads));
     };
     if (chunks <= 64)
         return wave(std::integral_constant<int, 1>{});

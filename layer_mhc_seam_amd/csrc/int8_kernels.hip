@@ -158,7 +158,7 @@ __device__ __forceinline__ bool block_of(int w, int mb, int nb, int &m, int &n)
 {
     const int total = mb * nb, per_xcd = (total + 7) / 8;
     const int L = (w % 8) * per_xcd + w / 8;
-    if (L >= total)
+    if (w >= 8 * per_xcd || L >= total)
         return false;
     const int group = L / (kGroupRows * nb), first = group * kGroupRows;
     const int gm = min(mb - first, kGroupRows), in = L % (kGroupRows * nb);
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_gemm_tile_kernel(Int8Gemm
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int T = P.T, N = P.N;
     int mi, ni;
-    if (!block_of(blockIdx.x, (T + C::TM - 1) / C::TM, (N + C::TN - 1) / C::TN, mi, ni))
+    if (!block_of((int)block_id(), (T - 1) / C::TM + 1, (N - 1) / C::TN + 1, mi, ni))
         return;
     const int m_blk = mi * C::TM, n_blk = ni * C::TN;
     const int wm = (wave / (C::TN / C::WN)) * C::WM, wn = (wave % (C::TN / C::WN)) * C::WN;
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(RingTile::kThreads, 1) void int8_gemm_ring_kernel(I
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int mi, ni;
-    if (!block_of(blockIdx.x, (P.T + C::TM - 1) / C::TM, (P.N + C::TN - 1) / C::TN, mi, ni))
+    if (!block_of((int)block_id(), (P.T - 1) / C::TM + 1, (P.N - 1) / C::TN + 1, mi, ni))
         return;
     const int m_blk = mi * C::TM, n_blk = ni * C::TN;
     const int wm = (wave / (C::TN / C::WN)) * C::WM, wn = (wave % (C::TN / C::WN)) * C::WN;
@@ -492,10 +492,10 @@ void int8_shapes(F &&f)
 template <class C, class O>
 hipError_t launch_tile(const Int8GemmParams &p, hipStream_t s)
 {
-    const int64_t total = (int64_t)((p.T + C::TM - 1) / C::TM) * ((p.N + C::TN - 1) / C::TN);
+    const int64_t total = (int64_t)((p.T - 1) / C::TM + 1) * ((p.N - 1) / C::TN + 1);
     if (total > INT32_MAX / 2)
         return hipErrorInvalidValue;
-    const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(C::kThreads);   // rounds of the XCDs
+    const dim3 grid = grid_of((total + 7) / 8 * 8), block(C::kThreads);   // rounds of the XCDs
     if constexpr (C::TM == RingTile::TM)
         hipLaunchKernelGGL(int8_gemm_ring_kernel<O>, grid, block, 0, s, p);
     else

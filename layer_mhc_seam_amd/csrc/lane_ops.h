@@ -1,5 +1,5 @@
-// lane_ops.h -- wave-wide and workgroup-wide reductions, and a rounding
-// barrier, shared by the block operators' kernels.
+// lane_ops.h -- what the block operators' kernels share: launches of any
+// number of workgroups, wave-wide reductions, a rounding barrier.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -7,6 +7,20 @@
 
 namespace mhc {
 namespace {
+
+// Grid of that many workgroups and, past 2^21, up to 2^21 - 1 more: a grid's
+// threads along x stay below 2^32 whatever the workgroup.  Workgroups past the
+// number asked for have nothing to do.
+inline dim3 grid_of(int64_t blocks)
+{
+    const int64_t x = blocks < (int64_t(1) << 21) ? blocks : int64_t(1) << 21;
+    return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+
+__device__ __forceinline__ int64_t block_id()
+{
+    return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
 
 // v as its own rounding left it: keeps the compiler from folding the product
 // or sum that made it into the conversion to fp16 that follows (one rounding

@@ -169,10 +169,12 @@ __device__ __forceinline__ void route_token(const RouteParams &P, int64_t t, int
 }
 
 template <class T, int EPL>
-__global__ __launch_bounds__(64) void route_kernel(RouteParams P)
+__global__ __launch_bounds__(64) void route_kernel(RouteParams P, int64_t tokens)
 {
     __shared__ double keys[EPL * 64];
-    route_token<T, EPL>(P, blockIdx.x, threadIdx.x, keys);
+    const int64_t t = block_id();
+    if (t < tokens)
+        route_token<T, EPL>(P, t, threadIdx.x, keys);
 }
 
 // ----------------------------------------------------- four tokens a wave --
@@ -288,7 +290,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
     __shared__ double keys_of[kRowWaves][EPL / 4 * 64];
     const int lane = threadIdx.x & 63, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t first_token = ((int64_t)blockIdx.x * kRowWaves + wave) * 4;
+    const int64_t first_token = (block_id() * kRowWaves + wave) * 4;
     if (first_token >= tokens)
         return;
     const int64_t own = first_token + (lane >> 4);
@@ -548,7 +550,7 @@ hipError_t launch(const RouteParams &p, int64_t tokens, hipStream_t s)
     if (rows_fit(p)) {
         const int lanes = 16 / p.groups, size = p.E / p.groups, per = (size + lanes - 1) / lanes;
         const int a_block = 4 * kRowWaves;
-        const dim3 grid((unsigned)((tokens + a_block - 1) / a_block)), block(64 * kRowWaves);
+        const dim3 grid = grid_of((tokens + a_block - 1) / a_block), block(64 * kRowWaves);
         if (per <= 4)
             hipLaunchKernelGGL((route_rows_kernel<T, 4>), grid, block, 0, s, p, tokens);
         else if (per <= 8)
@@ -559,17 +561,17 @@ hipError_t launch(const RouteParams &p, int64_t tokens, hipStream_t s)
             hipLaunchKernelGGL((route_rows_kernel<T, 32>), grid, block, 0, s, p, tokens);
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)tokens), block(64);
+    const dim3 grid = grid_of(tokens), block(64);
     if (p.E <= 64)
-        hipLaunchKernelGGL((route_kernel<T, 1>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((route_kernel<T, 1>), grid, block, 0, s, p, tokens);
     else if (p.E <= 128)
-        hipLaunchKernelGGL((route_kernel<T, 2>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((route_kernel<T, 2>), grid, block, 0, s, p, tokens);
     else if (p.E <= 256)
-        hipLaunchKernelGGL((route_kernel<T, 4>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((route_kernel<T, 4>), grid, block, 0, s, p, tokens);
     else if (p.E <= 512)
-        hipLaunchKernelGGL((route_kernel<T, 8>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((route_kernel<T, 8>), grid, block, 0, s, p, tokens);
     else
-        hipLaunchKernelGGL((route_kernel<T, 16>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((route_kernel<T, 16>), grid, block, 0, s, p, tokens);
     return hipGetLastError();
 }
 

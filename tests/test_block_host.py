@@ -223,3 +223,38 @@ def test_int8_gemm_blocks_by_token_count():
 def test_int8_gemm_blocks_refuses(T, N, cus):
     with pytest.raises(S.SeamError):
         S.int8_gemm_blocks(T, N, cus)
+
+
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    """The launch is made with the tensors' device current and on its stream,
+    and with no switch where it is current already."""
+    import contextlib
+    seen = []
+
+    @contextlib.contextmanager
+    def switched(device):
+        seen.append(("to", device.index))
+        yield
+        seen.append(("back", device.index))
+
+    def call(a, handle):
+        seen.append((a, handle))
+        return S.OK
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", switched)
+    S._enqueue(torch.device("cuda", 1), None, call, "x")
+    assert seen == [("to", 1), ("x", 101), ("back", 1)]
+    seen.clear()
+    S._enqueue(torch.device("cuda", 0), None, call, "x")
+    assert seen == [("x", 100)]
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 7
+
+    seen.clear()
+    S._enqueue(torch.device("cuda", 1), Stream, call, "x")
+    assert seen == [("to", 1), ("x", 7), ("back", 1)]
+    with pytest.raises(ValueError, match="stream is on"):
+        S._enqueue(torch.device("cuda", 0), Stream, call, "x")

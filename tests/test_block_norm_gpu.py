@@ -309,3 +309,21 @@ def test_results_do_not_depend_on_the_width_of_the_launch():
         assert not codes[:, 500:].any()
         same(scales, want[1])
     assert np.isfinite(float(want[1]))
+
+
+def test_more_rows_than_a_grid_line_holds():
+    """Rows whose threads number past 2^32: the last ones too."""
+    T, H = 70_000_001, 8
+    x = torch.zeros(T, H, dtype=BF16, device="cuda")
+    at = [0, 1, 8388607, 8388608, 33554431, 33554432, 67108863, 67108864, 67108865, T - 2, T - 1]
+    v = torch.randn(len(at), H).to(BF16)
+    x[at] = v.cuda()
+    codes, scales = seam().int8_quantize(x)
+    want = ref.quantize(v)
+    same(codes[at], want[0])
+    same(scales[at], want[1])
+    del codes, scales
+    g = torch.ones(H, dtype=BF16, device="cuda")
+    o = seam().block_norm(x, g)
+    _, n = ref.block_norm(v, g.cpu(), None, None, None, 1.0, 1.0)
+    same(o["norm"][at], n)

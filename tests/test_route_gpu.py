@@ -251,3 +251,13 @@ def test_route_rows_beside_each_other(T):
     for E, k in ((64, 8), (63, 16)):
         check(l[:, :E].contiguous(), k, "sigmoid", 0.1 * torch.randn(E, generator=g))
         check(l[:, :E].contiguous(), k, "softmax")
+
+
+def test_route_more_tokens_than_a_grid_line_holds():
+    from layer_mhc_seam_amd.seam import route
+    T = 270_000_003
+    l = torch.zeros(T, 2, dtype=torch.float16, device="cuda")
+    at = torch.tensor([0, 1, 33554431, 33554432, 268435455, 268435456, T - 2, T - 1], device="cuda")
+    l[at, 1] = 1.0
+    w, ids = route(l, 1)
+    assert int(ids.sum()) == len(at) and (ids[at] == 1).all() and bool((w == 1).all())
