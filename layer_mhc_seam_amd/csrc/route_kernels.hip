@@ -314,6 +314,15 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
     }
     top = row_max(top);
     odd |= !(top < inf && top > -inf);
+    // a softmax that is not renormalized needs the sum over all experts
+    double all = 1.0;
+    if (!P.sigmoid && !P.renorm) {
+        all = 0.0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            all += exp((double)v[j] - (double)top);
+        all = row_sum(all);
+    }
     const bool by_group = P.groups > P.keep;
     u32 key[EPL];
     u32 need = 0;
@@ -498,9 +507,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
     odd |= sure == 0;
     int id = (int)(kIndexMask - (chosen & kIndexMask)), rank = c;
     const double l = (double)(float)row[min(id, P.E - 1)];
-    double w = P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top);
+    double w = P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / all;
     if (__ballot(close)) {
-        odd |= close && P.bias && !P.sigmoid;   // needs the sum of all scores
+        odd |= close && P.bias && !P.sigmoid && P.renorm;   // would need `all`
         double mine = l;
         if (P.bias)
             mine = w + (double)P.bias[min(id, P.E - 1)];
@@ -536,12 +545,12 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
 }
 
 // Four tokens a wave where a lane's experts, the chosen and the groups fit a
-// row of 16 lanes, and weights need no sum over all experts' scores.
+// row of 16 lanes.
 bool rows_fit(const RouteParams &p)
 {
     const bool groups = p.groups == 1 || p.groups == 2 || p.groups == 4 || p.groups == 8 ||
                         p.groups == 16;
-    return groups && p.E <= 512 && p.k <= 16 && (p.sigmoid || p.renorm);
+    return groups && p.E <= 512 && p.k <= 16;
 }
 
 template <class T>
