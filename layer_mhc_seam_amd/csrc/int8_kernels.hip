@@ -14,7 +14,17 @@
 // 4 (l / 16) + e of column l % 16.  Both operands are read with the same
 // assignment of K to lanes and bytes, and a sum of integers does not depend
 // on its order, so the assignment itself is free: here the 16-byte pieces
-// l / 16 and l / 16 + 4 of a 128-wide step.
+// l / 16 + 4 q of a step.
+//
+// What bounds it, at N = K = 5120 (inputs beyond the L2, within the 256 MB
+// behind it): T = 1 the weights' bytes, 6.8 us, 2 of them the launch (3.9 TB/s;
+// a bare read of them takes 5.4); T = 384 the rows' way from L2 into LDS, 17.3
+// us (983 KB a CU, 17 TB/s in all; larger wave tiles with half the LDS reads
+// took as long); T = 16384 345 us, 2.49 PFLOP/s, of which the products alone
+// take 235 (the clock falls under them: 4.0 PFLOP/s is the instruction's own
+// rate over Gaussian codes, 4.7 over zeros), the loads alone 295.
+// Operands straight into registers, without LDS: 9 us at T = 1, since 64-byte
+// pieces of rows come at two thirds of the rate of 128-byte ones.
 #include <hip/hip_runtime.h>
 
 #include "lane_ops.h"
@@ -53,12 +63,11 @@ __device__ __forceinline__ void wait_vm()
     __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
 
-// The workgroup barrier alone, without a fence that would wait for the
-// stages' loads in flight: a wave's LDS reads have completed before it comes
-// here, since its products have used them.
+// The workgroup barrier with this wave's LDS reads complete, and without a
+// fence, which would wait for the stages' loads in flight too.
 __device__ __forceinline__ void block_barrier()
 {
-    asm volatile("s_barrier" ::: "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // ------------------------------------------------------------ tiled kernel --
@@ -439,8 +448,7 @@ __global__ __launch_bounds__(RingTile::kThreads, 1) void int8_gemm_ring_kernel(I
         read(a1, b1, slot_a, slot_b, 1);
         multiply(a0, b0);
         wait_vm<kHalf>();   // the next step's rows are in LDS, the A rows after them may not be
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and this step's in registers
-        block_barrier();
+        block_barrier();    // and this step's in every wave's registers
         if (ragged && ks + 1 == steps - 1)
             zero_tail<C>(lds + next_b * kSlot, pieces);
         fetch_b(ks + 2, slot_a);
