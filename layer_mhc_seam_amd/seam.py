@@ -358,7 +358,9 @@ def mxfp8_gemm(a, a_scales, b, b_scales, *, out=None, stream=None):
 # ------------------------------------------------ one-stream block boundary --
 #
 # Unlike the calls above, these run on the device their tensors are on,
-# whichever is current, and on that device's current stream.
+# whichever is current, and on that device's current stream.  A `stream` of
+# their own has to come after what made the tensors, as ever; it gets the
+# outputs' memory too.
 
 @functools.lru_cache(maxsize=None)
 def _types():
@@ -390,17 +392,12 @@ def _new(rows, cols, dtype, device):
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
-def _enqueue(device, stream, call, *args):
-    """call(*args, stream) on `device`: its current stream unless one of its
-    streams is given.  (Stream handle and device are asked for as they are: a
-    Stream object takes 2 us, as long as a small kernel's whole launch.)"""
+def _enqueue(device, call, *args):
+    """call(*args, stream) on `device` and its current stream.  (Stream handle
+    and device are asked for as they are: a Stream object takes 2 us, as long
+    as a small kernel's whole launch.)"""
     import torch
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    else:
-        handle = stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(device.index)
     if torch._C._cuda_getDevice() == device.index:
         status = call(*args, handle)
     else:
@@ -408,6 +405,30 @@ def _enqueue(device, stream, call, *args):
             status = call(*args, handle)
     if status != OK:
         _check(status)
+
+
+def _on_stream(stream, op, *args, **kw):
+    """op(*args, **kw) with `stream` current, so that its outputs are allocated
+    there.  The memory of the tensors given is not handed on by the allocator
+    before the stream is done with them."""
+    import torch
+    if stream.device != args[0].device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {args[0].device}")
+    with torch.cuda.stream(stream):
+        result = op(*args, **kw)
+    out = kw.get("out")
+    for t in (*args, *kw.values(), *(out.values() if isinstance(out, dict) else
+                                     out if isinstance(out, tuple) else ())):
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    return result
+
+
+def _fits(bits):
+    """Sizes, or'ed together, that the library takes: ctypes would cut longer
+    ones to their low 32 bits."""
+    if bits >> 31 not in (0, -1):
+        raise ValueError("a size is out of range")
 
 
 def _address(t):
@@ -429,9 +450,14 @@ def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_sc
     Returns a dict of outputs (allocated unless given in `out`; residual_out
     may be x)."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, block_norm, x, gamma, y, gamma_post=gamma_post, gate=gate,
+                          residual_scale=residual_scale, branch_scale=branch_scale, eps=eps,
+                          norm=norm, int8=int8, out=out)
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
     T, H = shape = x.shape
+    _fits(H)
     dev = x.device
     codes = _types()[1]
     dt = gamma.dtype if gamma is not None else None if y is None else y.dtype
@@ -480,7 +506,7 @@ def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_sc
                       x.data_ptr(), _address(y), _address(gamma_post), _address(gate),
                       _address(gamma), _address(o.get("residual_out")), _address(o.get("norm")),
                       _address(o.get("codes")), _address(o.get("scales")))
-    _enqueue(dev, stream, lib().mhc_block_norm, ctypes.byref(a))
+    _enqueue(dev, lib().mhc_block_norm, ctypes.byref(a))
     return o
 
 
@@ -489,11 +515,14 @@ def int8_quantize(src, *, out=None, stream=None):
     device tensor, one scale a row: the operands of int8_gemm.  out: the pair
     to write to."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, int8_quantize, src, out=out)
     if src.dim() != 2:
         raise ValueError("src must be [rows, H]")
     if src.dtype is not torch.bfloat16 and src.dtype is not torch.float16:
         raise ValueError(f"src must be bfloat16 or float16, got {src.dtype}")
     rows, H = src.shape
+    _fits(H)
     dev = src.device
     _need("src", src, src.dtype, (rows, H), dev)
     if out is None:
@@ -503,7 +532,7 @@ def int8_quantize(src, *, out=None, stream=None):
         codes, scales = out
         _need("codes", codes, torch.int8, (rows, H), dev)
         _need("scales", scales, torch.float32, (rows,), dev)
-    _enqueue(dev, stream, lib().mhc_int8_quantize, src.data_ptr(), _types()[1][src.dtype],
+    _enqueue(dev, lib().mhc_int8_quantize, src.data_ptr(), _types()[1][src.dtype],
              rows, H, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
@@ -514,10 +543,14 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None
     a int8 [T, K], a_scales f32 [T] (block_norm's or int8_quantize's), b int8
     [N, K], b_scales and bias f32 [N]; out_dtype bf16, f16 or f32."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, int8_gemm, a, a_scales, b, b_scales, bias, out_dtype=out_dtype,
+                          out=out)
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError("a must be [T, K] and b [N, K]")
     T, K = a.shape
     N = b.shape[0]
+    _fits(N | K)
     dev = a.device
     if out_dtype not in DTYPES:
         raise ValueError(f"out_dtype must be one of {', '.join(DTYPES)}")
@@ -532,7 +565,7 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None
         out = _new(T, N, dt, dev)
     else:
         _need("out", out, dt, (T, N), dev)
-    _enqueue(dev, stream, lib().mhc_int8_gemm, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
+    _enqueue(dev, lib().mhc_int8_gemm, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
              b_scales.data_ptr(), _address(bias), T, N, K, DTYPES[out_dtype], out.data_ptr())
     return out
 
@@ -540,6 +573,7 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None
 def int8_gemm_blocks(T, N, cu_count=256):
     """Output blocks (TM, TN) int8_gemm launches for T x N on cu_count CUs
     (host only)."""
+    _fits(N | cu_count)
     tm, tn = ctypes.c_int32(), ctypes.c_int32()
     _check(lib().mhc_int8_gemm_blocks(T, N, cu_count, ctypes.byref(tm), ctypes.byref(tn)))
     return tm.value, tn.value
@@ -555,6 +589,10 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
     weight 0 where masks (-inf) leave fewer than k experts.  out: the pair to
     write to."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, route, logits, k, scoring=scoring, bias=bias, groups=groups,
+                          topk_groups=topk_groups, group_top=group_top, renormalize=renormalize,
+                          scale=scale, out=out)
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     if logits.dtype not in _types()[1]:
@@ -562,6 +600,7 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
     if scoring not in SCORINGS:
         raise ValueError(f"scoring must be one of {', '.join(SCORINGS)}")
     T, E = logits.shape
+    _fits(E | k | groups | topk_groups | group_top)
     dev = logits.device
     _need("logits", logits, logits.dtype, (T, E), dev)
     if bias is not None:
@@ -576,5 +615,5 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
     a = RouteArgs(T, E, k, _types()[1][logits.dtype], SCORINGS[scoring], groups, topk_groups,
                   group_top, int(bool(renormalize)), scale, 0, logits.data_ptr(), _address(bias),
                   weights.data_ptr(), ids.data_ptr())
-    _enqueue(dev, stream, lib().mhc_route, ctypes.byref(a))
+    _enqueue(dev, lib().mhc_route, ctypes.byref(a))
     return weights, ids

@@ -103,6 +103,35 @@ def test_two_streams_at_once():
             assert torch.equal(o["l"], want[i]["l"]) and torch.equal(o["r"][1], want[i]["r"][1])
 
 
+def test_outputs_made_on_a_stream_of_their_own():
+    """A call on another stream than the current one: its outputs' memory is
+    that stream's (what the current one frees and fills meanwhile is not
+    theirs), and inputs dropped at once stay until it is done with them."""
+    from layer_mhc_seam_amd import seam as S
+    g = torch.Generator().manual_seed(10)
+    T, H = 2048, 5120
+    x = torch.randn(T, H, generator=g).bfloat16().cuda()
+    gamma = torch.ones(H).bfloat16().cuda()
+    w, ws = weights(H, H, g)
+    w, ws = w.cuda(), ws.cuda()
+    want = S.int8_gemm(*S.int8_quantize(x), w, ws)
+    want_norm = S.block_norm(x, gamma)["norm"]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        mine = x.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        n = S.block_norm(mine, gamma, stream=s)["norm"]
+        codes, scales = S.int8_quantize(mine, stream=s)
+        del mine
+        got = S.int8_gemm(codes, scales, w, ws, stream=s)
+        del codes, scales
+        for _ in range(4):   # takes what was freed on the current stream, if anything
+            torch.full((T, H), 7.0, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(n, want_norm)
+
+
 def test_seam_norm_through_the_int8_product():
     """The four-stream seam's norm is an operand like any other."""
     from layer_mhc_seam_amd import seam as S

@@ -244,17 +244,52 @@ def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
     monkeypatch.setattr(torch.cuda, "device", switched)
-    S._enqueue(torch.device("cuda", 1), None, call, "x")
+    S._enqueue(torch.device("cuda", 1), call, "x")
     assert seen == [("to", 1), ("x", 101), ("back", 1)]
     seen.clear()
-    S._enqueue(torch.device("cuda", 0), None, call, "x")
+    S._enqueue(torch.device("cuda", 0), call, "x")
     assert seen == [("x", 100)]
 
-    class Stream:
-        device, cuda_stream = torch.device("cuda", 1), 7
 
+def test_calls_on_a_stream(monkeypatch):
+    """With the stream current, on its device only; what the call was given is
+    recorded as used there."""
+    import contextlib
+    seen = []
+
+    @contextlib.contextmanager
+    def current(stream):
+        seen.append("in")
+        yield
+        seen.append("out")
+
+    class Stream:
+        device = torch.device("cpu")
+
+    def op(*args, **kw):
+        seen.append((args, kw))
+        return 5
+
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append(t.item()))
+    x, b, o1, o2 = (torch.tensor(i) for i in range(4))
+    assert S._on_stream(Stream, op, x, 8, bias=b, gate=None, out=(o1, o2)) == 5
+    assert seen[0] == "in" and seen[1][0][1] == 8 and seen[2:] == ["out", 0, 1, 2, 3]
     seen.clear()
-    S._enqueue(torch.device("cuda", 1), Stream, call, "x")
-    assert seen == [("to", 1), ("x", 7), ("back", 1)]
+    S._on_stream(Stream, op, x, None, out={"a": o1})
+    assert seen[2:] == ["out", 0, 2]
+    Stream.device = torch.device("cuda", 0)
     with pytest.raises(ValueError, match="stream is on"):
-        S._enqueue(torch.device("cuda", 0), Stream, call, "x")
+        S._on_stream(Stream, op, x)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """ctypes would cut them to ones that the library takes."""
+    S._fits(1 | 2 ** 31 - 1)
+    for bad in (2 ** 31, 64 | 2 ** 32 + 64, 8 | -(2 ** 32) + 8):
+        with pytest.raises(ValueError, match="out of range"):
+            S._fits(bad)
+    with pytest.raises(ValueError, match="out of range"):
+        S.route(torch.zeros(2, 8), 2 ** 32 + 2)
+    with pytest.raises(ValueError, match="out of range"):
+        S.int8_gemm_blocks(16, 2 ** 32 + 16)
