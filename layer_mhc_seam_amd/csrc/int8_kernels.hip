@@ -19,8 +19,11 @@
 // What bounds it, at N = K = 5120 (inputs beyond the L2, within the 256 MB
 // behind it): T = 1 the weights' bytes, 6.8 us, 2 of them the launch (3.9 TB/s;
 // a bare read of them takes 5.4); T = 384 the rows' way from L2 into LDS, 17.3
-// us (983 KB a CU, 17 TB/s in all; larger wave tiles with half the LDS reads
-// took as long); T = 16384 345 us, 2.49 PFLOP/s, of which the products alone
+// us (983 KB a CU, 17 TB/s in all; these loads alone, without products, take
+// 12.8; larger wave tiles with half the LDS reads, LDS reads moved between the
+// products, steps begun elsewhere in each block took as long), and 21.5 at K =
+// 5136, whose rows do not start on 128 bytes, so that a piece touches three
+// lines for two; T = 16384 345 us, 2.49 PFLOP/s, of which the products alone
 // take 235 (the clock falls under them: 4.0 PFLOP/s is the instruction's own
 // rate over Gaussian codes, 4.7 over zeros), the loads alone 295.
 // Operands straight into registers, without LDS: 9 us at T = 1, since 64-byte
