@@ -201,9 +201,9 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams P, int64_t tokens
 // neighbours among the k largest are nearer than that, or the k-th and the
 // next (then the choice goes on, up to 16, to a gap that is wide enough), the
 // binary64 keys of those chosen are compared.  A row whose groups are too
-// close on both sides of the border, that has too few experts left, or holds
-// infinities or NaN goes through route_token afterwards, one in 4000 at 256
-// experts in 8 groups.  Without a bias the order is the logits' own: bf16 and
+// close on both sides of the border, that has some experts left but too few, or
+// holds infinities or NaN goes through route_token afterwards, one in 4000 at
+// 256 experts in 8 groups.  Without a bias the order is the logits' own: bf16 and
 // fp16 logits fit a place whole, and no row is too close to call (equal
 // logits are common there and are ties).
 //
@@ -317,6 +317,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
         odd |= __builtin_isunordered(v[j], v[j + 1]);
     }
     top = row_max(top);
+    // every expert masked, as in a padded batch's rows
+    const bool none = top == -inf && (__ballot(odd) >> (lane & 48) & 0xffff) == 0;
     odd |= !(top < inf && top > -inf);
     // a softmax that is not renormalized needs the sum over all experts
     double share = 1.0;
@@ -541,9 +543,14 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
         P.weights[t * P.k + rank] = (float)(w * (double)P.scale);
         P.ids[t * P.k + rank] = id;
     }
+    const u64 lanes_none = __ballot(none);
+    if (none && own < tokens && c < P.k) {
+        P.weights[t * P.k + c] = 0.0f * P.scale;
+        P.ids[t * P.k + c] = -1;
+    }
     for (int r = 0; r < 4; ++r) {
         const int64_t tt = first_token + r;
-        if ((lanes_odd >> (16 * r) & 0xffff) && tt < tokens)
+        if (((lanes_odd & ~lanes_none) >> (16 * r) & 0xffff) && tt < tokens)
             route_token<T, EPL / 4>(P, tt, lane, keys_of[wave]);
     }
 }

@@ -253,6 +253,28 @@ def test_route_rows_beside_each_other(T):
         check(l[:, :E].contiguous(), k, "softmax")
 
 
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm,scale", [(True, 1.0), (False, -2.5)])
+def test_route_rows_of_masked_experts_only(dt, scoring, renorm, scale):
+    """A padded batch's rows, with every expert masked, at every place of
+    four, beside rows with one expert left, and one that holds a NaN too."""
+    g = torch.Generator().manual_seed(12)
+    for T, E, k, groups, keep, top in ((37, 160, 6, 1, 1, 1), (41, 64, 16, 8, 4, 2), (7, 512, 3, 16, 2, 1)):
+        l = torch.randn(T, E, generator=g).to(dt)
+        l[torch.rand(T, generator=g) < 0.6] = -math.inf
+        l[3] = -math.inf
+        l[4] = -math.inf
+        l[4, E - 1] = 1.0
+        l[5] = -math.inf
+        l[5, E // 2] = math.nan
+        for b in (None, 0.1 * torch.randn(E, generator=g)):
+            w, ids = check(l, k, scoring, b, groups, keep, top, renorm, scale)
+            assert (ids[3] == -1).all() and (w[3] == 0).all()
+            assert ids[4].tolist() == [E - 1] + [-1] * (k - 1)
+            assert (ids[5] == -1).all() and w[5].isnan().all()
+
+
 def test_route_more_tokens_than_a_grid_line_holds():
     from layer_mhc_seam_amd.seam import route
     T = 270_000_003
