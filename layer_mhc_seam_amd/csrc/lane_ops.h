@@ -31,7 +31,7 @@ __device__ __forceinline__ float rounded(float v)
     return v;
 }
 
-// Value of lane (l + N) mod 16 of the lane's row of 16
+// Value of lane (l - N) mod 16 of the lane's row of 16
 template <int N>
 __device__ __forceinline__ uint32_t row_ror(uint32_t v)
 {

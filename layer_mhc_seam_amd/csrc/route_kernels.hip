@@ -27,8 +27,10 @@
 //
 // Reading the logits would take 2.8 us at T = 16384, E = 256, the launch 2.
 // What bounds it is instructions: with a wave a token in binary64 34 us, four
-// tokens a wave 12.5 (980 vector instructions a wave, 6.5 us of them issued
-// back to back; the rest is one wave's latency, 5.4 us in all at T = 1).
+// tokens a wave 12.6 (about 1000 vector instructions a wave, 6.5 us of them
+// issued back to back; the rest is one wave's latency, 5.6 us in all at T = 1).
+// A row that has to be done again in binary64 costs 3 us by itself: with those
+// whose groups were close done so, T = 4160 took 9.6 where it now takes 7.6.
 #include <hip/hip_runtime.h>
 
 #include "lane_ops.h"
@@ -184,11 +186,12 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams P, int64_t tokens
 // ----------------------------------------------------- four tokens a wave --
 //
 // The choice from binary32 keys wherever they prove it right.  A row of 16
-// lanes takes a token, up to EPL experts a lane; with G groups 16 / G lanes
-// hold each group.  A key is a whole number: the score's place between the
-// row's lowest and highest, below 2^22, above the expert's index (inverted, so
-// that the lowest index of a place is the largest number); place 0 is no
-// expert.  One maximum then gives place and index at once.
+// lanes takes a token, up to EPL experts a lane; each group has a power of two
+// of the lanes, as many as there are for all.  A key is a whole number: the
+// score's place between the row's lowest and highest, below 2^22, above the
+// expert's index (inverted, so that the lowest index of a place is the largest
+// number); place 0 is no expert.  One maximum then gives place and index at
+// once.
 //
 // Each lane sorts out its four largest keys (76 minima and maxima for 16);
 // its two largest give the groups' sums, and the choice takes the largest
@@ -200,12 +203,14 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams P, int64_t tokens
 // apart than `need` places are in the order of the binary64 ones.  Where
 // neighbours among the k largest are nearer than that, or the k-th and the
 // next (then the choice goes on, up to 16, to a gap that is wide enough), the
-// binary64 keys of those chosen are compared.  A row whose groups are too
-// close on both sides of the border, that has some experts left but too few, or
-// holds infinities or NaN goes through route_token afterwards, one in 4000 at
-// 256 experts in 8 groups.  Without a bias the order is the logits' own: bf16 and
-// fp16 logits fit a place whole, and no row is too close to call (equal
-// logits are common there and are ties).
+// binary64 keys of those chosen are compared; where groups are too close on
+// both sides of the border (one row in 4000 at 256 experts in 8 groups), their
+// binary64 sums, if the experts that make them are certain.  What is left (it
+// is not, some experts are but fewer than asked for, infinities, NaN) goes
+// through route_token afterwards, which keeps its wave for 3 us.  Without a
+// bias the order is the logits' own: bf16 and fp16 logits fit a place whole,
+// and no row is too close to call (equal logits are common there and are
+// ties).
 //
 // Weights are binary64 of the k chosen.
 constexpr int kIndexBits = 9;
@@ -287,6 +292,12 @@ __device__ __forceinline__ void four_largest(const u32 (&key)[EPL], u32 (&h)[4])
     }
 }
 
+// Lanes of a row that hold each of up to 16 groups: a power of two
+__host__ __device__ __forceinline__ int lanes_of(int groups)
+{
+    return groups == 1 ? 16 : groups == 2 ? 8 : groups <= 4 ? 4 : groups <= 8 ? 2 : 1;
+}
+
 template <class T, int EPL>
 __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams P, int64_t tokens)
 {
@@ -300,9 +311,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
     const int64_t own = first_token + (lane >> 4);
     const int64_t t = own < tokens ? own : tokens - 1;
     const T *row = static_cast<const T *>(P.logits) + t * P.E;
-    const int lanes = 16 / P.groups, size = P.E / P.groups;   // of a group
+    const int lanes = lanes_of(P.groups), size = P.E / P.groups;   // of a group
+    const bool idle = c / lanes >= P.groups;
     const int per = (size + lanes - 1) / lanes, sub = (c % lanes) * per;
-    const int start = c / lanes * size + sub, count = max(0, min(per, size - sub));
+    const int start = idle ? 0 : c / lanes * size + sub;
+    const int count = idle ? 0 : max(0, min(per, size - sub));
     const float inf = __builtin_inff();
     float v[EPL], b[EPL];
     load_row<T, EPL>(row + start, count, -inf, v);
@@ -320,8 +333,18 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
     // every expert masked, as in a padded batch's rows
     const bool none = top == -inf && (__ballot(odd) >> (lane & 48) & 0xffff) == 0;
     odd |= !(top < inf && top > -inf);
-    // a softmax that is not renormalized needs the sum over all experts
+    // The factor of exp(l - top): 1 over the sum of all experts' in a softmax,
+    // or 1 where it cancels, in renormalized weights and in keys without a
+    // bias.  Keys with one, of a renormalized softmax, need it only where
+    // experts or groups are close.
     double share = 1.0;
+    auto share_of_all = [&] {
+        double all = 0.0;
+#pragma unroll 4
+        for (int j = 0; j < count; ++j)
+            all += exp((double)(float)row[start + j] - (double)top);
+        return 1.0 / row_sum(all);
+    };
     if (!P.sigmoid && !P.renorm) {
         double all = 0.0;
 #pragma unroll
@@ -329,6 +352,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
             all += exp((double)v[j] - (double)top);
         share = 1.0 / row_sum(all);
     }
+    double key_share = share;
+    bool known = P.sigmoid || !P.renorm || !P.bias;
+    auto score = [&](double l, double part) {
+        return P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) * part;
+    };
     const bool by_group = P.groups > P.keep;
     u32 key[EPL];
     u32 need = 0;
@@ -437,31 +465,68 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
             join(row_swap<kXor4>(first), row_swap<kXor4>(second));
         u32 mine = first;
         if (P.top == 2) {
-            odd |= second <= kIndexMask;
+            odd |= !idle && second <= kIndexMask;
             mine = (first >> kIndexBits) + (second >> kIndexBits);
         }
         // groups that come before this lane's
         int before = 0;
+#define OTHER_GROUPS(COUNT)                                                                 \
+    if (lanes == 1) {                                                                       \
+        COUNT(1) COUNT(3) COUNT(5) COUNT(7) COUNT(9) COUNT(11) COUNT(13) COUNT(15)          \
+    }                                                                                       \
+    if (lanes <= 2) {                                                                       \
+        COUNT(2) COUNT(6) COUNT(10) COUNT(14)                                               \
+    }                                                                                       \
+    if (lanes <= 4) {                                                                       \
+        COUNT(4) COUNT(12)                                                                  \
+    }                                                                                       \
+    COUNT(8)
 #define COUNT(N) before += row_ror<N>(mine) > mine;
-        if (lanes == 1) {
-            COUNT(1) COUNT(3) COUNT(5) COUNT(7) COUNT(9) COUNT(11) COUNT(13) COUNT(15)
-        }
-        if (lanes <= 2) {
-            COUNT(2) COUNT(6) COUNT(10) COUNT(14)
-        }
-        if (lanes <= 4) {
-            COUNT(4) COUNT(12)
-        }
-        COUNT(8)
+        OTHER_GROUPS(COUNT)
 #undef COUNT
-        const bool open = before < P.keep;
+        bool open = !idle && before < P.keep;
         const int shift = P.top == 2 ? 0 : kIndexBits;
         const u32 last = ~row_max(open ? ~(mine >> shift) : 0u);
         const u32 next = row_max(open ? 0u : mine >> shift);
-        odd |= next > 0 && last - next < need * (u32)P.top;
         // equal sums: more groups open than there should be
-        odd |= need > 0 &&
-               __builtin_popcountll(__ballot(open) >> (lane & 48) & 0xffff) != P.keep * lanes;
+        const bool near = (next > 0 && last - next < need * (u32)P.top) ||
+                          (need > 0 && __builtin_popcountll(__ballot(open) >> (lane & 48) &
+                                                            0xffff) != P.keep * lanes);
+        if (__ballot(near)) {
+            // the sums in binary64, where the keys tell for certain of what
+            u32 third = h[0] < second ? h[0] : h[1] < second ? h[1] : h[2];
+            if (lanes >= 2)
+                third = max(third, row_swap<kXor1>(third));
+            if (lanes >= 4)
+                third = max(third, row_swap<kXor2>(third));
+            if (lanes >= 8)
+                third = max(third, row_swap<kXor4>(third));
+            const u32 least = P.top == 2 ? second : first, rest = P.top == 2 ? third : second;
+            odd |= near && !idle && (least >> kIndexBits) - (rest >> kIndexBits) < need;
+            if (!known) {
+                key_share = share_of_all();
+                known = true;
+            }
+            double sum = idle ? -(double)inf : 0.0;
+#pragma unroll 1
+            for (int i = 0; i < P.top; ++i) {
+                const u32 k = i == 0 ? first : second;
+                const int e = min((int)(kIndexMask - (k & kIndexMask)), P.E - 1);
+                const double l = (double)(float)row[e];
+                const double s = P.bias || P.top == 2 ? score(l, key_share) : l;
+                sum += k <= kIndexMask ? -(double)inf : P.bias ? s + (double)P.bias[e] : s;
+            }
+            before = 0;
+#define COUNT(N)                                                                            \
+    {                                                                                       \
+        const double other = row_ror<N>(sum);                                               \
+        before += other > sum || (other == sum && ((c - N) & 15) < c);                      \
+    }
+            OTHER_GROUPS(COUNT)
+#undef COUNT
+            open = near ? !idle && before < P.keep : open;
+        }
+#undef OTHER_GROUPS
         if (!open) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
@@ -513,12 +578,15 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
     odd |= sure == 0;
     int id = (int)(kIndexMask - (chosen & kIndexMask)), rank = c;
     const double l = (double)(float)row[min(id, P.E - 1)];
-    double w = P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) * share;
+    double w = score(l, share);
     if (__ballot(close)) {
-        odd |= close && P.bias && !P.sigmoid && P.renorm;   // would need `share`
         double mine = l;
-        if (P.bias)
-            mine = w + (double)P.bias[min(id, P.E - 1)];
+        if (P.bias) {
+            if (!known)
+                key_share = share_of_all();
+            const double part = P.sigmoid || !P.renorm ? 1.0 : key_share;   // of w
+            mine = w * part + (double)P.bias[min(id, P.E - 1)];
+        }
         if (c >= sure)
             mine = -__builtin_inf();
         int before = 0;
@@ -555,20 +623,14 @@ __global__ __launch_bounds__(64 * kRowWaves) void route_rows_kernel(RouteParams 
     }
 }
 
-// Four tokens a wave where a lane's experts, the chosen and the groups fit a
-// row of 16 lanes.
-bool rows_fit(const RouteParams &p)
-{
-    const bool groups = p.groups == 1 || p.groups == 2 || p.groups == 4 || p.groups == 8 ||
-                        p.groups == 16;
-    return groups && p.E <= 512 && p.k <= 16;
-}
-
 template <class T>
 hipError_t launch(const RouteParams &p, int64_t tokens, hipStream_t s)
 {
-    if (rows_fit(p)) {
-        const int lanes = 16 / p.groups, size = p.E / p.groups, per = (size + lanes - 1) / lanes;
+    // Four tokens a wave where groups, experts and the chosen fit a row of 16
+    // lanes and 32 experts each
+    const int lanes = p.groups <= 16 ? lanes_of(p.groups) : 1, size = p.E / p.groups;
+    const int per = (size + lanes - 1) / lanes;
+    if (p.groups <= 16 && per <= 32 && p.k <= 16) {
         const int a_block = 4 * kRowWaves;
         const dim3 grid = grid_of((tokens + a_block - 1) / a_block), block(64 * kRowWaves);
         if (per <= 4)

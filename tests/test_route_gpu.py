@@ -275,6 +275,41 @@ def test_route_rows_of_masked_experts_only(dt, scoring, renorm, scale):
             assert (ids[5] == -1).all() and w[5].isnan().all()
 
 
+@pytest.mark.parametrize("groups", [3, 5, 6, 7, 9, 11, 12, 13, 15])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_groups_that_do_not_divide_a_row(groups, scoring):
+    """Groups with lanes of a row to spare: few experts and many, masked
+    groups, equal and near sums, one group kept and all but one."""
+    g = torch.Generator().manual_seed(groups)
+    for size in (2, 5, 17, 31):
+        E = groups * size
+        l = torch.randn(24, E, generator=g)
+        l[::5] = l[::5].masked_fill(torch.rand(5, E, generator=g) < 0.7, -math.inf)
+        l[1, :E - size] = -math.inf
+        l[2] = l[2, :size].repeat(groups)
+        l[3] = (l[2].view(torch.int32) + torch.randint(-2, 3, (E,), generator=g).int()).view(torch.float32)
+        l[4] = -math.inf
+        for dt in DTYPES:
+            for bias in (None, 0.1 * torch.randn(E, generator=g)):
+                for keep, top in ((1, 1), (1, 2), (groups - 1, 1), (groups - 1, 2), (groups, 1)):
+                    check(l.to(dt), min(2, size), scoring, bias, groups, keep, top)
+
+
+@pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_route_borders_in_every_wave(scoring, renorm):
+    """Close experts and close groups at every place of four, with a bias
+    that is not the same for all."""
+    g = torch.Generator().manual_seed(21)
+    E, groups = 128, 8
+    b = 0.1 * torch.randn(E // groups, generator=g).repeat(groups)
+    for step in (0.0, 2e-7, 1e-6, 1e-4):
+        l = torch.randn(50, 1, E // groups, generator=g) + step * torch.randn(50, groups, 1, generator=g)
+        l = l.expand(50, groups, E // groups).reshape(50, E)
+        for top in (1, 2):
+            check(l, 6, scoring, b, groups, 3, top, renorm)
+        check(l, 6, scoring, b, 1, 1, 1, renorm)
+
+
 def test_route_more_tokens_than_a_grid_line_holds():
     from layer_mhc_seam_amd.seam import route
     T = 270_000_003
