@@ -370,14 +370,15 @@ def _types():
     return types, {t: DTYPES[n] for n, t in types.items()}
 
 
-def _need(name, t, dtype, shape, device):
+def _need(name, t, dtype, shape, index):
     """t is a dense tensor of that type and shape on that device."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda \
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 \
             and t.is_contiguous():
         return
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a tensor on {device}" if device.type == "cuda"
-                         else f"{name} must be a device tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on cuda:{index}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -392,16 +393,16 @@ def _new(rows, cols, dtype, device):
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
-def _enqueue(device, call, *args):
-    """call(*args, stream) on `device` and its current stream.  (Stream handle
-    and device are asked for as they are: a Stream object takes 2 us, as long
-    as a small kernel's whole launch.)"""
+def _enqueue(index, call, *args):
+    """call(*args, stream) on that device and its current stream.  (Stream
+    handle and device are asked for as they are: a Stream object takes 2 us,
+    as long as a small kernel's whole launch.)"""
     import torch
-    handle = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch._C._cuda_getDevice() == device.index:
+    handle = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
         status = call(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = call(*args, handle)
     if status != OK:
         _check(status)
@@ -458,7 +459,7 @@ def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_sc
         raise ValueError("x must be [T, H]")
     T, H = shape = x.shape
     _fits(H)
-    dev = x.device
+    index = x.get_device()
     codes = _types()[1]
     dt = gamma.dtype if gamma is not None else None if y is None else y.dtype
     if dt is None:
@@ -466,47 +467,66 @@ def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_sc
     if dt is not torch.bfloat16 and dt is not torch.float16:
         raise ValueError(f"gamma and y must be bfloat16 or float16, got {dt}")
     x_dt = torch.float32 if x.dtype is torch.float32 else dt
-    _need("x", x, x_dt, shape, dev)
-    if gamma is not None:
-        _need("gamma", gamma, dt, (H,), dev)
-    elif int8:
-        raise ValueError("int8 codes are those of the norm: give gamma")
+    _need("x", x, x_dt, shape, index)
+    y_at = post_at = gate_at = gamma_at = r_at = n_at = c_at = s_at = None
+    o = {} if out is None else dict(out)
+    given, writes = len(o), 0
     if y is not None:
-        _need("y", y, dt, shape, dev)
+        _need("y", y, dt, shape, index)
+        y_at = y.data_ptr()
+        r = o.get("residual_out")
+        if r is None:
+            r = o["residual_out"] = torch.empty_like(x)   # x is dense
+        else:
+            _need("residual_out", r, x_dt, shape, index)
+            writes += 1
+        r_at = r.data_ptr()
+    if gamma is not None:
+        _need("gamma", gamma, dt, (H,), index)
+        gamma_at = gamma.data_ptr()
+        if norm:
+            n = o.get("norm")
+            if n is None:
+                n = o["norm"] = torch.empty_like(x, dtype=dt)
+            else:
+                _need("norm", n, dt, shape, index)
+                writes += 1
+            n_at = n.data_ptr()
+    if int8:
+        if gamma is None:
+            raise ValueError("int8 codes are those of the norm: give gamma")
+        c, s = o.get("codes"), o.get("scales")
+        if c is None:
+            c = o["codes"] = torch.empty_like(x, dtype=torch.int8)
+        else:
+            _need("codes", c, torch.int8, shape, index)
+            writes += 1
+        if s is None:
+            s = o["scales"] = torch.empty((T,), dtype=torch.float32, device=x.device)
+        else:
+            _need("scales", s, torch.float32, (T,), index)
+            writes += 1
+        c_at, s_at = c.data_ptr(), s.data_ptr()
+    if writes != given:
+        raise ValueError(f"out holds more than this call writes: {', '.join(out)}")
     if gamma_post is not None:
-        _need("gamma_post", gamma_post, dt, (H,), dev)
+        _need("gamma_post", gamma_post, dt, (H,), index)
+        post_at = gamma_post.data_ptr()
     kind = GATE_NONE
     if gate is not None:
         if gate.dtype is not torch.float32:
             kind = GATE_ELEMENT
-            _need("gate", gate, dt, shape, dev)
+            _need("gate", gate, dt, shape, index)
         elif gate.dim() == 1:
             kind = GATE_CHANNEL
-            _need("gate", gate, torch.float32, (H,), dev)
+            _need("gate", gate, torch.float32, (H,), index)
         else:
             kind = GATE_TOKEN
-            _need("gate", gate, torch.float32, (T, 1), dev)
-    o = dict(out) if out else {}
-    writes = 0
-    for name, wanted, dtype in (("residual_out", y is not None, x_dt),
-                                ("norm", norm and gamma is not None, dt),
-                                ("codes", int8, torch.int8), ("scales", int8, torch.float32)):
-        if not wanted:
-            continue
-        writes += 1
-        if name in o:
-            _need(name, o[name], dtype, (T,) if name == "scales" else shape, dev)
-        elif name == "scales":
-            o[name] = torch.empty((T,), dtype=dtype, device=dev)
-        else:
-            o[name] = torch.empty_like(x, dtype=dtype)   # x is dense
-    if len(o) != writes:
-        raise ValueError(f"out holds more than this call writes: {', '.join(out)}")
+            _need("gate", gate, torch.float32, (T, 1), index)
+        gate_at = gate.data_ptr()
     a = BlockNormArgs(T, H, codes[dt], codes[x_dt], kind, eps, residual_scale, branch_scale, 0,
-                      x.data_ptr(), _address(y), _address(gamma_post), _address(gate),
-                      _address(gamma), _address(o.get("residual_out")), _address(o.get("norm")),
-                      _address(o.get("codes")), _address(o.get("scales")))
-    _enqueue(dev, lib().mhc_block_norm, ctypes.byref(a))
+                      x.data_ptr(), y_at, post_at, gate_at, gamma_at, r_at, n_at, c_at, s_at)
+    _enqueue(index, lib().mhc_block_norm, ctypes.byref(a))
     return o
 
 
@@ -523,16 +543,16 @@ def int8_quantize(src, *, out=None, stream=None):
         raise ValueError(f"src must be bfloat16 or float16, got {src.dtype}")
     rows, H = src.shape
     _fits(H)
-    dev = src.device
-    _need("src", src, src.dtype, (rows, H), dev)
+    index = src.get_device()
+    _need("src", src, src.dtype, (rows, H), index)
     if out is None:
         codes = torch.empty_like(src, dtype=torch.int8)
-        scales = torch.empty((rows,), dtype=torch.float32, device=dev)
+        scales = torch.empty((rows,), dtype=torch.float32, device=src.device)
     else:
         codes, scales = out
-        _need("codes", codes, torch.int8, (rows, H), dev)
-        _need("scales", scales, torch.float32, (rows,), dev)
-    _enqueue(dev, lib().mhc_int8_quantize, src.data_ptr(), _types()[1][src.dtype],
+        _need("codes", codes, torch.int8, (rows, H), index)
+        _need("scales", scales, torch.float32, (rows,), index)
+    _enqueue(index, lib().mhc_int8_quantize, src.data_ptr(), _types()[1][src.dtype],
              rows, H, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
@@ -551,21 +571,21 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None
     T, K = a.shape
     N = b.shape[0]
     _fits(N | K)
-    dev = a.device
+    index = a.get_device()
     if out_dtype not in DTYPES:
         raise ValueError(f"out_dtype must be one of {', '.join(DTYPES)}")
     dt = _types()[0][out_dtype]
-    _need("a", a, torch.int8, (T, K), dev)
-    _need("a_scales", a_scales, torch.float32, (T,), dev)
-    _need("b", b, torch.int8, (N, K), dev)
-    _need("b_scales", b_scales, torch.float32, (N,), dev)
+    _need("a", a, torch.int8, (T, K), index)
+    _need("a_scales", a_scales, torch.float32, (T,), index)
+    _need("b", b, torch.int8, (N, K), index)
+    _need("b_scales", b_scales, torch.float32, (N,), index)
     if bias is not None:
-        _need("bias", bias, torch.float32, (N,), dev)
+        _need("bias", bias, torch.float32, (N,), index)
     if out is None:
-        out = _new(T, N, dt, dev)
+        out = _new(T, N, dt, a.device)
     else:
-        _need("out", out, dt, (T, N), dev)
-    _enqueue(dev, lib().mhc_int8_gemm, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
+        _need("out", out, dt, (T, N), index)
+    _enqueue(index, lib().mhc_int8_gemm, a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
              b_scales.data_ptr(), _address(bias), T, N, K, DTYPES[out_dtype], out.data_ptr())
     return out
 
@@ -601,19 +621,20 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
         raise ValueError(f"scoring must be one of {', '.join(SCORINGS)}")
     T, E = logits.shape
     _fits(E | k | groups | topk_groups | group_top)
-    dev = logits.device
-    _need("logits", logits, logits.dtype, (T, E), dev)
+    index = logits.get_device()
+    _need("logits", logits, logits.dtype, (T, E), index)
     if bias is not None:
-        _need("bias", bias, torch.float32, (E,), dev)
+        _need("bias", bias, torch.float32, (E,), index)
     if out is None:
+        dev = logits.device
         weights = _new(T, k, torch.float32, dev)
         ids = _new(T, k, torch.int32, dev)
     else:
         weights, ids = out
-        _need("weights", weights, torch.float32, (T, k), dev)
-        _need("ids", ids, torch.int32, (T, k), dev)
+        _need("weights", weights, torch.float32, (T, k), index)
+        _need("ids", ids, torch.int32, (T, k), index)
     a = RouteArgs(T, E, k, _types()[1][logits.dtype], SCORINGS[scoring], groups, topk_groups,
                   group_top, int(bool(renormalize)), scale, 0, logits.data_ptr(), _address(bias),
                   weights.data_ptr(), ids.data_ptr())
-    _enqueue(dev, lib().mhc_route, ctypes.byref(a))
+    _enqueue(index, lib().mhc_route, ctypes.byref(a))
     return weights, ids

@@ -232,10 +232,10 @@ def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
     seen = []
 
     @contextlib.contextmanager
-    def switched(device):
-        seen.append(("to", device.index))
+    def switched(index):
+        seen.append(("to", index))
         yield
-        seen.append(("back", device.index))
+        seen.append(("back", index))
 
     def call(a, handle):
         seen.append((a, handle))
@@ -244,10 +244,10 @@ def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
     monkeypatch.setattr(torch.cuda, "device", switched)
-    S._enqueue(torch.device("cuda", 1), call, "x")
+    S._enqueue(1, call, "x")
     assert seen == [("to", 1), ("x", 101), ("back", 1)]
     seen.clear()
-    S._enqueue(torch.device("cuda", 0), call, "x")
+    S._enqueue(0, call, "x")
     assert seen == [("x", 100)]
 
 
