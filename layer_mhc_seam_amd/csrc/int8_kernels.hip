@@ -17,7 +17,7 @@
 // l / 16 + 4 q of a step.
 //
 // What bounds it, at N = K = 5120 (inputs beyond the L2, within the 256 MB
-// behind it): T = 1 the weights' bytes, 6.8 us, 2 of them the launch (3.9 TB/s;
+// behind it): T = 1 the weights' bytes, 6.4 us, 2 of them the launch (4.1 TB/s;
 // a bare read of them takes 5.4); T = 384 the rows' way from L2 into LDS, 17.3
 // us (983 KB a CU, 17 TB/s in all; these loads alone, without products, take
 // 12.8; larger wave tiles with half the LDS reads, LDS reads moved between the
@@ -75,17 +75,22 @@ __device__ __forceinline__ void block_barrier()
 
 // ------------------------------------------------------------ tiled kernel --
 //
-// A workgroup of (TM / WM)(TN / WN) waves computes a TM x TN block, each wave
-// WM x WN of it, in steps of KS = 128, 256 or 512 of K.  A step's rows go from
+// A workgroup of KW (TM / WM)(TN / WN) waves computes a TM x TN block, each wave
+// WM x WN of it over a KW-th of every step of KS = 128, 256 or 512 of K; sums
+// of the KW parts are joined at the end.  (Small blocks wait for a step's chain
+// of LDS reads and products more than for its bytes.  T = 4, N = 256, K = 5120
+// with KW 1 and 16 x 32, then 4 and 16 x 32, then 8 and 16 x 16: 5.8, 5.0, 4.4
+// us; T = 32, N = 5120 with 32 x 32 and KW 1 and 2: 7.4 and 7.2; blocks of 64 x
+// 64 and more gain nothing.)  A step's rows go from
 // memory straight into LDS (16 bytes a lane, 1 KB a wave and instruction:
 // 1024 / KS rows of KS bytes); S stages keep S - 1 steps' loads in flight.
 // Piece c of row R lies in slot c ^ turn(R) of its row, which puts the 16
 // lanes of a read phase (16 rows, one piece each) on different banks: two
 // rows of 128 bytes, or 256 of a row, cover the banks once.
-template <int TM_, int TN_, int WM_, int WN_, int S_, int KS_ = 128>
+template <int TM_, int TN_, int WM_, int WN_, int S_, int KS_ = 128, int KW_ = 1>
 struct Tile {
-    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, S = S_, KS = KS_;
-    static constexpr int NW = (TM / WM) * (TN / WN);
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, S = S_, KS = KS_, KW = KW_;
+    static constexpr int kTiles = (TM / WM) * (TN / WN), NW = kTiles * KW;
     static constexpr int kThreads = 64 * NW;
     static constexpr int kPieces = KS / 16, kRunRows = 1024 / KS;   // of a row; of a 1 KB run
     static constexpr int kRunsA = TM / kRunRows / NW, kRunsB = TN / kRunRows / NW;   // a wave's
@@ -97,6 +102,8 @@ struct Tile {
     static_assert(S >= 2 && (S - 1) * kLoads + kFactors < 64,
                   "the loads in flight fit the vmcnt counter");
     static_assert(S * (TM + TN) * KS >= TM * TN * 2, "16-bit results fit the stages");
+    static_assert(S * (TM + TN) * KS >= (KW - 1) * TM * TN * 4, "and the parts' sums do");
+    static_assert(KS / 64 % KW == 0, "whole products per part");
     static __device__ __forceinline__ int turn(int row)
     {
         return KS == 128 ? row >> 1 & 7 : row & 15;
@@ -189,7 +196,8 @@ __device__ __forceinline__ O finish(int acc, float sa, float sb, float bias, boo
 // The block's results from a wave's sums: binary32 straight to memory (16
 // lanes store 64 consecutive bytes), 16-bit types by way of LDS (`ot`, free by
 // now) to 16-byte pieces of rows, or single elements, 64 in a row, where rows
-// do not start on 16 bytes.  factor: the block's sa, sb and bias.
+// do not start on 16 bytes.  factor: the block's sa, sb and bias.  The first
+// of the KW parts' waves hold the sums.
 template <class C, class O>
 __device__ __forceinline__ void store_block(const Int8GemmParams &P, int m_blk, int n_blk, int wm,
                                             int wn, const i32x4 (&acc)[C::WM / 16][C::WN / 16],
@@ -208,7 +216,7 @@ __device__ __forceinline__ void store_block(const Int8GemmParams &P, int m_blk, 
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4 && (C::KW == 1 || tid < 64 * C::kTiles); ++e) {
             const int row = wm + 16 * i + 4 * g + e;
             const float sa = factor[row];
 #pragma unroll
@@ -281,13 +289,14 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_gemm_tile_kernel(Int8Gemm
     if (!block_of((int)block_id(), (T - 1) / C::TM + 1, (N - 1) / C::TN + 1, mi, ni))
         return;
     const int m_blk = mi * C::TM, n_blk = ni * C::TN;
-    const int wm = (wave / (C::TN / C::WN)) * C::WM, wn = (wave % (C::TN / C::WN)) * C::WN;
+    const int part = wave / C::kTiles, tile = wave % C::kTiles;
+    const int wm = (tile / (C::TN / C::WN)) * C::WM, wn = (tile % (C::TN / C::WN)) * C::WN;
     const int g = lane >> 4, r = lane & 15;
-    constexpr int Q = C::KS / 64;   // products of a step: pieces g + 4 q of row r
+    constexpr int Q = C::KS / 64 / C::KW;   // products of a step: pieces g + 4 q of row r
     int at[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-        at[q] = r * C::KS + 16 * ((g + 4 * q) ^ C::turn(r));
+        at[q] = r * C::KS + 16 * ((g + 4 * (part * Q + q)) ^ C::turn(r));
     i32x4 acc[MI][NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -349,6 +358,22 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_gemm_tile_kernel(Int8Gemm
     }
     wait_vm<0>();      // the re-reads past the end have landed
     __syncthreads();   // and every wave is done with the stages
+    if constexpr (C::KW > 1) {
+        constexpr int kEach = 64 * MI * NJ;
+        i32x4 *sums = reinterpret_cast<i32x4 *>(&st[0]) + tile * kEach + lane;
+#pragma unroll
+        for (int i = 0; i < MI * NJ; ++i)
+            if (part > 0)
+                sums[(part - 1) * C::kTiles * kEach + 64 * i] = acc[i / NJ][i % NJ];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < C::KW - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < MI * NJ; ++i)
+                if (part == 0)
+                    acc[i / NJ][i % NJ] += sums[k * C::kTiles * kEach + 64 * i];
+        __syncthreads();
+    }
     store_block<C, O>(P, m_blk, n_blk, wm, wn, acc, factor, reinterpret_cast<O *>(&st[0]));
 }
 
@@ -487,9 +512,10 @@ __global__ __launch_bounds__(RingTile::kThreads, 1) void int8_gemm_ring_kernel(I
 template <class F>
 void int8_shapes(F &&f)
 {
-    f(Tile<16, 32, 16, 16, 3, 512>(), 10);
-    f(Tile<32, 32, 16, 16, 4, 256>(), 12);
-    f(Tile<32, 64, 16, 32, 4, 256>(), 16);
+    f(Tile<16, 16, 16, 16, 4, 512, 8>(), 5);
+    f(Tile<16, 32, 16, 16, 3, 512, 2>(), 10);
+    f(Tile<32, 32, 16, 16, 4, 256, 2>(), 11);
+    f(Tile<32, 64, 16, 32, 4, 256, 2>(), 15);
     f(Tile<64, 64, 16, 32, 3, 256>(), 21);
     f(Tile<96, 64, 48, 16, 3, 256>(), 28);
     f(Tile<128, 64, 32, 32, 3, 256>(), 32);

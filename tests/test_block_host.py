@@ -216,6 +216,8 @@ def test_int8_gemm_blocks_by_token_count():
     for T, shape in want.items():
         assert S.int8_gemm_blocks(T, 5120, 256) == shape, T
     assert S.int8_gemm_blocks(4160, 256, 256) == (96, 64)
+    assert S.int8_gemm_blocks(1, 4096, 256) == (16, 16) and S.int8_gemm_blocks(1, 4097, 256) == (16, 32)
+    assert S.int8_gemm_blocks(128, 256, 256) == (16, 16) and S.int8_gemm_blocks(384, 256, 256) == (16, 32)
     assert S.int8_gemm_blocks(128, 5120, 128) != S.int8_gemm_blocks(128, 5120, 256)
 
 

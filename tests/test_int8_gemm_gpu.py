@@ -201,8 +201,8 @@ def test_int8_gemm_refusals():
 
 # one shape, or more, for each of the launch's blocks: whole and ragged rows
 # and columns, K of one step, of several, and ending inside one
-BLOCK_SHAPES = [(16, 320, 512), (9, 333, 1040), (30, 5120, 256), (27, 5100, 784), (90, 4000, 512),
-                (70, 5099, 1296), (180, 5120, 256), (150, 4001, 528), (250, 5120, 768), (270, 4999, 272),
+BLOCK_SHAPES = [(16, 320, 512), (9, 333, 1040), (16, 5120, 512), (7, 5003, 1552), (30, 5120, 256),
+                (27, 5100, 784), (90, 4000, 512), (70, 5099, 1296), (180, 5120, 256), (150, 4001, 528), (250, 5120, 768), (270, 4999, 272),
                 (380, 5120, 512), (300, 5111, 800), (700, 5120, 256), (600, 5117, 400), (1000, 5120, 128),
                 (900, 5101, 656), (1500, 5120, 384), (1300, 5110, 144), (2000, 5120, 256), (1900, 5109, 304),
                 (2500, 5120, 128), (2400, 5103, 272), (5000, 5120, 640), (6100, 5099, 16)]
@@ -213,7 +213,7 @@ def test_block_shapes_cover_every_block():
     seen = {}
     for T, N, _ in BLOCK_SHAPES:
         seen.setdefault(int8_gemm_blocks(T, N, 256), []).append((T, N))
-    assert len(seen) == 11 and all(len(v) >= 2 for v in seen.values()), seen
+    assert len(seen) == 12 and all(len(v) >= 2 for v in seen.values()), seen
 
 
 @pytest.mark.parametrize("T,N,K", BLOCK_SHAPES)
