@@ -408,20 +408,31 @@ def _enqueue(index, call, *args):
         _check(status)
 
 
+def _tensors(v):
+    """The tensors in v: itself, or what a dict, tuple or list holds."""
+    import torch
+    if isinstance(v, torch.Tensor):
+        return (v,)
+    if isinstance(v, dict):
+        v = v.values()
+    elif not isinstance(v, (tuple, list)):
+        return ()
+    return tuple(t for t in v if isinstance(t, torch.Tensor))
+
+
 def _on_stream(stream, op, *args, **kw):
     """op(*args, **kw) with `stream` current, so that its outputs are allocated
     there.  The memory of the tensors given is not handed on by the allocator
-    before the stream is done with them."""
+    before the stream is done with them: of the inputs, and of the outputs,
+    which the result holds whatever `out` gave them in."""
     import torch
     if stream.device != args[0].device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {args[0].device}")
     with torch.cuda.stream(stream):
         result = op(*args, **kw)
-    out = kw.get("out")
-    for t in (*args, *kw.values(), *(out.values() if isinstance(out, dict) else
-                                     out if isinstance(out, tuple) else ())):
-        if isinstance(t, torch.Tensor):
-            t.record_stream(stream)
+    used = {id(t): t for v in (*args, *kw.values(), result) for t in _tensors(v)}
+    for t in used.values():
+        t.record_stream(stream)
     return result
 
 

@@ -285,6 +285,41 @@ def test_calls_on_a_stream(monkeypatch):
         S._on_stream(Stream, op, x)
 
 
+def test_calls_on_a_stream_keep_outputs_given_in_any_form(monkeypatch):
+    """int8_quantize and route write to any pair, block_norm to any mapping:
+    the tensors given are recorded as used on the stream whatever holds them,
+    and each once."""
+    import contextlib
+    import types
+    seen = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append(t.item()))
+
+    class Stream:
+        device = torch.device("cpu")
+
+    def pair(*args, out):
+        first, second = out
+        return first, second
+
+    def named(*args, out):
+        return dict(out)
+
+    def one(*args, out):
+        return out
+
+    x, o1, o2 = (torch.tensor(i) for i in range(3))
+    for op, out in ((pair, [o1, o2]), (pair, iter((o1, o2))), (pair, {o1: 0, o2: 0}.keys()),
+                    (pair, (o1, o2)), (named, types.MappingProxyType({"a": o1, "b": o2})),
+                    (named, [("a", o1), ("b", o2)]), (named, {"a": o1, "b": o2})):
+        seen.clear()
+        S._on_stream(Stream, op, x, out=out)
+        assert sorted(seen) == [0, 1, 2], (op.__name__, type(out))
+    seen.clear()
+    assert S._on_stream(Stream, one, x, out=o1) is o1
+    assert sorted(seen) == [0, 1]
+
+
 def test_sizes_past_32_bits_are_refused():
     """ctypes would cut them to ones that the library takes."""
     S._fits(1 | 2 ** 31 - 1)
