@@ -97,9 +97,9 @@ __device__ __forceinline__ double row_sum(double v)
     return v + row_ror<1>(v);
 }
 
-// Value of lane l ^ 1, l ^ 2; of lane l ^ 7 and l ^ 15, which stand for
-// l ^ 4 and l ^ 8 once the lanes of each four, or eight, hold one value.
-enum { kXor1 = 0xb1, kXor2 = 0x4e, kXor4 = 0x141, kXor8 = 0x140 };
+// Value of lane l ^ 1, l ^ 2; and of lane l ^ 7, which stands for l ^ 4 once
+// the lanes of each four hold one value.
+enum { kXor1 = 0xb1, kXor2 = 0x4e, kXor4 = 0x141 };
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t row_swap(uint32_t v)
