@@ -98,3 +98,36 @@ def route(logits, k, scoring, bias, groups, keep, top, renorm, scale):
         if poisoned:
             w[t] = np.nan
     return torch.from_numpy(w), torch.from_numpy(ids)
+
+
+def route_rows(logits, k, scoring, bias, groups, keep, top, renorm, scale):
+    """route() for many tokens at once, on the device the logits are on."""
+    T, E = logits.shape
+    inf = math.inf
+    l = logits.to(F64)
+    bad = l.isnan() | ((l == inf) if scoring == "softmax" else torch.zeros_like(l, dtype=torch.bool))
+    l = l.masked_fill(bad, -inf)
+    out = l == -inf
+    if scoring == "sigmoid":
+        s = 1.0 / (1.0 + torch.exp(-l))
+    else:
+        e = torch.exp(l - l.amax(1, keepdim=True).clamp_min(torch.finfo(F64).min))
+        s = e / e.sum(1, keepdim=True).clamp_min(torch.finfo(F64).tiny)
+    score = (s if bias is None else s + bias.to(F64)).masked_fill(out, -inf)
+    key = l.clone() if bias is None else score.clone()
+    if groups > 1:
+        by_group = (key if top == 1 else score).view(T, groups, E // groups)
+        best = by_group.sort(dim=2, descending=True).values[..., :top]
+        if top == 2:
+            best = best.masked_fill(best == -inf, -1e30)
+        order = best.sum(2).sort(dim=1, descending=True, stable=True).indices
+        shut = torch.ones(T, groups, dtype=torch.bool, device=l.device).scatter_(1, order[:, :keep], False)
+        key.view(T, groups, -1).masked_fill_(shut[..., None], -inf)
+    order = key.sort(dim=1, descending=True, stable=True)
+    ids, none = order.indices[:, :k], order.values[:, :k] == -inf
+    w = s.gather(1, ids).masked_fill(none, 0.0)
+    if renorm:
+        total = w.sum(1, keepdim=True)
+        w = torch.where(total > 0, w / total, torch.zeros_like(w))
+    w = (w * scale).masked_fill(bad.any(1, keepdim=True), math.nan)
+    return w, ids.masked_fill(none, -1).to(torch.int32)

@@ -202,6 +202,26 @@ def test_route_definition():
     assert w[:2].tolist() == [[1.0, 0.0], [0.0, 0.0]] and w[2].isnan().all()
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_definitions_agree(scoring):
+    """Many tokens at once choose as one token and one choice at a time."""
+    g = torch.Generator().manual_seed(3)
+    for E, k, groups, keep, top, renorm in ((1, 1, 1, 1, 1, True), (40, 6, 1, 1, 1, False), (64, 8, 8, 3, 1, True),
+                                            (63, 9, 7, 2, 2, True), (96, 40, 48, 20, 2, False)):
+        l = torch.randint(-8, 9, (60, E), generator=g) / 4
+        l[::2] = torch.randn(30, E, generator=g)
+        l = l.masked_fill(torch.rand(60, E, generator=g) < torch.linspace(0, 1.2, 60)[:, None], -math.inf)
+        l[5, 0], l[6, E - 1] = math.nan, math.inf
+        b = 0.1 * torch.randn(E, generator=g)
+        b[E // 3] = -math.inf
+        for bias in (None, b):
+            w, ids = ref.route(l, k, scoring, bias, groups, keep, top, renorm, 1.5)
+            w2, ids2 = ref.route_rows(l, k, scoring, bias, groups, keep, top, renorm, 1.5)
+            assert torch.equal(ids, ids2) and torch.equal(w.isnan(), w2.isnan())
+            # two evaluations in binary64: sums of up to 96 terms and k weights
+            assert ((w - w2).abs().nan_to_num(0) <= 2.0 ** -44 * w.abs().nan_to_num(0)).all()
+
+
 # ------------------------------------------- blocks of the int8 product --
 
 def test_int8_gemm_blocks_by_token_count():

@@ -327,3 +327,37 @@ def test_more_rows_than_a_grid_line_holds():
     o = seam().block_norm(x, g)
     _, n = ref.block_norm(v, g.cpu(), None, None, None, 1.0, 1.0)
     same(o["norm"][at], n)
+
+
+@pytest.mark.parametrize("H0,dt,xdt", [(500, BF16, BF16), (512, F16, F32), (509, BF16, F32), (512, BF16, BF16)])
+def test_norms_do_not_depend_on_the_width_of_the_launch(H0, dt, xdt):
+    """The same values among zeros, at random places of rows 4, 16 and 64
+    times as wide: a row's mean is then 4^k times smaller, which eps 4^-k and
+    gammas of 2^-k times take back without a rounding.  The sums of squares
+    go over other lanes, waves and workgroup sizes each time, and every
+    output has the bits of the narrow row's and of the definition."""
+    T = 7
+    c = inputs(T, H0, dt, xdt, "channel", True, seed=H0)
+    first = None
+    for k in range(4):
+        H = H0 * 4 ** k
+        if H > (32768 if H % 8 == 0 else 32752):
+            break
+        g = torch.Generator().manual_seed(k)
+        at = torch.randperm(H, generator=g)[:H0].sort().values if k else torch.arange(H0)
+        w = {}
+        for name, v in c.items():
+            w[name] = torch.zeros(*v.shape[:-1], H, dtype=v.dtype)
+            w[name][..., at] = v / 2 ** k if name in ("gamma", "gamma_post") else v
+        eps = 2.0 ** -20 / 4 ** k
+        o = seam().block_norm(**dev(w), branch_scale=0.5, eps=eps, int8=True)
+        r, n = ref.block_norm(**w, residual_scale=1.0, branch_scale=0.5, eps=eps)
+        codes, scales = ref.quantize(n)
+        for name, want in (("residual_out", r), ("norm", n), ("codes", codes), ("scales", scales)):
+            same(o[name], want)
+        got = [o[name].cpu()[:, at] for name in ("residual_out", "norm", "codes")] + [o["scales"].cpu()]
+        if first is None:
+            first = got
+        for a, b in zip(got, first):
+            same(a, b)
+    assert k >= 2

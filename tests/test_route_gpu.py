@@ -5,6 +5,7 @@ differ by less than a few of its last places are exact ties (equal logits).
 Weights are binary64 until their one rounding: 2^-24 relative, and 2^-40 for
 the difference of two binary64 evaluations."""
 import math
+import random
 
 import pytest
 import torch
@@ -318,3 +319,64 @@ def test_route_more_tokens_than_a_grid_line_holds():
     l[at, 1] = 1.0
     w, ids = route(l, 1)
     assert int(ids.sum()) == len(at) and (ids[at] == 1).all() and bool((w == 1).all())
+
+
+def random_case(rng):
+    E = rng.choice((rng.randint(1, 1024), rng.randint(1, 300), 8 * rng.randint(1, 64), 16 * rng.randint(1, 32)))
+    groups = rng.choice([1] + [n for n in range(1, 65) if E % n == 0])
+    size = E // groups
+    keep = rng.randint(1, groups)
+    top = rng.choice((1, 2)) if groups > 1 and size > 1 else 1
+    k = rng.randint(1, min(rng.choice((8, 8, 16, 64)), keep * size))
+    return dict(E=E, k=k, groups=groups, keep=keep, top=top, dt=rng.choice(DTYPES),
+                scoring=rng.choice(("softmax", "sigmoid")), renorm=rng.random() < 0.7,
+                scale=rng.choice((1.0, 2.5, -0.5)), bias=rng.choice((0.0, 0.05, 1.0, "masked")),
+                mask=rng.choice(("none", "none", "some", "groups", "low", "lowest", "odd")),
+                spread=rng.choice((1.5, 1.5, 0.05, 10.0, "few")))
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_route_many_rows_of_random_layouts(seed):
+    """Thousands of rows of drawn layouts, types, biases and masks, so that
+    experts and groups come as close as they do in a batch: every id equal to
+    the binary64 choice.  Masks by -inf, by whole groups, by a large finite
+    value or the type's lowest, NaN and infinities strewn in."""
+    from layer_mhc_seam_amd.seam import route
+    c = random_case(random.Random(seed))
+    E, groups = c["E"], c["groups"]
+    T = min(6000, (1 << 20) // E)
+    g = torch.Generator().manual_seed(seed)
+    # few values, and no x beside -x, whose sigmoids add up to 1 for every x
+    l = 0.3 + torch.randint(-6, 7, (T, E), generator=g) / 8 if c["spread"] == "few" else \
+        c["spread"] * torch.randn(T, E, generator=g)
+    hit = torch.rand(T, E, generator=g) < 0.6 * torch.rand(T, 1, generator=g)
+    if c["mask"] == "groups":
+        hit = (torch.rand(T, groups, 1, generator=g) < 0.4).expand(T, groups, E // groups).reshape(T, E)
+    if c["mask"] in ("some", "groups"):
+        l = l.masked_fill(hit, -math.inf)
+    elif c["mask"] == "low":
+        l = l.masked_fill(hit, -1e4)
+    elif c["mask"] == "lowest":
+        l = l.masked_fill(hit, torch.finfo(c["dt"]).min)
+    elif c["mask"] == "odd":
+        for v in (math.nan, math.inf, -math.inf):
+            l = l.masked_fill(torch.rand(T, E, generator=g) < 0.3 / E, v)
+    l = l.to(c["dt"]).cuda()
+    bias = None
+    if c["bias"]:
+        bias = 0.1 * torch.randn(E, generator=g)
+        if c["bias"] == "masked":
+            bias = bias.masked_fill(torch.rand(E, generator=g) < 0.2, -math.inf)
+        else:
+            bias = c["bias"] * bias
+        bias = bias.cuda()
+    w, ids = route(l, c["k"], scoring=c["scoring"], bias=bias, groups=groups, topk_groups=c["keep"],
+                   group_top=c["top"], renormalize=c["renorm"], scale=c["scale"])
+    want_w, want = ref.route_rows(l, c["k"], c["scoring"], bias, groups, c["keep"], c["top"], c["renorm"],
+                                  c["scale"])
+    bad = (ids != want).any(1).nonzero()
+    assert not len(bad), f"{c}: {len(bad)} rows, first {bad[0].item()}: {ids[bad[0]]} for {want[bad[0]]}"
+    nan = want_w.isnan()
+    assert torch.equal(w.isnan(), nan)
+    err = (w.double() - want_w).abs()[~nan]
+    assert (err <= (2.0 ** -24 + 2.0 ** -40) * want_w.abs()[~nan] + 2.0 ** -149).all(), c
