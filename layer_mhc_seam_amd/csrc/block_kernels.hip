@@ -24,13 +24,14 @@
 // One pass over memory: a workgroup owns a row and keeps it in registers
 // between the two (or three) reductions, so each input is read once and each
 // output written once.  The row's bytes bound it: T = 16384, H = 5120, bf16,
-// both norms, a gate for each element, norm and codes (923 MB) take 152.5 us,
-// 6.05 TB/s, which is what a copy reaches; the quantiser alone 41.1 us (6.13
-// TB/s).  Vector instructions are next, 635 a wave of 1024 values, 85 us of
-// them issued back to back: hence the cheap roundings and maxima below.  With
-// 802 (a quotient and a square root in binary64 a wave, masks for each value)
-// the same call took 163 us.  Asking for the gammas ahead of the sums costs
-// registers and with them rows in flight (182 us).
+// both norms, a gate for each element, norm and codes (923 MB) take 153 us at
+// best, 6.05 TB/s, which is what a copy reaches, and 157 to 161 call after
+// call; the quantiser alone 42 us (6.0 TB/s).  Vector instructions are next,
+// 638 a wave of 1024 values, 85 us of them issued back to back: hence the
+// cheap roundings and maxima below.  (With 802, of a quotient and a square
+// root in binary64 a wave and masks for each value, the best was 163 us.)
+// Asking for the gammas ahead of the sums changes nothing (157 to 161 us; T = 4
+// 5.0 for 4.9).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -63,8 +64,11 @@ struct F32 {
 // `from` to `to` - 1 exist (the rest read as zero).  Chunks end where memory
 // has a multiple of 8 elements, so that whole ones are aligned in every tensor
 // of the row's layout whatever the width; the first and last of a row may be
-// partial.  (T = 16384, H = 5117, bf16 with int8: 202 us with chunks counted
-// from the row's first element, 187 with these; H = 5120 takes 117.)
+// partial.  (Chunks counted from the row's first element took 8% longer at
+// T = 16384, H = 5117, bf16 with int8.  With these it takes 160 us where H =
+// 5120 takes 125: 558 vector instructions a wave for 457, of the partial
+// chunks' code, and six waves a row for five, since a row spans up to 642
+// chunks; the bytes written are 4% more.)
 template <bool RAGGED>
 struct Span {
     int at, from, to;
@@ -532,10 +536,12 @@ __global__ __launch_bounds__((max_threads<NC, WAVE>())) void int8_quantize_kerne
 }
 
 // Rows of up to 128 chunks (H = 1024) take a wave each, four in a workgroup,
-// without barriers (H = 2048 in a wave and in a workgroup: 57.9 and 56.7 us at
-// T = 16384, 4.8 and 3.7 at T = 4).  Longer ones take a workgroup of up to 512
-// threads with two chunks each (H = 5120 with one, two and four a thread: 193,
-// 162 and 167 us at T = 16384), the longest up to 1024 with four.
+// without barriers (bf16, both norms, element gate, int8, in a wave and in a
+// workgroup: H = 512 17.8 and 20.5 us at T = 16384, 2.7 and 3.3 at T = 4; H =
+// 1024 no difference; H = 2048 64.3 and 63.0, 5.0 and 4.0).  Longer ones take a
+// workgroup of up to 512 threads with two chunks each (H = 5120 with one, two
+// and four a thread: 186, 157 and 158 us at T = 16384; 4.4, 4.9 and 5.7 at T =
+// 4, channel gate), the longest up to 1024 with four.
 template <class F>
 hipError_t with_shape(int64_t rows, int H, F &&f)
 {

@@ -16,16 +16,18 @@
 // on its order, so the assignment itself is free: here the 16-byte pieces
 // l / 16 + 4 q of a step.
 //
-// What bounds it, at N = K = 5120 (inputs beyond the L2, within the 256 MB
-// behind it): T = 1 the weights' bytes, 6.4 us, 2 of them the launch (4.1 TB/s;
-// a bare read of them takes 5.4); T = 384 the rows' way from L2 into LDS, 17.3
-// us (983 KB a CU, 17 TB/s in all; these loads alone, without products, take
+// What bounds it, at N = K = 5120 (times in a graph of such products over four
+// sets of operands in turn, beyond the L2, within the 256 MB behind it): T = 1
+// the weights' bytes, 6.4 us, 2 of them the launch (4.1 TB/s; a bare read of
+// them takes 5.4); T = 384 the rows' way from L2 into LDS, 17.3 to 18.0 us
+// (983 KB a CU, 17 TB/s in all; these loads alone, without products, take
 // 12.8; larger wave tiles with half the LDS reads, LDS reads moved between the
-// products, steps begun elsewhere in each block took as long), and 21.5 at K =
-// 5136, whose rows do not start on 128 bytes, so that a piece touches three
-// lines for two; T = 16384 345 us, 2.49 PFLOP/s, of which the products alone
-// take 235 (the clock falls under them: 4.0 PFLOP/s is the instruction's own
-// rate over Gaussian codes, 4.7 over zeros), the loads alone 295.
+// products, steps begun elsewhere in each block took as long), and 19.9 to
+// 20.5 at K = 5136, whose rows do not start on 128 bytes, so that a piece
+// touches three lines for two; T = 16384 the clock under the products and the
+// loads: 340 us at best (2.53 PFLOP/s), 380 to 395 call after call (2.2), the
+// loads alone 295 and the products alone 235 (4.0 PFLOP/s is the instruction's
+// own rate over Gaussian codes, 4.7 over zeros).
 // Operands straight into registers, without LDS: 9 us at T = 1, since 64-byte
 // pieces of rows come at two thirds of the rate of 128-byte ones.
 #include <hip/hip_runtime.h>
@@ -79,9 +81,9 @@ __device__ __forceinline__ void block_barrier()
 // WM x WN of it over a KW-th of every step of KS = 128, 256 or 512 of K; sums
 // of the KW parts are joined at the end.  (Small blocks wait for a step's chain
 // of LDS reads and products more than for its bytes.  T = 4, N = 256, K = 5120
-// with KW 1 and 16 x 32, then 4 and 16 x 32, then 8 and 16 x 16: 5.8, 5.0, 4.4
-// us; T = 32, N = 5120 with 32 x 32 and KW 1 and 2: 7.4 and 7.2; blocks of 64 x
-// 64 and more gain nothing.)  A step's rows go from
+// with 16 x 32 and KW 1, 2 and 4, then 16 x 16 and 8: 5.6, 5.0, 4.8, 4.4 us; T =
+// 32, N = 5120 with 32 x 32 and KW 1 and 2: 7.7 and 7.2; blocks of 64 x 64 and
+// more gain nothing.)  A step's rows go from
 // memory straight into LDS (16 bytes a lane, 1 KB a wave and instruction:
 // 1024 / KS rows of KS bytes); S stages keep S - 1 steps' loads in flight.
 // Piece c of row R lies in slot c ^ turn(R) of its row, which puts the 16
@@ -505,10 +507,11 @@ __global__ __launch_bounds__(RingTile::kThreads, 1) void int8_gemm_ring_kernel(I
 
 // The shapes a launch chooses from, smallest first, with what a round of the
 // CUs costs: measured times of one workgroup a CU at K = 5120 less the
-// launch's 2 us, in units of half a microsecond.  Few rows of K a step leave
-// the small blocks waiting at barriers (16 x 32 in steps of 128, 256 and 512:
-// 8.1, 7.0 and 6.8 us at T = 1, N = K = 5120); from 128 x 128 on LDS has no
-// room for more than 128.
+// launch's 2 us, in units of half a microsecond.  K is not asked for: the
+// prologue, the re-reads and the store weigh more at short depths than these
+// costs say.  Few rows of K a step leave the small blocks waiting at barriers
+// (16 x 32 with KW 1 in steps of 128, 256 and 512: 7.7, 6.7 and 6.4 us at T = 1,
+// N = K = 5120); from 128 x 128 on LDS has no room for more than 128.
 template <class F>
 void int8_shapes(F &&f)
 {

@@ -25,12 +25,19 @@
 // softmax) is taken out likewise and turns the row's weights to NaN, so ids
 // always lie in -1 .. E - 1 and are distinct but for -1.
 //
-// Reading the logits would take 2.8 us at T = 16384, E = 256, the launch 2.
-// What bounds it is instructions: with a wave a token in binary64 34 us, four
-// tokens a wave 12.6 (about 1000 vector instructions a wave, 6.5 us of them
-// issued back to back; the rest is one wave's latency, 5.6 us in all at T = 1).
+// Reading the logits would take 2.8 us at T = 16384, E = 256 (8 groups,
+// sigmoid, bias), the launch 2.  With a wave a token in binary64 it took 34 us;
+// four tokens a wave 12.0 to 12.3.  Past that instructions bound it: 1027
+// vector ones a wave, and each 16384 tokens more cost 6.2 to 7.2 us, about what
+// these take issued back to back (T = 32768 19 us, 65536 33, 131072 58).  Below
+// it is latency: 6.0 us at T = 1, 7.3 at T = 4096.  At 16384 all waves, four a
+// SIMD, are resident at once and wait for their logits together, so that first
+// wait and the last stores are not hidden behind another wave's instructions.
 // A row that has to be done again in binary64 costs 3 us by itself: with those
-// whose groups were close done so, T = 4160 took 9.6 where it now takes 7.6.
+// whose groups were close done so, T = 4160 took 9.6 where it then took 7.6.
+// Where a mask sends many rows there, it shows: T = 16384 with one of the eight
+// groups out in every row 48 us; without groups, with 30% of the rows short of
+// experts 31, and softmax over logits with 30% of them at -1e9 43 for 9.
 #include <hip/hip_runtime.h>
 
 #include "lane_ops.h"
@@ -627,7 +634,9 @@ template <class T>
 hipError_t launch(const RouteParams &p, int64_t tokens, hipStream_t s)
 {
     // Four tokens a wave where groups, experts and the chosen fit a row of 16
-    // lanes and 32 experts each
+    // lanes and 32 experts each; a wave a token, in binary64, past that (T =
+    // 16384, 512 experts without groups 18 us, 768 84, 1024 89; 256 experts in 8
+    // groups 12 and in 32 groups 34; 32 chosen of 256 71)
     const int lanes = p.groups <= 16 ? lanes_of(p.groups) : 1, size = p.E / p.groups;
     const int per = (size + lanes - 1) / lanes;
     if (p.groups <= 16 && per <= 32 && p.k <= 16) {

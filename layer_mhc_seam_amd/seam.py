@@ -360,7 +360,8 @@ def mxfp8_gemm(a, a_scales, b, b_scales, *, out=None, stream=None):
 # Unlike the calls above, these run on the device their tensors are on,
 # whichever is current, and on that device's current stream.  A `stream` of
 # their own has to come after what made the tensors, as ever; it gets the
-# outputs' memory too.
+# outputs' memory too.  Tensors are dense and start on 16 bytes (route's, and
+# scales and biases, on their elements): a slice that does not is refused.
 
 @functools.lru_cache(maxsize=None)
 def _types():
@@ -459,8 +460,10 @@ def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_sc
     gamma: residual_out alone.  int8: also the norm's codes (int8 [T, H]) and
     scales (f32 [T]), the operand of int8_gemm; norm=False then leaves the
     norm itself out.
-    Returns a dict of outputs (allocated unless given in `out`; residual_out
-    may be x)."""
+    H up to 32768, or 32752 if no multiple of 8.  eps in [0, 1]; 0 selects
+    1e-6.
+    Returns a dict of outputs (allocated unless given in `out`, a dict too;
+    residual_out may be x)."""
     import torch
     if stream is not None:
         return _on_stream(stream, block_norm, x, gamma, y, gamma_post=gamma_post, gate=gate,
@@ -543,8 +546,9 @@ def block_norm(x, gamma=None, y=None, *, gamma_post=None, gate=None, residual_sc
 
 def int8_quantize(src, *, out=None, stream=None):
     """int8 codes [rows, H] and f32 scales [rows] of a bf16 or f16 [rows, H]
-    device tensor, one scale a row: the operands of int8_gemm.  out: the pair
-    to write to."""
+    device tensor, one scale a row: the operands of int8_gemm, which takes
+    widths that are multiples of 16.  H up to 32768, or 32752 if no multiple of
+    8.  out: the pair to write to."""
     import torch
     if stream is not None:
         return _on_stream(stream, int8_quantize, src, out=out)
@@ -572,7 +576,8 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, *, out_dtype="bf16", out=None
     """Product of int8 codes with a scale for each token and channel:
     out[t, n] = sum_k a[t, k] b[n, k] * a_scales[t] * b_scales[n] (+ bias[n]).
     a int8 [T, K], a_scales f32 [T] (block_norm's or int8_quantize's), b int8
-    [N, K], b_scales and bias f32 [N]; out_dtype bf16, f16 or f32."""
+    [N, K], b_scales and bias f32 [N]; out_dtype bf16, f16 or f32.  K a
+    multiple of 16, up to 131056; any N."""
     import torch
     if stream is not None:
         return _on_stream(stream, int8_gemm, a, a_scales, b, b_scales, bias, out_dtype=out_dtype,
@@ -617,8 +622,8 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
     their scores (softmax or sigmoid), renormalized and times scale.  bias f32
     [E].  A group's score is the sum of its group_top (1 or 2) highest keys.
     Returns (weights f32 [T, k], ids int32 [T, k]), highest first; id -1 and
-    weight 0 where masks (-inf) leave fewer than k experts.  out: the pair to
-    write to."""
+    weight 0 where masks (-inf) leave fewer than k experts.  E up to 1024, k
+    and groups up to 64.  out: the pair to write to."""
     import torch
     if stream is not None:
         return _on_stream(stream, route, logits, k, scoring=scoring, bias=bias, groups=groups,
