@@ -501,6 +501,197 @@ typedef struct mhc_route_args {
 
 int mhc_route(const mhc_route_args *args, void *stream);
 
+/* --------------------------------------------- attention over a 4-bit cache
+ *
+ * What stands between a block's first product and its second in a decoder:
+ * rotary positions, the cache of keys and values, and attention over it.
+ * Rules as above (no handle, no state, nothing allocated, calls on any
+ * streams, captured or not), but for what is said of strides and of the
+ * attention's workspace.
+ *
+ * The cache is u8 [pages][kv_heads][page_size * (D + D/16)], D channels a
+ * head.  A page of a head holds, one after another,
+ *   codes of the keys    [page_size][D/2]     e2m1, channel 2j in the low half of byte j
+ *   codes of the values  [page_size][D/2]
+ *   scales of the keys   [D/32][page_size]    ue8m0, one for 32 channels
+ *   scales of the values [D/32][page_size]
+ * and a value is code * 2^(scale - 127), the OCP MX formats' MXFP4.  D is 64,
+ * 128 or 256, page_size a multiple of 16 in 16 .. 512.  A slot names a
+ * token's place: page * page_size + its place in the page.  A cache of zero
+ * bytes holds zeros.
+ */
+
+/*
+ * Rotary positions: of q [T][q_heads][D] and k [T][k_heads][D] the pairs
+ * (a, b) of the first `rotary` channels turn by theta = p * inv_freq[i], p the
+ * token's position along the pair's axis:
+ *   a' = scale (a cos theta - b sin theta)
+ *   b' = scale (b cos theta + a sin theta)
+ * Pair i is channels i and i + rotary/2, or 2i and 2i + 1 if interleaved.
+ * inverse turns by -theta: with the same scale the gradient with regard to q
+ * and k of a loss, given that with regard to the outputs.  Channels from
+ * `rotary` on are copied.  theta is taken in binary64 and whole turns are
+ * left out there, so far positions lose nothing: sine and cosine are within
+ * 2^-22 (plus |p inv_freq| 2^-52) of the real angle's.  The rest is binary32,
+ * rounded once.
+ *   q, k        dtype (MHC_BF16 or MHC_F16); a token's heads q_head apart, its
+ *               channels dense, tokens q_token apart (elements), and so on: a
+ *               slice of a wider product's rows is fine.  k with k_heads > 0
+ *   q_out, k_out  likewise; may be q and k themselves with the same strides
+ *   positions   int32 or int64 (position_bytes 4 or 8) [axes][T], axes
+ *               position_axis elements apart; |p inv_freq| below 2^48
+ *   inv_freq    f32 [rotary/2]
+ *   pair_axis   HOST u8 [rotary/2], the axis of each pair, or NULL: all 0
+ * 1 <= D <= 512, rotary even, 2 .. D; axes 1 .. 4; heads 1 .. 4096; strides
+ * positive, heads of a token and tokens apart from each other; T < 2^31, the
+ * tensors' extents below 2^40 elements.  Tensors need the alignment of their
+ * elements; strides and addresses that are multiples of 16 bytes are fastest.
+ * Outputs overlap no input (but in place, or where rows lie side by side in
+ * one wider row) and not each other.
+ */
+typedef struct mhc_rope_args {
+    int64_t T;
+    int32_t q_heads;
+    int32_t k_heads;        /* 0: no k */
+    int32_t head_dim;
+    int32_t rotary;
+    int32_t dtype;          /* mhc_dtype of q, k and the outputs */
+    int32_t position_bytes; /* 4 or 8 */
+    int32_t axes;
+    int32_t interleaved;    /* 0 or 1 */
+    int32_t inverse;        /* 0 or 1 */
+    float scale;
+    int64_t position_axis;
+    int64_t q_token, q_head, k_token, k_head;
+    int64_t q_out_token, q_out_head, k_out_token, k_out_head;
+    const void *q;
+    const void *k;
+    const void *positions;
+    const float *inv_freq;
+    const uint8_t *pair_axis;
+    void *q_out;
+    void *k_out;
+} mhc_rope_args;
+
+int mhc_rope(const mhc_rope_args *args, void *stream);
+
+/*
+ * Quantises keys and values as they are written: token t's go to slot
+ * slots[t].  Of each 32 channels, with a = max |v|: e is the smallest whole
+ * number with 6 * 2^e >= a, in -125 .. 125 for bf16 and -23 .. 13 for fp16
+ * (the type then holds every value of the group's grid), scale byte e + 127;
+ * codes are v * 2^-e rounded to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6, ties
+ * to the even code, larger ones 6.  A group holding an infinity or NaN gets
+ * codes 0 and scale 255, which reads as NaN.
+ * A slot below 0 or past the cache writes nothing (padding).  The others
+ * have to differ: of two tokens given one slot it may hold part of each.
+ *   k, v    dtype (MHC_BF16 or MHC_F16) [T][heads][D], strides in elements as
+ *           in mhc_rope, multiples of 8; 16-byte aligned
+ *   slots   int32 or int64 (slot_bytes 4 or 8) [T]
+ * heads 1 .. 4096; pages * heads * page_size < 2^40; T * heads < 2^34, T <
+ * 2^31.  T == 0 does nothing.
+ */
+typedef struct mhc_cache_args {
+    int64_t T;
+    int64_t pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t head_dim;
+    int32_t dtype;
+    int32_t slot_bytes;     /* 4 or 8 */
+    int32_t reserved;       /* 0 */
+    int64_t k_token, k_head, v_token, v_head;
+    void *cache;            /* read only in mhc_cache_read */
+    const void *slots;
+    void *k;                /* read only in mhc_cache_write */
+    void *v;
+} mhc_cache_args;
+
+int mhc_cache_write(const mhc_cache_args *args, void *stream);
+
+/*
+ * The way back: k and v of token t are the values that slot slots[t] holds,
+ * rounded to dtype (exact for what that dtype wrote).  A slot below 0 or past
+ * the cache reads as zeros.  k or v may be NULL: not read.  Slots may repeat.
+ * k and v overlap neither the cache nor the slots nor each other.
+ */
+int mhc_cache_read(const mhc_cache_args *args, void *stream);
+
+/*
+ * Attention of ragged sequences' queries over the cache.  Sequence b has the
+ * query rows q_starts[b] .. q_starts[b + 1] of q [T][q_heads][D], n of them,
+ * which are its last n tokens, and lens[b] cached tokens, token t on page
+ * tables[b][t / page_size].  Query head h reads kv head h / (q_heads /
+ * kv_heads).  Row i of n, at token p = lens[b] - n + i, sees the tokens
+ *   t < lens[b],  t <= p if causal,  t > p - window if window > 0
+ *   s_t = scale (q . k_t);  with softcap c > 0: c tanh(s_t / c)
+ *   out = sum_t exp(s_t) v_t / sum_t exp(s_t),   lse = log sum_t exp(s_t)
+ * A row that sees nothing has out 0 and lse -inf.  What no row sees may hold
+ * anything, NaN too.
+ * Scores, sums and the output are held in binary32; products take q and the
+ * cache's values as they are and exp(s - max) rounded to dtype (with 2^12
+ * before it in fp16, whose smallest numbers would end it at 2^-24), which
+ * costs what one rounding of the output costs.  Results do not depend on what
+ * else runs; they may in the last bits on the other sequences of the call,
+ * since those decide where a sequence's tokens are split.
+ *   q          dtype (MHC_BF16 or MHC_F16), strides in elements, multiples of
+ *              8; 16-byte aligned
+ *   cache      as above; 16-byte aligned.  To be read in the type it was
+ *              written in, or in fp16 where its values are in fp16's range
+ *   tables     int32 [B][table_width], rows table_stride apart.  A page
+ *              outside 0 .. pages - 1 hides its tokens
+ *   lens       int32 [B]; below 0 counts as 0, past max_len or the table as
+ *              those.  max_len 0: what the table holds
+ *   q_starts   int32 [B + 1], not falling, or NULL: T == B, one row each.
+ *              Rows outside every sequence are left as they were
+ *   out        dtype [T][q_heads][D], dense, 16-byte aligned
+ *   lse        f32 [T][q_heads] or NULL
+ *   workspace  16-byte aligned, as many bytes as mhc_cache_attention_workspace
+ *              says.  Nothing has to be in it, nothing is kept in it; calls
+ *              that may overlap need one each, and so do graphs that may
+ * kv_heads divides q_heads, q_heads up to 4096; B up to 65535;
+ * table_width * page_size < 2^31; pages * kv_heads < 2^31.
+ * T == 0 or B == 0 does nothing.
+ */
+typedef struct mhc_cache_attention_args {
+    int64_t T;
+    int64_t max_len;
+    int64_t pages;
+    int64_t q_token, q_head;
+    int64_t table_stride;
+    int32_t B;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t table_width;
+    int32_t dtype;
+    int32_t causal;         /* 0 or 1 */
+    int32_t window;
+    float scale;
+    float softcap;
+    int32_t reserved;       /* 0 */
+    const void *q;
+    const uint8_t *cache;
+    const int32_t *tables;
+    const int32_t *lens;
+    const int32_t *q_starts;
+    void *out;
+    float *lse;
+    void *workspace;
+    uint64_t workspace_bytes;
+} mhc_cache_attention_args;
+
+int mhc_cache_attention(const mhc_cache_attention_args *args, void *stream);
+
+/*
+ * Bytes of workspace for such a call: a function of T, B, q_heads, kv_heads,
+ * head_dim and cu_count (the device's compute units) alone.  Host only.
+ * INVALID_ARG for sizes that the call itself refuses.
+ */
+int mhc_cache_attention_workspace(int64_t T, int32_t B, int32_t q_heads, int32_t kv_heads,
+                                  int32_t head_dim, int32_t cu_count, uint64_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

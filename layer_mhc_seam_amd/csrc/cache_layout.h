@@ -1,0 +1,90 @@
+// cache_layout.h -- where a token's codes and scales lie in the 4-bit cache
+// u8 [pages][heads][page_size * (D + D/16)]: of each page and head the keys'
+// codes [page_size][D/2], the values' codes, the keys' scales
+// [D/32][page_size], the values' scales.  Plain C++, for the kernels and for
+// host code alike.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIP__)
+#define MHC_BOTH __host__ __device__ __forceinline__
+#else
+#define MHC_BOTH inline
+#endif
+
+namespace mhc {
+
+constexpr int kCacheTile = 16;       // tokens that never straddle two pages
+constexpr int kCacheMaxPage = 512;   // tokens a page
+
+struct CacheLayout {
+    int64_t pages;
+    int32_t heads;
+    int32_t page_size;
+    uint64_t magic;                  // ceil(2^63 / (page_size / 16))
+};
+
+MHC_BOTH CacheLayout cache_layout(int64_t pages, int32_t heads, int32_t page_size)
+{
+    const uint64_t tiles = (uint64_t)page_size / kCacheTile;
+    return {pages, heads, page_size, ((uint64_t(1) << 63) + tiles - 1) / tiles};
+}
+
+MHC_BOTH uint64_t high_product(uint64_t a, uint64_t b)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __umul64hi(a, b);
+#else
+    return (uint64_t)((unsigned __int128)a * b >> 64);
+#endif
+}
+
+// Bytes of one head's page, and where its four parts begin
+MHC_BOTH constexpr uint32_t cache_page_bytes(int ps, int D) { return (uint32_t)(ps * (D + D / 16)); }
+MHC_BOTH constexpr uint32_t cache_codes(int ps, int D, int kind) { return (uint32_t)(kind * ps * (D / 2)); }
+MHC_BOTH constexpr uint32_t cache_scales(int ps, int D, int kind)
+{
+    return (uint32_t)(ps * D + kind * ps * (D / 32));
+}
+
+// Page of token (or slot) t and its place there.  The quotient is exact: with
+// d = page_size / 16 <= 32 and u = t / 16 < 2^36, magic exceeds 2^63 / d by
+// less than 1, so 2u magic / 2^64 exceeds u / d by less than 2^-26 < 1 / d.
+MHC_BOTH void cache_place(const CacheLayout &c, uint64_t t, int64_t *page, int32_t *at)
+{
+    const uint64_t p = high_product((t / kCacheTile) * 2, c.magic);
+    *page = (int64_t)p;
+    *at = (int32_t)(t - p * (uint64_t)c.page_size);
+}
+
+// Place of a slot; false for one that is not in the cache
+MHC_BOTH bool cache_slot(const CacheLayout &c, int64_t slot, int64_t *page, int32_t *at)
+{
+    if (slot < 0 || slot >= c.pages * c.page_size)
+        return false;
+    cache_place(c, (uint64_t)slot, page, at);
+    return true;
+}
+
+// First byte of a head's page
+MHC_BOTH int64_t cache_page_at(const CacheLayout &c, int64_t page, int head, int D)
+{
+    return (page * c.heads + head) * (int64_t)cache_page_bytes(c.page_size, D);
+}
+
+// The page that a sequence's tokens [t, t + 16), t a multiple of 16, lie on, and
+// where: false, reading no table, where the sequence has none there, and where
+// the table names a page that there is not
+MHC_BOTH bool cache_tile(const CacheLayout &c, const int32_t *table, int64_t len, int64_t t,
+                         int64_t *page, int32_t *at)
+{
+    if (t >= len)
+        return false;
+    int64_t i;
+    cache_place(c, (uint64_t)t, &i, at);
+    *page = table[i];
+    return *page >= 0 && *page < c.pages;
+}
+
+}  // namespace mhc

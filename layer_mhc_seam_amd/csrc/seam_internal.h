@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/mhc_seam.h"
+#include "cache_layout.h"
 
 namespace mhc {
 
@@ -135,6 +136,62 @@ struct RouteParams {
     float scale;
 };
 hipError_t launch_route(const RouteParams &p, int64_t tokens, int dtype, hipStream_t s);
+
+// Rotary positions (rope_kernels.hip)
+struct RopeParams {
+    int64_t T;
+    int q_heads, k_heads, head_dim, rotary;
+    int inverse, position_bytes;
+    float scale;
+    int units;                // of a head: pairs by the vector, and channels to copy
+    int head_steps;           // threads that share a unit of a token, heads dealt out in turn
+    int64_t position_axis;
+    int64_t q_token, q_head, k_token, k_head, q_out_token, q_out_head, k_out_token, k_out_head;
+    const uint16_t *q;
+    const uint16_t *k;
+    const void *positions;
+    const float *inv_freq;
+    uint16_t *q_out;
+    uint16_t *k_out;
+    uint32_t axis[16];        // two bits a pair
+};
+hipError_t launch_rope(RopeParams p, int dtype, int vector, bool interleaved, bool in_place, int cus, hipStream_t s);
+
+// The 4-bit cache (cache_kernels.hip)
+struct CacheParams {
+    CacheLayout c;
+    int64_t T;
+    int slot_bytes;
+    int64_t k_token, k_head, v_token, v_head;
+    uint8_t *cache;
+    const void *slots;
+    void *k;
+    void *v;
+};
+hipError_t launch_cache(const CacheParams &p, int head_dim, int dtype, bool write, hipStream_t s);
+
+// Attention over it (attention_kernels.hip)
+struct AttentionParams {
+    CacheLayout c;
+    int64_t T, max_len;       // max_len: no more than the tables hold
+    int64_t q_token, q_head, table_stride;
+    int B, q_heads, group;    // group: query heads a kv head
+    int causal, window;
+    float scale, softcap;
+    const uint16_t *q;
+    const uint8_t *cache;
+    const int32_t *tables;
+    const int32_t *lens;
+    const int32_t *q_starts;
+    uint16_t *out;
+    float *lse;
+    float *workspace;
+    int workers;
+    int64_t blocks;           // row blocks that the batch may have
+};
+// Floats of workspace and the launch, which takes as many
+uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus);
+hipError_t launch_attention(const AttentionParams &p, int head_dim, int dtype, int cus, hipStream_t s);
 
 hipError_t launch_quantize(const uint16_t *src, int rows, int H, int group, uint8_t *codes,
                            uint8_t *scales, uint16_t *grid, hipStream_t s);

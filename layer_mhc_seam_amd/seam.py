@@ -67,12 +67,50 @@ class RouteArgs(ctypes.Structure):
                 ("logits", _P), ("bias", _P), ("weights", _P), ("ids", _P)]
 
 
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("position_bytes", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("position_axis", ctypes.c_int64),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("q_out_token", ctypes.c_int64), ("q_out_head", ctypes.c_int64),
+                ("k_out_token", ctypes.c_int64), ("k_out_head", ctypes.c_int64),
+                ("q", _P), ("k", _P), ("positions", _P), ("inv_freq", _P), ("pair_axis", _P),
+                ("q_out", _P), ("k_out", _P)]
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("slot_bytes", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("k_token", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_token", ctypes.c_int64),
+                ("v_head", ctypes.c_int64), ("cache", _P), ("slots", _P), ("k", _P), ("v", _P)]
+
+
+class CacheAttentionArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("max_len", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("B", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("q", _P), ("cache", _P), ("tables", _P), ("lens", _P), ("q_starts", _P),
+                ("out", _P), ("lse", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_uint64)]
+
+
 EXPORTS = ("mhc_seam_create", "mhc_seam_run", "mhc_seam_run_noalloc", "mhc_seam_destroy",
            "mhc_seam_validate",
            "mhc_seam_plan_for", "mhc_seam_status_string", "mhc_seam_last_error",
            "mhc_seam_copy", "mhc_stream_mix", "mhc_seam_quantize", "mhc_head_reduce",
            "mhc_mxfp8_gemm", "mhc_mxfp8_gemm_blocks", "mhc_block_norm", "mhc_int8_quantize",
-           "mhc_int8_gemm", "mhc_int8_gemm_blocks", "mhc_route")
+           "mhc_int8_gemm", "mhc_int8_gemm_blocks", "mhc_route", "mhc_rope", "mhc_cache_write",
+           "mhc_cache_read", "mhc_cache_attention", "mhc_cache_attention_workspace")
 
 _lib = None
 
@@ -121,8 +159,15 @@ def lib():
     L.mhc_int8_gemm_blocks.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                        ctypes.POINTER(ctypes.c_int32),
                                        ctypes.POINTER(ctypes.c_int32)]
+    L.mhc_rope.argtypes = [ctypes.POINTER(RopeArgs), _P]
+    L.mhc_cache_write.argtypes = [ctypes.POINTER(CacheArgs), _P]
+    L.mhc_cache_read.argtypes = [ctypes.POINTER(CacheArgs), _P]
+    L.mhc_cache_attention.argtypes = [ctypes.POINTER(CacheAttentionArgs), _P]
+    L.mhc_cache_attention_workspace.argtypes = [ctypes.c_int64, *[ctypes.c_int32] * 5,
+                                                ctypes.POINTER(ctypes.c_uint64)]
     for name in ("mhc_block_norm", "mhc_int8_quantize", "mhc_int8_gemm", "mhc_int8_gemm_blocks",
-                 "mhc_route"):
+                 "mhc_route", "mhc_rope", "mhc_cache_write", "mhc_cache_read",
+                 "mhc_cache_attention", "mhc_cache_attention_workspace"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("mhc_seam_create", "mhc_seam_run", "mhc_seam_run_noalloc", "mhc_seam_destroy",
                  "mhc_seam_validate",
@@ -654,3 +699,271 @@ def route(logits, k, *, scoring="softmax", bias=None, groups=1, topk_groups=1, g
                   weights.data_ptr(), ids.data_ptr())
     _enqueue(index, lib().mhc_route, ctypes.byref(a))
     return weights, ids
+
+
+# ------------------------------------------- attention over a 4-bit cache --
+#
+# Streams and devices as above.  q, k and v may be slices of wider rows, a
+# qkv product's say: their channels are dense, strides else are free.
+
+def _head_strides(name, t, dtype, shape, index):
+    """(token, head) strides of t, [T, heads, D] of that type and shape on that
+    device with dense channels.  An axis of one takes the stride it would have."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be a tensor on cuda:{index}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    token, head, channel = t.stride()
+    if channel != 1 and shape[2] > 1:
+        raise ValueError(f"{name}'s channels must be dense")
+    if shape[1] == 1:
+        head = shape[2]
+    if shape[0] <= 1:
+        token = head * shape[1]
+    return token, head
+
+
+@functools.lru_cache(maxsize=64)
+def _pair_axes(axes, pairs, most):
+    """axes, one for each pair, as the library's bytes."""
+    if len(axes) != pairs or any(type(a) is not int or not 0 <= a < most for a in axes):
+        raise ValueError(f"axes must be {pairs} whole numbers from 0 to {most - 1}")
+    return (ctypes.c_uint8 * pairs)(*axes)
+
+
+_WHOLE = {}
+
+
+def _whole_bytes(name, t):
+    """Bytes of int32 or int64 elements."""
+    if not _WHOLE:
+        import torch
+        _WHOLE.update({torch.int32: 4, torch.int64: 8})
+    size = _WHOLE.get(t.dtype)
+    if size is None:
+        raise ValueError(f"{name} must be int32 or int64, got {t.dtype}")
+    return size
+
+
+def rope(q, k, positions, inv_freq, *, axes=None, interleaved=False, inverse=False, scale=1.0,
+         out=None, stream=None):
+    """Rotary positions: pair i of the first 2 len(inv_freq) channels of q
+    [T, Hq, D] and k [T, Hk, D] (bf16 or f16; k may be None) turns by
+    positions * inv_freq[i] and is multiplied with scale; pairs are channels i
+    and i + len(inv_freq), or 2 i and 2 i + 1 if interleaved.  positions [T],
+    or [A, T] for up to four axes (time, height, width), of which axes[i] is
+    pair i's: [0] * 16 + [1] * 24 + [2] * 24, or 0, 1, 2 in turn.  int32 or
+    int64, any size: theta is taken in 64 bits.  inv_freq f32 [R / 2].
+    inverse turns the other way: rope(dq, dk, ..., inverse=True) is the
+    gradient.
+    Returns (q', k'), dense, or written to the pair given in `out`, (q, k)
+    itself for one."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, rope, q, k, positions, inv_freq, axes=axes,
+                          interleaved=interleaved, inverse=inverse, scale=scale, out=out)
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k must be [T, heads, D]")
+    if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
+        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+    T, Hq, D = q.shape
+    Hk = 0 if k is None else k.shape[1]
+    pairs = inv_freq.numel()
+    _fits(Hq | Hk | D | pairs * 2)
+    index = q.get_device()
+    dt = q.dtype
+    qs = _head_strides("q", q, dt, q.shape, index)
+    _need("inv_freq", inv_freq, torch.float32, (pairs,), index)
+    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        raise ValueError(f"positions must be [{T}] or [axes, {T}], got {tuple(positions.shape)}")
+    if positions.get_device() != index:
+        raise ValueError(f"positions must be a tensor on cuda:{index}")
+    most = positions.shape[0] if positions.dim() == 2 else 1
+    if T > 1 and positions.stride(-1) != 1:
+        raise ValueError("each axis of positions must be dense")
+    of_axis = positions.stride(0) if most > 1 else T
+    table = None if axes is None else _pair_axes(tuple(axes), pairs, most)
+    ks = (0, 0)
+    if k is not None:
+        ks = _head_strides("k", k, dt, (T, Hk, D), index)
+        if Hk == 0:
+            raise ValueError("k has no heads: give None")
+    if out is None:
+        qo = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        ko = None if k is None else torch.empty((T, Hk, D), dtype=dt, device=q.device)
+        qos, kos = (Hq * D, D), (Hk * D, D)
+    else:
+        qo, ko = out
+        if (ko is None) != (k is None):
+            raise ValueError("out must be a pair (q, k), k None exactly where k is")
+        qos = _head_strides("out's q", qo, dt, (T, Hq, D), index)
+        kos = (0, 0) if ko is None else _head_strides("out's k", ko, dt, (T, Hk, D), index)
+    a = RopeArgs(T, Hq, Hk, D, 2 * pairs, _types()[1][dt], _whole_bytes("positions", positions), most,
+                 bool(interleaved), bool(inverse), scale, of_axis, *qs, *ks, *qos, *kos,
+                 q.data_ptr(), _address(k), positions.data_ptr(), inv_freq.data_ptr(),
+                 None if table is None else ctypes.addressof(table), qo.data_ptr(), _address(ko))
+    _enqueue(index, lib().mhc_rope, ctypes.byref(a))
+    return qo, ko
+
+
+def kv_cache(pages, heads, head_dim, page_size=64, *, device="cuda"):
+    """An empty 4-bit cache: u8 [pages, heads, page_size * (head_dim +
+    head_dim / 16)] of zeros, codes and scales of keys and values.  Slot
+    page * page_size + i is place i of a page.  head_dim 64, 128 or 256,
+    page_size a multiple of 16 up to 512."""
+    import torch
+    if head_dim not in (64, 128, 256) or page_size not in range(16, 513, 16):
+        raise ValueError("head_dim must be 64, 128 or 256, page_size a multiple of 16 up to 512")
+    return torch.zeros((pages, heads, page_size * (head_dim + head_dim // 16)), dtype=torch.uint8,
+                       device=device)
+
+
+def _cache_sizes(cache, heads, D, index):
+    """(pages, page_size) of a cache for those heads."""
+    import torch
+    if cache.dim() != 3:
+        raise ValueError("cache must be [pages, heads, bytes of a page]")
+    pages, H, each = cache.shape
+    token = D + D // 16
+    if H != heads or each == 0 or each % (16 * token):    # pages of whole 16 tokens
+        raise ValueError(f"cache {tuple(cache.shape)} does not hold {heads} heads of {D} channels")
+    _need("cache", cache, torch.uint8, cache.shape, index)
+    return pages, each // token
+
+
+def cache_write(cache, k, v, slots, *, stream=None):
+    """Quantises k and v [T, H, D] (bf16 or f16) into slots [T] (int32 or
+    int64) of the cache: 4-bit codes, one power of two for 32 channels.  A slot
+    below 0 or past the cache writes nothing; the others must differ.  Returns
+    the cache."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, cache_write, cache, k, v, slots)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [T, heads, D]")
+    dt = k.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError(f"k and v must be bfloat16 or float16, got {dt}")
+    T, H, D = shape = k.shape
+    _fits(H | D)
+    index = k.get_device()
+    ks, vs = _head_strides("k", k, dt, shape, index), _head_strides("v", v, dt, shape, index)
+    pages, ps = _cache_sizes(cache, H, D, index)
+    _need("slots", slots, slots.dtype, (T,), index)
+    a = CacheArgs(T, pages, ps, H, D, _types()[1][dt], _whole_bytes("slots", slots), 0, *ks, *vs,
+                  cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr())
+    _enqueue(index, lib().mhc_cache_write, ctypes.byref(a))
+    return cache
+
+
+def cache_read(cache, slots, head_dim, *, dtype="bf16", out=None, stream=None):
+    """k and v [T, H, head_dim] of the cache's slots [T] (int32 or int64), in
+    bf16 or f16.  A slot below 0 or past the cache reads as zeros.  out: the
+    pair to write to."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, cache_read, cache, slots, head_dim, dtype=dtype, out=out)
+    if slots.dim() != 1 or cache.dim() != 3:
+        raise ValueError("slots must be [T] and cache [pages, heads, bytes of a page]")
+    if dtype not in ("bf16", "f16"):
+        raise ValueError("dtype must be bf16 or f16")
+    T, H = slots.shape[0], cache.shape[1]
+    _fits(H | head_dim)
+    index = cache.get_device()
+    pages, ps = _cache_sizes(cache, H, head_dim, index)
+    _need("slots", slots, slots.dtype, (T,), index)
+    dt, shape = _types()[0][dtype], (T, H, head_dim)
+    if out is None:
+        k = torch.empty(shape, dtype=dt, device=cache.device)
+        v = torch.empty(shape, dtype=dt, device=cache.device)
+        ks = vs = (H * head_dim, head_dim)
+    else:
+        k, v = out
+        ks, vs = _head_strides("k", k, dt, shape, index), _head_strides("v", v, dt, shape, index)
+    a = CacheArgs(T, pages, ps, H, head_dim, DTYPES[dtype], _whole_bytes("slots", slots), 0, *ks, *vs,
+                  cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr())
+    _enqueue(index, lib().mhc_cache_read, ctypes.byref(a))
+    return k, v
+
+
+@functools.lru_cache(maxsize=None)
+def _compute_units(index):
+    import torch
+    return torch.cuda.get_device_properties(index).multi_processor_count
+
+
+@functools.lru_cache(maxsize=4096)
+def cache_attention_workspace(T, B, q_heads, kv_heads, head_dim, cu_count=256):
+    """Bytes of workspace that cache_attention takes for T query rows in B
+    sequences (host only)."""
+    _fits(B | q_heads | kv_heads | head_dim | cu_count)
+    n = ctypes.c_uint64()
+    _check(lib().mhc_cache_attention_workspace(T, B, q_heads, kv_heads, head_dim, cu_count,
+                                               ctypes.byref(n)))
+    return n.value
+
+
+def cache_attention(q, cache, tables, lens, *, q_starts=None, scale=None, causal=True, window=0,
+                    softcap=0.0, lse=False, max_len=None, out=None, stream=None):
+    """Attention of q [T, Hq, D] (bf16 or f16) over the 4-bit cache.  Sequence b
+    has lens[b] tokens (int32 [B]), token t on page tables[b, t // page_size]
+    (int32 [B, pages a sequence may have]), and the query rows q_starts[b] ..
+    q_starts[b + 1] (int32 [B + 1]), which are its last tokens; without
+    q_starts one row each.  Query head h reads kv head h // (Hq / Hkv).  A row
+    sees the tokens up to its own (causal) or all, the last `window` of them
+    if window > 0; scores are q . k * scale (D ** -0.5), capped by softcap *
+    tanh(s / softcap) if softcap > 0.  Rows that see nothing are 0.
+    max_len: no sequence is longer, or is cut there.
+    Returns out [T, Hq, D] in q's type, and with lse the logarithms of the sums
+    too (f32 [T, Hq]), by which parts over different tokens can be joined.  out:
+    the tensor, or with lse the pair, to write to; rows that belong to no
+    sequence are left as they are."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, cache_attention, q, cache, tables, lens, q_starts=q_starts,
+                          scale=scale, causal=causal, window=window, softcap=softcap, lse=lse,
+                          max_len=max_len, out=out)
+    if q.dim() != 3 or cache.dim() != 3 or tables.dim() != 2:
+        raise ValueError("q must be [T, heads, D], cache [pages, heads, bytes], tables [B, pages]")
+    dt = q.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError(f"q must be bfloat16 or float16, got {dt}")
+    T, Hq, D = shape = q.shape
+    B, width = tables.shape
+    Hk = cache.shape[1]
+    most = 0 if max_len is None else max_len
+    _fits(Hq | D | B | width | window)
+    index = q.get_device()
+    qs = _head_strides("q", q, dt, shape, index)
+    pages, ps = _cache_sizes(cache, Hk, D, index)
+    if tables.dtype is not torch.int32 or tables.get_device() != index \
+            or (width > 1 and tables.stride(1) != 1):
+        raise ValueError(f"tables must be int32 with dense rows on cuda:{index}")
+    _need("lens", lens, torch.int32, (B,), index)
+    if q_starts is not None:
+        _need("q_starts", q_starts, torch.int32, (B + 1,), index)
+    if max_len is not None and max_len < 1:
+        raise ValueError("max_len must be positive")
+    sums = None
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=q.device)
+        if lse:
+            sums = _new(T, Hq, torch.float32, q.device)
+    else:
+        if lse:
+            out, sums = out
+            _need("lse", sums, torch.float32, (T, Hq), index)
+        _need("out", out, dt, shape, index)
+    size = cache_attention_workspace(T, B, Hq, Hk, D, _compute_units(index))
+    space = torch.empty((size,), dtype=torch.uint8, device=q.device) if size else None
+    a = CacheAttentionArgs(T, most, pages, *qs, tables.stride(0) if B > 1 else width, B, Hq, Hk, D, ps,
+                           width, _types()[1][dt], bool(causal), window,
+                           D ** -0.5 if scale is None else scale, softcap, 0, q.data_ptr(),
+                           cache.data_ptr(), tables.data_ptr(), lens.data_ptr(), _address(q_starts),
+                           out.data_ptr(), _address(sums), _address(space), size)
+    _enqueue(index, lib().mhc_cache_attention, ctypes.byref(a))
+    return (out, sums) if lse else out

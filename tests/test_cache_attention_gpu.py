@@ -1,0 +1,336 @@
+"""Attention over the 4-bit cache against its definition in 64 bits: head layouts and widths, lengths from none to
+several thousand, ragged queries, masks that leave rows empty, NaN where nobody looks, bad pages, both ways the work
+is split.  The tolerance is derived in cache_reference.attention: a rounding of the output and of the weights, and
+the binary32 sums."""
+import math
+
+import pytest
+import torch
+
+import cache_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF, F16, F64 = torch.bfloat16, torch.float16, torch.float64
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def batch(lens, rows, Hq, Hk, D, ps, dt, seed=0, width=None, sharp=1.0):
+    """A cache of shuffled pages: (device tensors, host keys, values)."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // ps) for n in lens]
+    width = width or max(max(need), 1)
+    pages = sum(need) + 2
+    order = torch.randperm(pages, generator=g)
+    tables = torch.full((len(lens), width), -7, dtype=torch.int32)
+    at, keys, values, slots, ks, vs = 0, [], [], [], [], []
+    for b, n in enumerate(lens):
+        mine = order[at:at + need[b]]
+        at += need[b]
+        tables[b, :need[b]] = mine.to(torch.int32)
+        ks.append(torch.randn(n, Hk, D, generator=g).to(dt))
+        vs.append((torch.randn(n, Hk, D, generator=g) * torch.exp(torch.randn(n, Hk, 1, generator=g))).to(dt))
+        t = torch.arange(n)
+        slots.append(mine[t // ps] * ps + t % ps if n else t)
+    cache, hk, hv = ref.packed(torch.cat(ks), torch.cat(vs), torch.cat(slots), pages, ps)
+    first = 0
+    for n in lens:
+        keys.append(hk[first:first + n])
+        values.append(hv[first:first + n])
+        first += n
+    starts = [0]
+    for n in rows:
+        starts.append(starts[-1] + n)
+    q = (sharp * torch.randn(starts[-1], Hq, D, generator=g)).to(dt)
+    return dict(q=q, cache=cache, tables=tables, lens=torch.tensor(lens, dtype=torch.int32),
+                starts=starts), keys, values
+
+
+def run(d, single=False, **kw):
+    from layer_mhc_seam_amd import seam as S
+    starts = None if single else torch.tensor(d["starts"], dtype=torch.int32).cuda()
+    return S.cache_attention(d["q"].cuda(), d["cache"].cuda(), d["tables"].cuda(), d["lens"].cuda(),
+                             q_starts=starts, lse=True, **kw)
+
+
+def check(got, want, first=0):
+    out, lse = (x.cpu().to(F64) for x in got)
+    w, l, bound, lbound = want
+    assert torch.equal(out.isnan(), w.isnan())
+    off = (out - w).abs().nan_to_num(0)
+    assert (off <= bound.nan_to_num(0)).all(), (off / bound).nan_to_num(0).max()
+    fine = l.isfinite()
+    assert torch.equal(lse[~fine].nan_to_num(nan=5.0), l[~fine].nan_to_num(nan=5.0))
+    assert ((lse - l).abs()[fine] <= lbound[fine]).all(), ((lse - l).abs() / lbound)[fine].max()
+
+
+def both(lens, rows, Hq, Hk, D, ps, dt, seed=0, sharp=1.0, width=None, visible=None, **kw):
+    d, keys, values = batch(lens, rows, Hq, Hk, D, ps, dt, seed, sharp=sharp, width=width)
+    single = all(n == 1 for n in rows)
+    want = ref.attention(d["q"], keys, values, lens, d["starts"], visible, **kw)
+    got = run(d, single=single, **kw)
+    check(got, want)
+    if single:
+        again = run(d, **kw)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    return d, got
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (8, 8), (10, 2), (16, 1), (40, 2)])
+def test_one_token(D, Hq, Hk, dt):
+    both([1, 200, 33, 0, 64], [1] * 5, Hq, Hk, D, 16, dt)
+
+
+@pytest.mark.parametrize("L", [1, 2, 15, 16, 17, 31, 32, 33, 127, 128, 129, 255, 256, 1003, 4097])
+@pytest.mark.parametrize("dt", [BF, F16])
+def test_lengths(L, dt):
+    both([L], [1], 6, 2, 128, 48, dt, seed=L)
+
+
+@pytest.mark.parametrize("ps", [16, 32, 48, 80, 256, 512])
+def test_page_sizes(ps):
+    both([700, 3, ps, ps + 1], [1] * 4, 4, 1, 64, ps, BF)
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal,window,softcap", [(True, 0, 0.0), (False, 0, 0.0), (True, 50, 0.0), (False, 20, 8.0),
+                                                   (True, 1, 30.0), (True, 0, 5.0)])
+def test_ragged_rows(causal, window, softcap, D, dt):
+    """One to many query rows a sequence, none too, and more than its tokens."""
+    both([90, 200, 41, 5, 0, 130], [7, 1, 41, 0, 3, 20], 6, 2, D, 32, dt, causal=causal, window=window,
+         softcap=softcap)
+    both([3, 70], [9, 2], 5, 5, D, 16, dt, causal=causal, window=window, softcap=softcap)
+
+
+@pytest.mark.parametrize("T,L,Hq,Hk", [(200, 333, 4, 1), (64, 64, 8, 1), (300, 300, 3, 3), (17, 1500, 16, 2)])
+@pytest.mark.parametrize("dt", [BF, F16])
+def test_prompts(T, L, Hq, Hk, dt):
+    both([L, 20, 77], [T, 20, 1], Hq, Hk, 128, 64, dt)
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
+def test_sharp_scores(dt):
+    """Scores far apart: a maximum that moves often, weights that vanish."""
+    both([600, 50], [3, 50], 4, 2, 128, 16, dt, sharp=30.0)
+    both([600, 50], [1, 1], 4, 2, 64, 16, dt, sharp=200.0)
+    both([600, 50], [1, 1], 4, 2, 64, 16, dt, scale=-0.3)
+    both([600, 50], [1, 1], 4, 2, 64, 16, dt, scale=0.0)
+
+
+def test_rising_maximum():
+    """Scores that rise along the sequence, by less and by more than the slack, and fall again."""
+    for slope in (0.02, 0.3, 5.0, -0.3):
+        d, keys, values = batch([900], [1], 1, 1, 64, 16, BF, seed=3)
+        k = torch.zeros(900, 1, 64, dtype=BF)
+        k[:, 0, 0] = (torch.arange(900) * slope).to(BF)
+        v = torch.randn(900, 1, 64, generator=torch.Generator().manual_seed(1)).to(BF)
+        t = torch.arange(900)
+        slots = d["tables"][0][t // 16].long() * 16 + t % 16
+        d["cache"], hk, hv = ref.packed(k, v, slots, d["cache"].shape[0], 16)
+        d["q"] = torch.zeros(1, 1, 64, dtype=BF)
+        d["q"][0, 0, 0] = 1.0
+        check(run(d, scale=1.0), ref.attention(d["q"], [hk], [hv], [900], [0, 1], scale=1.0))
+
+
+def test_many_tiny_weights():
+    """One token far above thousands of others, whose weights of 2^-22 and below add up: fp16 keeps them."""
+    n = 6000
+    d, _, _ = batch([n], [1], 1, 1, 64, 512, F16, seed=3)
+    k = torch.zeros(n, 1, 64, dtype=F16)
+    k[0, 0, 0] = 1.0
+    v = torch.ones(n, 1, 64, dtype=F16)
+    v[0] = 0
+    t = torch.arange(n)
+    slots = d["tables"][0][t // 512].long() * 512 + t % 512
+    d["cache"], hk, hv = ref.packed(k, v, slots, d["cache"].shape[0], 512)
+    d["q"] = torch.zeros(1, 1, 64, dtype=F16)
+    for gap in (14.0, 17.0, 19.0):
+        d["q"][0, 0, 0] = gap
+        got = run(d, scale=1.0)
+        want = ref.attention(d["q"], [hk], [hv], [n], [0, 1], scale=1.0)
+        check(got, want)
+        assert ((got[0].cpu().double() / want[0] - 1).abs() < 2.0 ** -8).all() or want[0].max() < 2.0 ** -14
+
+
+def put(d, b, t, kind, D, ps, block, byte=255):
+    """A scale byte of one token, in the bytes."""
+    page, at = int(d["tables"][b, t // ps]), t % ps
+    base = ps * D + kind * ps * D // 32
+    d["cache"][page, :, base + block * ps + at] = byte
+    codes = kind * ps * D // 2 + at * D // 2 + block * 16
+    d["cache"][page, :, codes:codes + 16] = 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dt", [BF, F16])
+def test_nan_reaches_who_sees_it(D, dt):
+    """A NaN in a key makes the rows that see it NaN, one in a value only its 32 channels of them."""
+    lens, rows, ps = [70, 140, 300], [30, 4, 1], 16
+    d, keys, values = batch(lens, rows, 4, 2, D, ps, dt, seed=9)
+    for b, t, kind, block in ((0, 45, 1, 1), (0, 60, 0, 0), (1, 138, 1, D // 32 - 1), (1, 139, 0, 1), (2, 20, 1, 0),
+                              (2, 133, 1, 1)):
+        put(d, b, t, kind, D, ps, block)
+        (values if kind else keys)[b][t, :, block * 32:block * 32 + 32] = math.nan
+    got = run(d)
+    out, lse = got[0].cpu().to(F64), got[1].cpu().to(F64)
+    w, l, bound, lbound = ref.attention(d["q"], keys, values, lens, d["starts"])
+    assert torch.equal(out.isnan(), w.isnan()) and torch.equal(lse.isnan(), l.isnan())
+    assert w.isnan().any() and not w.isnan().all(dim=(1, 2))[:15].any()
+    fine = ~w.isnan()
+    assert ((out - w).abs()[fine] <= bound[fine]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_what_nobody_sees_may_be_anything(D):
+    """Bytes of 255 everywhere but in the tokens: behind the last one, in other pages, before a window."""
+    lens, rows, ps = [70, 129, 1, 260], [1, 3, 1, 2], 32
+    for kw in ({}, dict(window=40)):
+        d, keys, values = batch(lens, rows, 4, 2, D, ps, BF, seed=2)
+        clean = run(d, **kw)
+        dirty = torch.full_like(d["cache"], 255)
+        for b, n in enumerate(lens):
+            for t in range(max(0, n - rows[b] + 1 - kw.get("window", n)), n):
+                page, at = int(d["tables"][b, t // ps]), t % ps
+                for kind in range(2):
+                    c = kind * ps * D // 2 + at * D // 2
+                    s = ps * D + kind * ps * D // 32 + torch.arange(D // 32) * ps + at
+                    dirty[page, :, c:c + D // 2] = d["cache"][page, :, c:c + D // 2]
+                    dirty[page, :, s] = d["cache"][page, :, s]
+        d["cache"] = dirty
+        got = run(d, **kw)
+        assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+
+
+def test_bad_pages_hide_their_tokens():
+    lens, rows, ps, D = [100, 64, 40], [3, 1, 1], 16, 128
+    d, keys, values = batch(lens, rows, 4, 2, D, ps, BF, seed=4)
+    seen = [torch.ones(n, dtype=torch.bool) for n in lens]
+    pages = d["cache"].shape[0]
+    for b, page, bad in ((0, 2, -1), (0, 6, pages), (1, 0, 2 ** 31 - 1), (1, 3, -2 ** 31), (2, 0, pages + 5),
+                         (2, 1, -3), (2, 2, 10 ** 6)):
+        d["tables"][b, page] = bad
+        seen[b][page * ps:(page + 1) * ps] = False
+    want = ref.attention(d["q"], keys, values, lens, d["starts"], seen)
+    assert (want[0][-1] == 0).all()               # a sequence with no page left
+    check(run(d), want)
+
+
+def test_lengths_and_rows_that_do_not_fit():
+    """Lengths below none and past the table, starts that fall or pass the rows, rows behind the last sequence."""
+    from layer_mhc_seam_amd import seam as S
+    lens, rows, ps, D = [64, 64, 30], [1, 1, 1], 16, 64
+    d, keys, values = batch(lens, rows, 4, 2, D, ps, BF, seed=5)
+    want = ref.attention(d["q"], keys, values, [64, 0, 30], d["starts"])
+    d["lens"] = torch.tensor([1000, -5, 30], dtype=torch.int32)
+    check(run(d, single=True), want)
+    want = ref.attention(d["q"], keys, values, [20, 0, 20], d["starts"])
+    check(run(d, single=True, max_len=20), want)
+    # rows 0 and 4 belong to nobody, and stay
+    q = torch.randn(5, 4, D, generator=torch.Generator().manual_seed(7)).to(BF)
+    d["lens"] = torch.tensor([64, 64, 30], dtype=torch.int32)
+    out = torch.full((5, 4, D), 7.0, dtype=BF).cuda()
+    lse = torch.full((5, 4), 9.0).cuda()
+    starts = torch.tensor([1, 3, 3, 4], dtype=torch.int32).cuda()
+    got = S.cache_attention(q.cuda(), d["cache"].cuda(), d["tables"].cuda(), d["lens"].cuda(), q_starts=starts,
+                            lse=True, out=(out, lse))
+    assert got[0] is out and (out[[0, 4]] == 7.0).all() and (lse[[0, 4]] == 9.0).all()
+    w = ref.attention(q, keys, values, lens, [1, 3, 3, 4])
+    check((out[1:4], lse[1:4]), tuple(x[1:4] for x in w))
+    # falling starts, and ones outside the rows: nothing is written outside, nothing read
+    for bad in ([3, 1, 0, 2], [0, 9, 9, 9], [-4, 2, 1, 5], [2 ** 31 - 1, 0, 5, 2 ** 31 - 1], [-9, -8, -7, -6]):
+        S.cache_attention(q.cuda(), d["cache"].cuda(), d["tables"].cuda(), d["lens"].cuda(),
+                          q_starts=torch.tensor(bad, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+
+
+def test_slices():
+    """q inside a product's rows, tables inside wider ones."""
+    from layer_mhc_seam_amd import seam as S
+    lens, rows, ps, D, Hq = [64, 90, 30], [2, 5, 1], 16, 128, 6
+    d, keys, values = batch(lens, rows, Hq, 2, D, ps, BF, seed=6, width=9)
+    want = ref.attention(d["q"], keys, values, lens, d["starts"])
+    wide = torch.randn(8, 10 * D).to(BF).cuda()
+    q = wide[:, 2 * D:2 * D + Hq * D].view(8, Hq, D)
+    q.copy_(d["q"])
+    tables = torch.full((3, 20), 2 ** 30, dtype=torch.int32).cuda()
+    tables[:, 5:14] = d["tables"].cuda()
+    starts = torch.tensor(d["starts"], dtype=torch.int32).cuda()
+    got = S.cache_attention(q, d["cache"].cuda(), tables[:, 5:14], d["lens"].cuda(), q_starts=starts, lse=True)
+    check(got, want)
+    plain = S.cache_attention(q, d["cache"].cuda(), tables[:, 5:14], d["lens"].cuda(), q_starts=starts)
+    assert torch.equal(plain, got[0])
+
+
+def test_many_sequences():
+    """More sequences than a worker adds up, and blocks for every CU many times over."""
+    g = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 60, (1500,), generator=g).tolist()
+    both(lens, [1] * 1500, 2, 1, 64, 16, BF)
+    rows = torch.randint(0, 4, (1500,), generator=g).tolist()
+    both(lens, rows, 4, 2, 64, 16, BF)
+    both([40] * 300, [1] * 300, 16, 16, 64, 16, F16)
+
+
+@pytest.mark.parametrize("B", [1, 3, 64, 65, 200])
+def test_shares(B):
+    """Workers' shares that begin and end anywhere in blocks of very unequal sequences."""
+    g = torch.Generator().manual_seed(B)
+    lens = (torch.rand(B, generator=g) ** 6 * 9000).long().tolist()
+    lens[-1] = 5000
+    both(lens, [1] * B, 2, 1, 64, 64, BF)
+
+
+def test_far_pages():
+    """A cache past 4 GiB whose last pages are read."""
+    from layer_mhc_seam_amd import seam as S
+    ps, D, Hk, L = 512, 128, 16, 1100
+    pages = 5000
+    cache = S.kv_cache(pages, Hk, D, ps)
+    assert cache.numel() > 5 << 30
+    g = torch.Generator().manual_seed(8)
+    k, v = torch.randn(L, Hk, D, generator=g).to(BF), torch.randn(L, Hk, D, generator=g).to(BF)
+    table = torch.tensor([[pages - 1, pages - 3, pages - 2]], dtype=torch.int32)
+    t = torch.arange(L)
+    small, hk, hv = ref.packed(k, v, (table[0][t // ps].long() - (pages - 3)) * ps + t % ps, 3, ps)
+    cache[pages - 3:] = small.cuda()
+    q = torch.randn(1, 32, D, generator=g).to(BF)
+    got = S.cache_attention(q.cuda(), cache, table.cuda(), torch.tensor([L], dtype=torch.int32).cuda(), lse=True)
+    check(got, ref.attention(q, [hk], [hv], [L], [0, 1]))
+
+
+def test_device_refusals():
+    from layer_mhc_seam_amd import seam as S
+    d, _, _ = batch([64, 30], [1, 1], 4, 2, 64, 16, BF)
+    q, c, tb, n = (d[k].cuda() for k in ("q", "cache", "tables", "lens"))
+    for call in (lambda: S.cache_attention(q, c, tb.long(), n), lambda: S.cache_attention(q, c, tb, n.long()),
+                 lambda: S.cache_attention(q, c, tb, n[:1]), lambda: S.cache_attention(q, c, tb.cpu(), n),
+                 lambda: S.cache_attention(q, c, tb, n, q_starts=n), lambda: S.cache_attention(q, c, tb, n, max_len=0),
+                 lambda: S.cache_attention(q, c[:, :, :-1].contiguous(), tb, n),
+                 lambda: S.cache_attention(q, c, tb, n, out=q.half()),
+                 lambda: S.cache_attention(q, c, tb, n, lse=True, out=(q.clone(), q)),
+                 lambda: S.cache_attention(q, c, tb.t().contiguous().t(), n)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: S.cache_attention(q[:1], c, tb, n), lambda: S.cache_attention(q[:, :3].contiguous(), c, tb, n),
+                 lambda: S.cache_attention(q, c, tb, n, out=q), lambda: S.cache_attention(q, c, tb, n, window=-1),
+                 lambda: S.cache_attention(q, c, tb, n, softcap=-1.0)):
+        with pytest.raises(S.SeamError):
+            call()
+
+
+def test_nothing_to_do():
+    from layer_mhc_seam_amd import seam as S
+    d, _, _ = batch([64], [1], 4, 2, 64, 16, BF)
+    none = torch.zeros(0, dtype=torch.int32).cuda()
+    out = S.cache_attention(d["q"][:0].cuda(), d["cache"].cuda(), d["tables"][:0].cuda(), none)
+    assert out.shape == (0, 4, 64)
+    out = S.cache_attention(d["q"][:0].cuda(), d["cache"].cuda(), d["tables"].cuda(), d["lens"].cuda(),
+                            q_starts=torch.zeros(2, dtype=torch.int32).cuda())
+    assert out.shape == (0, 4, 64)
