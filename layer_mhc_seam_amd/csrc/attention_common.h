@@ -1,0 +1,186 @@
+// attention_common.h -- what the two kernels of attention over the 4-bit cache
+// share: the softmax's constants, where a row block lies, what a row sees, NaN
+// that only some rows of a step see.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "cache_layout.h"
+#include "half_ops.h"
+#include "lane_ops.h"
+#include "seam_internal.h"
+
+namespace mhc {
+namespace {
+
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kLog2e = 1.44269504089f;
+constexpr float kLn2 = 0.69314718056f;
+
+template <int DT> struct Softmax;
+// exp(s - max) is kept times 2^kShift: fp16's smallest number is 2^-24
+template <> struct Softmax<MHC_BF16> {
+    static constexpr float kShift = 0.0f, kSlack = 8.0f;
+};
+template <> struct Softmax<MHC_F16> {
+    static constexpr float kShift = 12.0f, kSlack = 3.0f;
+};
+
+// Over the lanes of equal c = l % 16, the same value in each
+__device__ __forceinline__ float max_over_groups(float v)
+{
+    u32 x = __float_as_uint(v);
+    auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    x = __float_as_uint(v);
+    auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+__device__ __forceinline__ float sum_over_groups(float v)
+{
+    u32 x = __float_as_uint(v);
+    auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    x = __float_as_uint(v);
+    auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+__device__ __forceinline__ u32 or_over_groups(u32 x)
+{
+    auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = p[0] | p[1];
+    auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return q[0] | q[1];
+}
+
+// Lengths, starts and tables, which no kernel writes: where the index is the
+// wave's, it and what follows from it stay in scalar registers
+typedef const __attribute__((address_space(4))) int32_t *Whole;
+
+__device__ __forceinline__ Whole whole(const int32_t *p) { return (Whole)(uintptr_t)p; }
+
+// Tokens [lo, hi) that query row i of n, the last of len tokens, sees
+__device__ __forceinline__ void row_sees(const AttentionParams &P, int len, int n, int i, int *lo, int *hi)
+{
+    const int p = len - n + i;       // -2^31 < p < len < 2^31
+    *hi = P.causal ? max(p + 1, 0) : len;
+    *lo = P.window > 0 ? max(max(p, -1) + 1 - P.window, 0) : 0;
+}
+
+// First query row of sequence b and past its last
+__device__ __forceinline__ int64_t row_start(const AttentionParams &P, int b)
+{
+    return P.q_starts ? min((int64_t)max(whole(P.q_starts)[b], 0), P.T) : b;
+}
+
+__device__ __forceinline__ int length_of(const AttentionParams &P, int b)
+{
+    return (int)min((int64_t)max(whole(P.lens)[b], 0), P.max_len);
+}
+
+// Row blocks of `rows` rows: those of sequence b have the numbers from
+// first_number on, of which there may be more than it has blocks.
+__device__ __forceinline__ int64_t first_number(const AttentionParams &P, int b, int64_t start, int rows)
+{
+    return P.q_starts ? start * P.group / rows + b : (int64_t)b * ((P.group + rows - 1) / rows);
+}
+
+// The sequence that number `id` is one of, and its first number
+__device__ __forceinline__ int sequence_of(const AttentionParams &P, int64_t id, int rows, int64_t *first)
+{
+    int low = 0, high = P.B;
+    if (!P.q_starts) {
+        low = (int)(id / ((P.group + rows - 1) / rows));
+    } else {
+        while (high - low > 1) {
+            const int mid = (low + high) / 2;
+            if (first_number(P, mid, row_start(P, mid), rows) <= id)
+                low = mid;
+            else
+                high = mid;
+        }
+    }
+    *first = first_number(P, low, row_start(P, low), rows);
+    return low;
+}
+
+// How many numbers T rows in B sequences take
+inline int64_t most_blocks(int64_t T, int B, int group, int rows, bool ragged)
+{
+    return ragged ? T * group / rows + B : (int64_t)B * ((group + rows - 1) / rows);
+}
+
+// Which groups of 32 channels of a token's values are NaN, by their scales.  The
+// token is there.
+template <int D>
+__device__ u32 nan_groups(const AttentionParams &P, Whole table, int32_t t, int head)
+{
+    int32_t page, at;
+    if (!cache_page(P.c, table, t + 1, t / kCacheTile * kCacheTile, &page, &at))
+        return 0;
+    const uint8_t *vs = P.cache + cache_page_at(P.c, page, head, D) + cache_scales(P.c.page_size, D, 1) + at +
+                        t % kCacheTile;
+    u32 bits = 0;
+    for (int j = 0; j < D / 32; ++j)
+        bits |= (u32)(vs[j * P.c.page_size] == 255) << j;
+    return bits;
+}
+
+// A page of a head, its loads by a lane's offset plus the wave's: the lanes'
+// offsets stay as they are from page to page.  The long loads, of whole lines
+// that nobody asks for again, go past the caches: a cache of 520 MB then reads
+// at 5.9 TB/s for 4.7, and one that the last level holds no slower.  Short ones
+// that share lines go through them (with all loads past them: 5.0).
+struct Page {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ u32 load8(u32 lane, int wave) const
+    {
+        return __builtin_amdgcn_raw_buffer_load_b8(r, lane, wave, 0);
+    }
+    __device__ __forceinline__ u32 load16(u32 lane, int wave) const
+    {
+        return __builtin_amdgcn_raw_buffer_load_b16(r, lane, wave, 0);
+    }
+    __device__ __forceinline__ u32 load32(u32 lane, int wave) const
+    {
+        return __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0);
+    }
+    __device__ __forceinline__ u32x2 load64(u32 lane, int wave) const
+    {
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, lane, wave, 0));
+    }
+    __device__ __forceinline__ u32x4 load128(u32 lane, int wave) const
+    {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, wave, 2));
+    }
+};
+
+template <int D> __device__ __forceinline__ Page page_of(const AttentionParams &P, int page, int head)
+{
+    const uint8_t *base = P.cache + cache_page_at(P.c, page, head, D);
+    return {__builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)cache_page_bytes(P.c.page_size, D), 0x00027000)};
+}
+
+// Scores in base 2 of N products q . k: scaled, capped
+template <int N> __device__ __forceinline__ void scores(const AttentionParams &P, float v[N])
+{
+    if (P.softcap > 0) {
+        const float in = P.scale / P.softcap, out = P.softcap * kLog2e;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // tanh x = 1 - 2 / (exp 2|x| + 1), its sign x's
+            const float e = __builtin_amdgcn_exp2f(fabsf(v[i] * in) * (2.0f * kLog2e));
+            v[i] = copysignf(out - 2.0f * out * __builtin_amdgcn_rcpf(e + 1.0f), v[i] * in);
+        }
+    } else {
+        const float f = P.scale * kLog2e;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] *= f;
+    }
+}
+
+}  // namespace
+}  // namespace mhc

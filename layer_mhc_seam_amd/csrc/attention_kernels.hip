@@ -15,10 +15,7 @@
 // The values' pairs of channels become pairs of tokens by two byte permutes.
 #include <hip/hip_runtime.h>
 
-#include "cache_layout.h"
-#include "half_ops.h"
-#include "lane_ops.h"
-#include "seam_internal.h"
+#include "attention_common.h"
 
 namespace mhc {
 namespace {
@@ -26,147 +23,112 @@ namespace {
 constexpr int kRows = 16;                 // query rows a block: heads of one kv head, tokens in order
 constexpr int kStep = 32;                 // tokens a wave's step
 constexpr int kAttnWaves = 4;
+constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kQuantum = kStep * kAttnWaves;   // tokens that a workgroup's waves take side by side
 constexpr int kMostBalanced = 1024;       // sequences whose lengths a worker adds up
-constexpr int kLeastQuanta = 2;           // of a worker's share
-constexpr float kLowest = -3.402823466e38f;
-constexpr float kLog2e = 1.44269504089f;
-constexpr float kLn2 = 0.69314718056f;
-
-template <int DT> struct Softmax;
-// exp(s - max) is kept times 2^kShift: fp16's smallest number is 2^-24
-template <> struct Softmax<MHC_BF16> {
-    static constexpr float kShift = 0.0f, kSlack = 8.0f;
-};
-template <> struct Softmax<MHC_F16> {
-    static constexpr float kShift = 12.0f, kSlack = 3.0f;
-};
-
-// Over the lanes of equal c = l % 16, the same value in each
-__device__ __forceinline__ float max_over_groups(float v)
-{
-    u32 x = __float_as_uint(v);
-    auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
-    x = __float_as_uint(v);
-    auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
-}
-
-__device__ __forceinline__ float sum_over_groups(float v)
-{
-    u32 x = __float_as_uint(v);
-    auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-    x = __float_as_uint(v);
-    auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
-}
-
-__device__ __forceinline__ u32 or_over_groups(u32 x)
-{
-    auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    x = p[0] | p[1];
-    auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    return q[0] | q[1];
-}
+constexpr int kLeastQuanta = 4;           // of a worker's share
+constexpr int kJoinWaves = 4;
 
 // A sequence's share of the work: blocks of rows, and the quanta of tokens that
 // some row of it sees, the same number for every block and kv head.
 struct Sequence {
     int64_t first;      // its first query row
     int64_t rows;       // query rows times heads of a kv head
-    int64_t n;          // query rows
-    int64_t len;        // cached tokens
-    int64_t lo;         // first quantum's first token
-    int64_t blocks;     // of kRows rows
-    int64_t quanta;
+    int n;              // query rows
+    int len;            // cached tokens
+    int lo;             // first quantum's first token
+    int blocks;         // of kRows rows
+    int quanta;
 };
 
 __device__ __forceinline__ Sequence sequence(const AttentionParams &P, int b)
 {
     Sequence s;
-    int64_t from = b, to = b + 1;
-    if (P.q_starts) {
-        from = min((int64_t)max(P.q_starts[b], 0), P.T);
-        to = min((int64_t)max(P.q_starts[b + 1], 0), P.T);
-    }
+    const int64_t from = row_start(P, b), to = row_start(P, b + 1);
     s.first = from;
-    s.n = max(to - from, (int64_t)0);
-    s.rows = s.n * P.group;
-    s.len = min((int64_t)max(P.lens[b], 0), P.max_len);
-    s.lo = P.window > 0 ? max(s.len - s.n + 1 - P.window, (int64_t)0) / kStep * kStep : 0;
-    s.blocks = (s.rows + kRows - 1) / kRows;
-    s.quanta = max((s.len - s.lo + kQuantum - 1) / kQuantum, (int64_t)1);
+    s.n = (int)max(to - from, (int64_t)0);
+    s.rows = (int64_t)s.n * P.group;
+    s.len = length_of(P, b);
+    int hi;
+    row_sees(P, s.len, s.n, 0, &s.lo, &hi);
+    s.lo = s.lo / kStep * kStep;
+    s.blocks = (int)((s.rows + kRows - 1) / kRows);
+    s.quanta = max((s.len - s.lo + kQuantum - 1) / kQuantum, 1);
     return s;
 }
 
-__device__ __forceinline__ int64_t wave_total(int64_t v)
+// A worker's share of all quanta, which are those of sequence after sequence, of
+// kv head after kv head in it, of block after block.  Their number is below 2^31.
+struct Share {
+    int begin, end;
+    int total, workers;
+    int b;              // the sequence of quantum `begin`
+    int start;          // that sequence's first quantum
+};
+
+__device__ __forceinline__ int quanta_of(const AttentionParams &P, int b, int *shares)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const u64 x = (u64)v;
-        const u32 lo = __shfl_xor((u32)x, d), hi = __shfl_xor((u32)(x >> 32), d);
-        v += (int64_t)((u64)hi << 32 | lo);
-    }
-    const u32 lo = read_lane((u32)(u64)v, 0), hi = read_lane((u32)((u64)v >> 32), 0);
-    return (int64_t)((u64)hi << 32 | lo);
+    if (b >= P.B)
+        return 0;
+    const Sequence s = sequence(P, b);
+    *shares += s.blocks * P.c.heads * ((s.quanta + kLeastQuanta - 1) / kLeastQuanta);
+    return s.blocks * s.quanta * P.c.heads;
 }
 
-// All quanta of the batch: of each sequence blocks * kv heads * quanta, in that
-// order of sequences, kv heads, blocks.
-__device__ int64_t all_quanta(const AttentionParams &P)
+// Sum of v over the lanes up to this one: inside rows of 16, then over the rows
+__device__ __forceinline__ int sum_upto(int v)
 {
-    int64_t mine = 0;
-    for (int b = threadIdx.x & 63; b < P.B; b += 64) {
-        const Sequence s = sequence(P, b);
-        mine += s.blocks * s.quanta;
-    }
-    return wave_total(mine) * P.c.heads;
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // lanes 1, 2, 4, 8 before
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // lane 15 to the next row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // lane 31 to the last two
+    return v;
 }
 
-// Sequence that quantum `at` (below the total) belongs to, and the first quantum of it
-__device__ int find_sequence(const AttentionParams &P, int64_t at, int64_t *start)
+__device__ __forceinline__ int share_start(int total, int workers, int w)
+{
+    return (int)((int64_t)total * w / workers);
+}
+
+// The worker whose share holds that quantum
+__device__ __forceinline__ int share_of(int total, int workers, int quantum)
+{
+    return (int)(((int64_t)workers * (quantum + 1) - 1) / total);
+}
+
+__device__ Share share(const AttentionParams &P, int worker)
 {
     const int lane = threadIdx.x & 63;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < P.B; b0 += 64) {
-        int64_t mine = 0;
-        if (b0 + lane < P.B) {
-            const Sequence s = sequence(P, b0 + lane);
-            mine = s.blocks * s.quanta * P.c.heads;
+    Share h;
+    // a worker for kLeastQuanta quanta of a block, if there are as many
+    int shares = 0, own = quanta_of(P, lane, &shares), upto = sum_upto(own);
+    h.total = (int)read_lane((u32)upto, 63);
+    for (int b0 = 64; b0 < P.B; b0 += 64)
+        h.total += (int)read_lane((u32)sum_upto(quanta_of(P, b0 + lane, &shares)), 63);
+    shares = (int)read_lane((u32)sum_upto(shares), 63);
+    h.workers = max(min(shares, P.workers), 1);
+    h.begin = worker < h.workers ? share_start(h.total, h.workers, worker) : h.total;
+    h.end = worker < h.workers ? share_start(h.total, h.workers, worker + 1) : h.total;
+    h.b = h.start = 0;
+    if (h.begin == h.end)
+        return h;
+    int before = 0;
+    for (int b0 = 0;; b0 += 64) {
+        if (b0 > 0) {
+            own = quanta_of(P, b0 + lane, &shares);
+            upto = sum_upto(own);
         }
-        int64_t upto = mine;             // sum over lanes 0 .. lane
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const u64 x = (u64)upto;
-            const u32 lo = __shfl_up((u32)x, d), hi = __shfl_up((u32)(x >> 32), d);
-            if (lane >= d)
-                upto += (int64_t)((u64)hi << 32 | lo);
-        }
-        const u64 past = __ballot(before + upto > at);
+        const u64 past = __ballot(before + upto > h.begin);
         if (past) {
             const int l = __ffsll((unsigned long long)past) - 1;
-            const int64_t first = before + upto - mine;
-            const u32 lo = read_lane((u32)(u64)first, l), hi = read_lane((u32)((u64)first >> 32), l);
-            *start = (int64_t)((u64)hi << 32 | lo);
-            return b0 + l;
+            h.b = b0 + l;
+            h.start = before + (int)read_lane((u32)(upto - own), l);
+            return h;
         }
-        const u32 lo = read_lane((u32)(u64)upto, 63), hi = read_lane((u32)((u64)upto >> 32), 63);
-        before += (int64_t)((u64)hi << 32 | lo);
+        before += (int)read_lane((u32)upto, 63);
     }
-    *start = before;
-    return P.B;
-}
-
-__device__ __forceinline__ int64_t share_start(int64_t total, int64_t workers, int64_t w)
-{
-    return total * w / workers;          // total < 2^40, workers < 2^13
-}
-
-__device__ __forceinline__ int64_t workers_for(int64_t total, int64_t most)
-{
-    return max(min((total + kLeastQuanta - 1) / kLeastQuanta, most), (int64_t)1);
 }
 
 // A partial result: kRows maxima, kRows sums, [kRows][D] weighted values.  A
@@ -176,17 +138,35 @@ template <int D> __device__ __forceinline__ float *record(const AttentionParams 
     return P.workspace + (2 * worker + (first ? 0 : 1)) * (int64_t)(kRows * (D + 2));
 }
 
+// What is to be joined of a block: its parts are those of workers `from` on.
+// parts is 0 where one worker has all of it.
+struct alignas(8) Join {
+    int from;
+    int parts;          // below 2^13; its top bit: the first part is all of its worker's share
+};
+
+constexpr int kWholeShare = 1 << 30;
+
+// Of the block with that number and that kv head
+template <int D>
+__device__ __forceinline__ Join *join_of(const AttentionParams &P, int64_t number, int head)
+{
+    return (Join *)(P.workspace + 2 * (int64_t)P.workers * (kRows * (D + 2))) + number * P.c.heads + head;
+}
+
+// 32 tokens of a kv head as a lane holds them
 template <int D> struct Tile {
-    u32 k[2][D / 32];
+    u32 k[2][D / 32];                    // token c of each half, its quarter g of the channels
     u32 ks[2][(D + 127) / 128];
-    u32 v[8][(D + 127) / 128];
+    u32 v[8][(D + 127) / 128];           // tokens 4g .. 4g + 3 of each half, chunk c of the channels
     u32 vs[2];
+    bool there[2];
 };
 
 // The rows of a block as a lane of row c sees them
 struct Rows {
-    int64_t lo, hi;          // tokens that the lane's row sees
-    int64_t most_lo, least_hi;   // that every row of the block sees
+    int lo, hi;              // tokens that the lane's row sees
+    int most_lo, least_hi;   // that every row of the block sees
 };
 
 template <int DT, int D> struct Attention {
@@ -197,23 +177,30 @@ template <int DT, int D> struct Attention {
     static constexpr int VB = VC / 2;        // bytes of them
 
     const AttentionParams &P;
-    const int lane, c, g;
+    const int c, g;
+    u32 at_k, at_v, at_ks, at_vs;            // the lane's bytes in a tile
     u32x4 q[KC];
     f32x4 acc[VC];
     float top, sum;
     u32 nans;                // groups of V's channels that a NaN reaches in this lane's row
 
-    __device__ Attention(const AttentionParams &p)
-        : P(p), lane(threadIdx.x & 63), c(lane & 15), g(lane >> 4)
+    __device__ Attention(const AttentionParams &p) : P(p), c(threadIdx.x & 15), g(threadIdx.x >> 4 & 3)
     {
+        const int ps = P.c.page_size;
+        at_k = c * (D / 2) + g * (D / 8);
+        at_v = cache_codes(ps, D, 1) + 4 * g * (D / 2) + c * VB;
+        at_ks = cache_scales(ps, D, 0) + g * D / 128 * ps + c;
+        at_vs = cache_scales(ps, D, 1) + c * VC / 32 * ps + 4 * g;
     }
 
-    __device__ void load_q(const Sequence &s, int64_t block, int head)
+    // Rows of the block that begins with head `skip` of the sequence's query row
+    // i0: the lane's query row, counted in the sequence, and head
+    __device__ void load_q(const Sequence &s, int i0, int skip, int head)
     {
-        const int64_t r = block * kRows + c;
-        const int64_t i = r / P.group;
-        if (r < s.rows) {
-            const uint16_t *at = P.q + (s.first + i) * P.q_token + (head * P.group + (r - i * P.group)) * P.q_head;
+        const int over = (skip + c) / P.group, i = i0 + over;
+        if (i < s.n) {
+            const uint16_t *at =
+                P.q + (s.first + i) * P.q_token + (int64_t)(head * P.group + (skip + c - over * P.group)) * P.q_head;
 #pragma unroll
             for (int j = 0; j < KC; ++j)
                 q[j] = *(const u32x4 *)(at + g * (D / 4) + j * 8);
@@ -224,152 +211,111 @@ template <int DT, int D> struct Attention {
         }
     }
 
-    __device__ Rows rows_of(const Sequence &s, int64_t block)
+    __device__ Rows rows_of(const Sequence &s, int i0, int skip)
     {
-        auto bounds = [&](int64_t r, int64_t *lo, int64_t *hi) {
-            const int64_t p = s.len - s.n + r / P.group;
-            *hi = P.causal ? max(min(p + 1, s.len), (int64_t)0) : s.len;
-            *lo = P.window > 0 ? max(p + 1 - P.window, (int64_t)0) : 0;
-        };
         Rows w;
-        const int64_t first = block * kRows, last = min(first + kRows, s.rows) - 1;
-        int64_t skip;
-        bounds(first, &skip, &w.least_hi);
-        bounds(last, &w.most_lo, &skip);
-        if (first + c <= last)
-            bounds(first + c, &w.lo, &w.hi);
-        else
+        int none;
+        const int i = i0 + (skip + c) / P.group, last = min(i0 + (skip + kRows - 1) / P.group, s.n - 1);
+        row_sees(P, s.len, s.n, i0, &none, &w.least_hi);
+        row_sees(P, s.len, s.n, last, &w.most_lo, &none);
+        row_sees(P, s.len, s.n, i, &w.lo, &w.hi);
+        if (i >= s.n)
             w.lo = w.hi = 0;
         return w;
     }
 
-    // Half h of the tile at t: page and place, or page 0, which no token of it is read from
-    __device__ bool place(const int32_t *table, int64_t len, int64_t t, int64_t *page, int32_t *at)
+    __device__ __forceinline__ void load(Tile<D> &x, Whole table, int len, int t, int head)
     {
-        const bool there = cache_tile(P.c, table, len, t, page, at);
-        if (!there) {
-            *page = 0;
-            *at = 0;
-        }
-        return there;
-    }
-
-    __device__ void load(Tile<D> &x, bool there[2], const int32_t *table, int64_t len, int64_t t, int head)
-    {
-        const int ps = P.c.page_size;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            int64_t page;
-            int32_t at;
-            there[h] = place(table, len, t + 16 * h, &page, &at);
-            const uint8_t *base = P.cache + cache_page_at(P.c, page, head, D);
-            const uint8_t *kc = base + (u32)((at + c) * (D / 2) + g * (D / 8));
+            int32_t page, at;
+            x.there[h] = cache_page(P.c, table, len, t + 16 * h, &page, &at);
+            const Page from = page_of<D>(P, page, head);
+            const int codes = at * (D / 2);
             if constexpr (D == 64) {
-                const u32x2 w = *(const u32x2 *)kc;
+                const u32x2 w = from.load64(at_k, codes);
                 x.k[h][0] = w[0];
                 x.k[h][1] = w[1];
             } else {
 #pragma unroll
                 for (int j = 0; j < KC / 4; ++j) {
-                    const u32x4 w = *(const u32x4 *)(kc + 16 * j);
+                    const u32x4 w = from.load128(at_k + 16 * j, codes);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         x.k[h][4 * j + i] = w[i];
                 }
             }
-            const uint8_t *ks = base + cache_scales(ps, D, 0) + (u32)(g * D / 128 * ps + at + c);
 #pragma unroll
             for (int j = 0; j < (D + 127) / 128; ++j)
-                x.ks[h][j] = ks[j * ps];
-            const uint8_t *vc = base + cache_codes(ps, D, 1) + (u32)((at + 4 * g) * (D / 2) + c * VB);
+                x.ks[h][j] = from.load8(at_ks, at + j * P.c.page_size);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint8_t *from = vc + j * (D / 2);
+                const u32 v = at_v + j * (D / 2);
                 if constexpr (D == 64) {
-                    x.v[4 * h + j][0] = *(const uint16_t *)from;
+                    x.v[4 * h + j][0] = from.load16(v, codes);
                 } else if constexpr (D == 128) {
-                    x.v[4 * h + j][0] = *(const u32 *)from;
+                    x.v[4 * h + j][0] = from.load32(v, codes);
                 } else {
-                    const u32x2 w = *(const u32x2 *)from;
+                    const u32x2 w = from.load64(v, codes);
                     x.v[4 * h + j][0] = w[0];
                     x.v[4 * h + j][1] = w[1];
                 }
             }
-            x.vs[h] = *(const u32 *)(base + cache_scales(ps, D, 1) + (u32)(c * VC / 32 * ps + at + 4 * g));
+            x.vs[h] = from.load32(at_vs, at);
         }
     }
 
-    // Which groups of V's channels of a token are NaN, by their scales
-    __device__ u32 nan_groups(const int32_t *table, int64_t t, int head)
+    // Hides what the lane's row does not see of the 32 tokens at t0
+    __device__ void mask(Tile<D> &x, float v[8], const Rows &rows, int len, Whole table, int t0, int head)
     {
-        int64_t page;
-        int32_t at;
-        cache_tile(P.c, table, t + 1, t / 16 * 16, &page, &at);
-        const uint8_t *vs = P.cache + cache_page_at(P.c, page, head, D) + cache_scales(P.c.page_size, D, 1) + at + t % 16;
-        u32 bits = 0;
-        for (int j = 0; j < D / 32; ++j)
-            bits |= (u32)(vs[j * P.c.page_size] == 255) << j;
-        return bits;
+        u32 nan_tokens = 0, seen = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = t0 + 16 * (i / 4) + 4 * g + i % 4;
+            const bool sees = x.there[i / 4] && t >= rows.lo && t < rows.hi;
+            seen |= (u32)sees << i;
+            v[i] = sees ? v[i] : -__builtin_inff();
+            // what no row sees may be anything; a NaN that only some rows see
+            // goes by `nans` to those
+            const bool valid = x.there[i / 4] && t < len;
+#pragma unroll
+            for (int j = 0; j < (D + 127) / 128; ++j)
+                x.v[i][j] = valid ? x.v[i][j] : 0;
+            const u32 byte = x.vs[i / 4] >> (8 * (i % 4)) & 255;
+            if (byte == 255 || !valid)
+                x.vs[i / 4] &= ~(255u << (8 * (i % 4)));
+            nan_tokens |= (u32)(byte == 255 && valid);
+        }
+        if (__any(nan_tokens != 0))
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i)
+                if (seen >> i & 1)
+                    nans |= nan_groups<D>(P, table, t0 + 16 * (i / 4) + 4 * g + i % 4, head);
     }
 
-    template <bool MASKED>
-    __device__ void step(Tile<D> &x, const bool there[2], const Rows &rows, int64_t len, const int32_t *table,
-                         int64_t t0, int head)
+    __device__ __forceinline__ void step(Tile<D> &x, const Rows &rows, int len, Whole table, int t0, int head)
     {
-        f32x4 s[2];
+        float v[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            s[h] = f32x4{0, 0, 0, 0};
+            f32x4 s = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < KC; ++j) {
                 const float f = scale_of(x.ks[h][D == 256 ? j / 4 : 0]);
                 const u32 w = x.k[h][j];
                 const u32x4 a = {H::template from_fp4<0>(w, f), H::template from_fp4<1>(w, f),
                                  H::template from_fp4<2>(w, f), H::template from_fp4<3>(w, f)};
-                s[h] = H::mfma16(a, q[j], s[h]);
+                s = H::mfma16(a, q[j], s);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[4 * h + i] = s[i];
         }
-        float v[8];
-        const float to_base2 = P.softcap > 0 ? 1.0f : P.scale * kLog2e;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = s[i / 4][i % 4] * to_base2;
-        if (P.softcap > 0) {
-            const float in = 2.0f * kLog2e * (P.scale / P.softcap), out = P.softcap * kLog2e;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fabsf(v[i] * in));
-                v[i] = copysignf(out - 2.0f * out * __builtin_amdgcn_rcpf(e + 1.0f), v[i] * in);
-            }
-        }
-        if constexpr (MASKED) {
-            u32 nan_tokens = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t t = t0 + 16 * (i / 4) + 4 * g + i % 4;
-                const bool seen = there[i / 4] && t >= rows.lo && t < rows.hi;
-                v[i] = seen ? v[i] : -__builtin_inff();
-                // what no row sees may be anything; what some row does not see,
-                // NaN: it then goes by `nans` to those that do
-                const bool valid = there[i / 4] && t < len;
-#pragma unroll
-                for (int j = 0; j < (D + 127) / 128; ++j)
-                    x.v[i][j] = valid ? x.v[i][j] : 0;
-                const u32 byte = x.vs[i / 4] >> (8 * (i % 4)) & 255;
-                if (byte == 255 || !valid)
-                    x.vs[i / 4] &= ~(255u << (8 * (i % 4)));
-                nan_tokens |= (u32)(byte == 255 && valid) << i;
-            }
-            if (__any(nan_tokens != 0)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t t = t0 + 16 * (i / 4) + 4 * g + i % 4;
-                    if (there[i / 4] && t >= rows.lo && t < rows.hi)
-                        nans |= nan_groups(table, t, head);
-                }
-            }
-        }
-        float most = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+        scores<8>(P, v);
+        if (!(t0 >= rows.most_lo && t0 + kStep <= rows.least_hi && x.there[0] && x.there[1]))
+            mask(x, v, rows, len, table, t0, head);
+        const float most =
+            fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
         if (__any(most > top + S::kSlack)) {
             const float now = fmaxf(top, max_over_groups(most));
             const float a = __builtin_amdgcn_exp2f(top - now);
@@ -420,9 +366,9 @@ template <int DT, int D> struct Attention {
         acc[2 * BYTE + 1] = H::mfma16(hi, p, acc[2 * BYTE + 1]);
     }
 
-    // The wave's part of quanta [from, to) of the block
-    __device__ void run(const Sequence &s, const Rows &rows, const int32_t *table, int head, int64_t from, int64_t to,
-                        int wave)
+    // The wave's part of quanta [from, to) of the block: each step's tokens are
+    // asked for before the step before
+    __device__ void run(const Sequence &s, const Rows &rows, Whole table, int head, int from, int to, int wave)
     {
         top = kLowest;
         sum = 0.0f;
@@ -430,17 +376,25 @@ template <int DT, int D> struct Attention {
 #pragma unroll
         for (int m = 0; m < VC; ++m)
             acc[m] = f32x4{0, 0, 0, 0};
-        for (int64_t n = from; n < to; ++n) {
-            const int64_t t = s.lo + n * kQuantum + wave * kStep;
-            if (t >= s.len)
+        int t = s.lo + from * kQuantum + wave * kStep;
+        const int end = min(s.len - s.lo, to * kQuantum) + s.lo;
+        if (t >= end)
+            return;
+        // no branch stands about the loads, so that each wait is for one step's
+        // and not for those behind it; past the end they read page 0
+        Tile<D> a, b;
+        load(a, table, s.len, t, head);
+        while (true) {
+            load(b, table, s.len, t + kQuantum, head);
+            step(a, rows, s.len, table, t, head);
+            t += kQuantum;
+            if (t >= end)
                 break;
-            Tile<D> x;
-            bool there[2];
-            load(x, there, table, s.len, t, head);
-            if (t >= rows.most_lo && t + kStep <= rows.least_hi && there[0] && there[1])
-                step<false>(x, there, rows, s.len, table, t, head);
-            else
-                step<true>(x, there, rows, s.len, table, t, head);
+            load(a, table, s.len, t + kQuantum, head);
+            step(b, rows, s.len, table, t, head);
+            t += kQuantum;
+            if (t >= end)
+                break;
         }
     }
 };
@@ -450,16 +404,14 @@ template <int D> struct Shared {
     float o[kAttnWaves][kRows][D + 4];
 };
 
-// Four channels of a finished row
+// Four channels of a finished row: head `skip` behind those of query row i
 template <int DT, int D>
-__device__ void store(const AttentionParams &P, const Sequence &s, int64_t block, int head, int row, int d, float4 o,
-                      float top, float sum)
+__device__ __forceinline__ void store(const AttentionParams &P, int64_t i, int skip, int head, int d, float4 o,
+                                      float top, float sum)
 {
     typedef Half<DT> H;
-    const int64_t r = block * kRows + row;
-    if (r >= s.rows)
-        return;
-    const int64_t i = r / P.group, at = (s.first + i) * P.q_heads + head * P.group + (r - i * P.group);
+    const int over = skip / P.group;
+    const int64_t at = (i + over) * P.q_heads + head * P.group + (skip - over * P.group);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const u32x2 w = {H::pack(o.x * inv, o.y * inv), H::pack(o.z * inv, o.w * inv)};
     *(u32x2 *)(P.out + at * D + d) = w;
@@ -470,67 +422,60 @@ __device__ void store(const AttentionParams &P, const Sequence &s, int64_t block
 // BALANCED: the workers share all quanta evenly, and a block that several have
 // parts of is put together by attention_join_kernel.  Otherwise a workgroup a block.
 template <int DT, int D, bool BALANCED>
-__global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(const AttentionParams P)
+__global__ __launch_bounds__(kAttnThreads)
+    __attribute__((amdgpu_waves_per_eu(2))) void attention_kernel(const AttentionParams P)
 {
     __shared__ Shared<D> L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t at = 0, end = 0, start = 0, worker = 0;
-    int b;
+    const int64_t id = block_id();
+    Sequence s;
+    Share h;
+    int at, end, start = 0, b, block = 0, head = 0;
     if constexpr (BALANCED) {
-        worker = block_id();
-        const int64_t total = all_quanta(P), workers = workers_for(total, P.workers);
-        if (worker >= workers || total == 0)
+        if (id >= P.workers)
             return;
-        at = share_start(total, workers, worker);
-        end = share_start(total, workers, worker + 1);
-        b = find_sequence(P, at, &start);
+        h = share(P, (int)id);
+        at = h.begin;
+        end = h.end;
+        b = h.b;
+        start = h.start;
+        if (at == end)
+            return;
+        s = sequence(P, b);
     } else {
-        // row blocks of sequence b have numbers first * group / kRows + b on, or none
-        const int64_t id = block_id() / P.c.heads;
-        if (id >= P.blocks)
+        const int64_t number = id / P.c.heads;
+        if (number >= P.blocks)
             return;
-        int low = 0, high = P.B;
-        if (P.q_starts) {
-            while (high - low > 1) {
-                const int mid = (low + high) / 2;
-                const int64_t from = min((int64_t)max(P.q_starts[mid], 0), P.T);
-                if (from * P.group / kRows + mid <= id)
-                    low = mid;
-                else
-                    high = mid;
-            }
-            start = min((int64_t)max(P.q_starts[low], 0), P.T) * P.group / kRows + low;
-        } else {
-            const int each = (P.group + kRows - 1) / kRows;
-            low = (int)(id / each);
-            start = (int64_t)low * each;
-        }
-        b = low;
-        const Sequence s = sequence(P, b);
-        if (id < start || id - start >= s.blocks)
+        int64_t first;
+        b = sequence_of(P, number, kRows, &first);
+        s = sequence(P, b);
+        if (number < first || number - first >= s.blocks)
             return;
-        // as if this block's quanta were a worker's share
-        const int64_t head = block_id() % P.c.heads;
-        at = (head * s.blocks + (id - start)) * s.quanta;
-        end = at + s.quanta;
-        start = 0;
+        head = (int)(id - number * P.c.heads);
+        block = (int)(number - first);
+        at = 0;
+        end = s.quanta;
     }
     Attention<DT, D> A(P);
-    const int64_t begin = at;
+    const int begin = at;
     while (at < end) {
-        Sequence s = sequence(P, b);
-        while (at - start >= s.blocks * P.c.heads * s.quanta) {
-            start += s.blocks * P.c.heads * s.quanta;
-            s = sequence(P, ++b);
+        int from = 0;
+        if constexpr (BALANCED) {
+            while (at - start >= s.blocks * P.c.heads * s.quanta) {
+                start += s.blocks * P.c.heads * s.quanta;
+                s = sequence(P, ++b);
+            }
+            const int index = (at - start) / s.quanta;
+            from = at - start - index * s.quanta;
+            head = index / s.blocks;
+            block = index - head * s.blocks;
         }
-        const int64_t index = (at - start) / s.quanta, from = at - start - index * s.quanta;
-        const int head = (int)(index / s.blocks);
-        const int64_t block = index - head * s.blocks;
-        const int64_t to = min(s.quanta, from + (end - at));
-        const Rows rows = A.rows_of(s, block);
-        A.load_q(s, block, head);
-        const int32_t *table = P.tables + b * P.table_stride;
-        A.run(s, rows, table, head, from, to, wave);
+        const int to = min(s.quanta, from + (end - at));
+        const int64_t row = (int64_t)block * kRows;
+        const int i0 = (int)(row / P.group), skip = (int)(row - (int64_t)i0 * P.group);
+        const Rows rows = A.rows_of(s, i0, skip);
+        A.load_q(s, i0, skip, head);
+        A.run(s, rows, whole(P.tables + b * P.table_stride), head, from, to, wave);
 
         // the waves' parts, over their largest maximum
         const float sum = sum_over_groups(A.sum);
@@ -554,128 +499,191 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(const Attent
             }
         __syncthreads();
         const bool whole = from == 0 && to == s.quanta;
-        float *rec = record<D>(P, worker, at == begin);
-        for (int e = threadIdx.x; e < kRows * D / 4; e += 64 * kAttnWaves) {
-            const int row = e / (D / 4), d = e % (D / 4) * 4;
+        const int count = (int)min(s.rows - row, (int64_t)kRows);
+        float *rec = record<D>(P, id, at == begin);
+        for (int e = threadIdx.x; e < count * (D / 4); e += kAttnThreads) {
+            const int r = e / (D / 4), d = e % (D / 4) * 4;
             float most = kLowest, all = 0.0f;
             float4 o = {0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < kAttnWaves; ++w)
-                most = fmaxf(most, L.top[w][row]);
+                most = fmaxf(most, L.top[w][r]);
 #pragma unroll
             for (int w = 0; w < kAttnWaves; ++w) {
-                all += L.sum[w][row] * __builtin_amdgcn_exp2f(L.top[w][row] - most);
-                const float4 x = *(const float4 *)&L.o[w][row][d];
+                all += L.sum[w][r] * __builtin_amdgcn_exp2f(L.top[w][r] - most);
+                const float4 x = *(const float4 *)&L.o[w][r][d];
                 o.x += x.x;
                 o.y += x.y;
                 o.z += x.z;
                 o.w += x.w;
             }
             if (whole) {
-                store<DT, D>(P, s, block, head, row, d, o, most, all);
+                store<DT, D>(P, s.first + i0, skip + r, head, d, o, most, all);
             } else {
-                *(float4 *)(rec + 2 * kRows + row * D + d) = o;
+                *(float4 *)(rec + 2 * kRows + r * D + d) = o;
                 if (d == 0) {
-                    rec[row] = most;
-                    rec[kRows + row] = all;
+                    rec[r] = most;
+                    rec[kRows + r] = all;
                 }
             }
         }
+        if constexpr (BALANCED)
+            if (from == 0 && threadIdx.x == 0) {
+                Join *j = join_of<D>(P, first_number(P, b, s.first, kRows) + block, head);
+                j->from = (int)id;
+                j->parts = whole ? 0
+                                 : (share_of(h.total, h.workers, at + s.quanta - 1) - (int)id + 1) |
+                                       (at == begin ? kWholeShare : 0);
+            }
         __syncthreads();
         at += to - from;
     }
 }
 
-// Puts together the block that begins in this worker's share and ends in another's
-template <int DT, int D>
-__global__ __launch_bounds__(64 * kAttnWaves) void attention_join_kernel(const AttentionParams P)
+// Puts together the blocks that several workers have parts of.  WAVES waves a
+// row, D/4 lanes a part, eight parts a lane at once.
+template <int DT, int D, int WAVES>
+__global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(const AttentionParams P)
 {
-    const int64_t worker = block_id();
-    const int64_t total = all_quanta(P), workers = workers_for(total, P.workers);
-    if (worker + 1 >= workers || total == 0)
+    constexpr int ROWS = kJoinWaves / WAVES, LANES = D / 4, AT_ONCE = 64 / LANES * WAVES, BATCH = WAVES > 1 ? 8 : 2;
+    __shared__ float4 L[kJoinWaves][LANES];
+    __shared__ float2 M[kJoinWaves];
+    const int64_t id = block_id(), segment = id / (kRows / ROWS), number = segment / P.c.heads;
+    if (number >= P.blocks)
         return;
-    const int64_t begin = share_start(total, workers, worker), end = share_start(total, workers, worker + 1);
-    if (begin == end)
-        return;
-    int64_t start;
-    const int b = find_sequence(P, end - 1, &start);
+    const int head = (int)(segment - number * P.c.heads);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int row = (int)(id % (kRows / ROWS)) * ROWS + wave / WAVES;
+    const Join j = *join_of<D>(P, number, head);
+    int64_t first;
+    const int b = sequence_of(P, number, kRows, &first);
     const Sequence s = sequence(P, b);
-    const int64_t index = (end - 1 - start) / s.quanta;
-    const int64_t first = start + index * s.quanta, last = first + s.quanta;
-    if (first < begin || last == end)
+    // every block's Join has been written, those of numbers that no block has not
+    if (number < first || number - first >= s.blocks)
         return;
-    int64_t upto = worker;       // the last worker with a part
-    while (share_start(total, workers, upto + 1) < last)
-        ++upto;
-    const int head = (int)(index / s.blocks);
-    const int64_t block = index - head * s.blocks;
-    for (int e = threadIdx.x; e < kRows * D / 4; e += 64 * kAttnWaves) {
-        const int row = e / (D / 4), d = e % (D / 4) * 4;
-        float most = kLowest, all = 0.0f;
-        float4 o = {0, 0, 0, 0};
-        for (int64_t w = worker; w <= upto; ++w) {
-            const float *rec = record<D>(P, w, w > worker || first == begin);
-            const float top = rec[row], now = fmaxf(most, top);
-            const float old = __builtin_amdgcn_exp2f(most - now), part = __builtin_amdgcn_exp2f(top - now);
-            const float4 x = *(const float4 *)(rec + 2 * kRows + row * D + d);
-            all = all * old + rec[kRows + row] * part;
-            o.x = o.x * old + x.x * part;
-            o.y = o.y * old + x.y * part;
-            o.z = o.z * old + x.z * part;
-            o.w = o.w * old + x.w * part;
+    const int parts = j.parts & ~kWholeShare;
+    const int64_t at = (number - first) * kRows;
+    if (parts == 0 || (WAVES > 1 && at + row >= s.rows))      // the workgroup's all
+        return;
+    const int d = lane % LANES * 4;
+    float most = kLowest, all = 0.0f;
+    float4 o = {0, 0, 0, 0};
+    if (at + row < s.rows)
+        for (int i0 = wave % WAVES * (64 / LANES) + lane / LANES; i0 < parts; i0 += AT_ONCE * BATCH) {
+            float top[BATCH], sum[BATCH];
+            float4 x[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                // past the last: the last once more, with a weight of 0
+                const int i = min(i0 + k * AT_ONCE, parts - 1);
+                const float *rec = record<D>(P, j.from + i, i > 0 || (j.parts & kWholeShare));
+                top[k] = rec[row];
+                sum[k] = rec[kRows + row];
+                x[k] = *(const float4 *)(rec + 2 * kRows + row * D + d);
+            }
+            float now = most;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                now = fmaxf(now, top[k]);
+            const float old = __builtin_amdgcn_exp2f(most - now);
             most = now;
+            all *= old;
+            o = {o.x * old, o.y * old, o.z * old, o.w * old};
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                if (i0 + k * AT_ONCE >= parts)
+                    continue;
+                const float w = __builtin_amdgcn_exp2f(top[k] - now);
+                all += sum[k] * w;
+                o = {o.x + x[k].x * w, o.y + x[k].y * w, o.z + x[k].z * w, o.w + x[k].w * w};
+            }
         }
-        store<DT, D>(P, s, block, head, row, d, o, most, all);
+    auto add = [&](float top, float sum, const float4 &x) {
+        const float now = fmaxf(most, top);
+        const float a = __builtin_amdgcn_exp2f(most - now), c = __builtin_amdgcn_exp2f(top - now);
+        most = now;
+        all = all * a + sum * c;
+        o = {o.x * a + x.x * c, o.y * a + x.y * c, o.z * a + x.z * c, o.w * a + x.w * c};
+    };
+#pragma unroll
+    for (int x = LANES; x < 64; x <<= 1) {
+        const float top = __shfl_xor(most, x), sum = __shfl_xor(all, x);
+        const float4 v = {__shfl_xor(o.x, x), __shfl_xor(o.y, x), __shfl_xor(o.z, x), __shfl_xor(o.w, x)};
+        add(top, sum, v);
+    }
+    if constexpr (WAVES > 1) {
+        if (lane < LANES)
+            L[wave][lane] = o;
+        if (lane == 0)
+            M[wave] = {most, all};
+        __syncthreads();
+        if (wave > 0)
+            return;
+        for (int w = 1; w < WAVES; ++w)
+            add(M[w].x, M[w].y, L[w][lane % LANES]);
+    }
+    if (lane < LANES && at + row < s.rows) {
+        const int64_t i = at / P.group;
+        store<DT, D>(P, s.first + i, (int)(at - i * P.group) + row, head, d, o, most, all);
     }
 }
 
-// Row blocks that T rows in B sequences may have, numbered as above
-int64_t most_blocks(int64_t T, int B, int group, bool ragged)
-{
-    return ragged ? T * group / kRows + B : (int64_t)B * ((group + kRows - 1) / kRows);
-}
+int workers_of(int cus, int D) { return cus * (D == 256 ? 2 : 3); }
 
-int workers_of(int cus) { return cus * 3; }
-
-template <int DT, int D> hipError_t launch(AttentionParams p, int cus, hipStream_t s)
+template <int DT, int D> hipError_t launch(AttentionParams p, hipStream_t s)
 {
     if (p.workspace) {
-        attention_kernel<DT, D, true><<<grid_of(p.workers), 64 * kAttnWaves, 0, s>>>(p);
-        attention_join_kernel<DT, D><<<grid_of(p.workers), 64 * kAttnWaves, 0, s>>>(p);
+        attention_kernel<DT, D, true><<<grid_of(p.workers), kAttnThreads, 0, s>>>(p);
+        // few blocks have many parts each
+        const int64_t segments = p.blocks * p.c.heads;
+        if (segments * 4 <= p.workers)
+            attention_join_kernel<DT, D, kJoinWaves><<<grid_of(segments * kRows), 64 * kJoinWaves, 0, s>>>(p);
+        else
+            attention_join_kernel<DT, D, 1>
+                <<<grid_of(segments * (kRows / kJoinWaves)), 64 * kJoinWaves, 0, s>>>(p);
     } else {
-        attention_kernel<DT, D, false><<<grid_of(p.blocks * p.c.heads), 64 * kAttnWaves, 0, s>>>(p);
+        attention_kernel<DT, D, false><<<grid_of(p.blocks * p.c.heads), kAttnThreads, 0, s>>>(p);
     }
     return hipGetLastError();
 }
 
-template <int DT> hipError_t launch_width(const AttentionParams &p, int D, int cus, hipStream_t s)
+template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipStream_t s)
 {
-    return D == 64 ? launch<DT, 64>(p, cus, s) : D == 128 ? launch<DT, 128>(p, cus, s) : launch<DT, 256>(p, cus, s);
+    return D == 64 ? launch<DT, 64>(p, s) : D == 128 ? launch<DT, 128>(p, s) : launch<DT, 256>(p, s);
 }
 
-// Whether a batch's quanta are shared out: not where there are blocks for every
-// CU many times over, or more sequences than a worker adds up
+// Whether a batch's quanta may be shared out: not where there are blocks for
+// every CU many times over, or more sequences than a worker adds up
 bool balanced(int64_t T, int B, int q_heads, int kv_heads, int cus)
 {
-    return B <= kMostBalanced && most_blocks(T, B, q_heads / kv_heads, true) * kv_heads < (int64_t)cus * 16;
+    return B <= kMostBalanced && most_blocks(T, B, q_heads / kv_heads, kRows, true) * kv_heads < (int64_t)cus * 16;
+}
+
+// Nor where the quanta's number might not fit 31 bits
+bool countable(const AttentionParams &p)
+{
+    const int64_t blocks = most_blocks(p.T, p.B, p.group, kRows, true) * p.c.heads;
+    return blocks * (p.max_len / kQuantum + 1) <= INT32_MAX;
 }
 
 }  // namespace
 
 uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus)
 {
-    return balanced(T, B, q_heads, kv_heads, cus) ? (uint64_t)workers_of(cus) * 2 * kRows * (head_dim + 2) : 0;
+    if (!balanced(T, B, q_heads, kv_heads, cus))
+        return 0;
+    return (uint64_t)workers_of(cus, head_dim) * 2 * kRows * (head_dim + 2) +
+           (uint64_t)most_blocks(T, B, q_heads / kv_heads, kRows, true) * kv_heads * sizeof(Join) / 4;
 }
 
 hipError_t launch_attention(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
 {
     AttentionParams p = a;
-    p.blocks = most_blocks(p.T, p.B, p.group, p.q_starts != nullptr);
-    p.workers = workers_of(cus);
-    if (!balanced(p.T, p.B, p.q_heads, p.c.heads, cus))
+    p.blocks = most_blocks(p.T, p.B, p.group, kRows, p.q_starts != nullptr);
+    p.workers = workers_of(cus, head_dim);
+    if (!balanced(p.T, p.B, p.q_heads, p.c.heads, cus) || !countable(p))
         p.workspace = nullptr;
-    return dtype == MHC_BF16 ? launch_width<MHC_BF16>(p, head_dim, cus, s)
-                             : launch_width<MHC_F16>(p, head_dim, cus, s);
+    return dtype == MHC_BF16 ? launch_width<MHC_BF16>(p, head_dim, s) : launch_width<MHC_F16>(p, head_dim, s);
 }
 
 }  // namespace mhc

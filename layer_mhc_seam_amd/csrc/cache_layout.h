@@ -23,12 +23,14 @@ struct CacheLayout {
     int32_t heads;
     int32_t page_size;
     uint64_t magic;                  // ceil(2^63 / (page_size / 16))
+    uint32_t magic32;                // ceil(2^32 / (page_size / 16)), 0 for 2^32
 };
 
 MHC_BOTH CacheLayout cache_layout(int64_t pages, int32_t heads, int32_t page_size)
 {
     const uint64_t tiles = (uint64_t)page_size / kCacheTile;
-    return {pages, heads, page_size, ((uint64_t(1) << 63) + tiles - 1) / tiles};
+    return {pages, heads, page_size, ((uint64_t(1) << 63) + tiles - 1) / tiles,
+            (uint32_t)(((uint64_t(1) << 32) + tiles - 1) / tiles)};
 }
 
 MHC_BOTH uint64_t high_product(uint64_t a, uint64_t b)
@@ -73,18 +75,31 @@ MHC_BOTH int64_t cache_page_at(const CacheLayout &c, int64_t page, int head, int
     return (page * c.heads + head) * (int64_t)cache_page_bytes(c.page_size, D);
 }
 
-// The page that a sequence's tokens [t, t + 16), t a multiple of 16, lie on, and
-// where: false, reading no table, where the sequence has none there, and where
-// the table names a page that there is not
-MHC_BOTH bool cache_tile(const CacheLayout &c, const int32_t *table, int64_t len, int64_t t,
-                         int64_t *page, int32_t *at)
+// The page of a sequence, and the place there, that its tokens [t, t + 16), t a
+// multiple of 16 below 2^31, lie on.  Exact: u = t / 16 < 2^27 times magic32's
+// excess, below page_size / 16 <= 32, is below 2^32.
+MHC_BOTH void cache_tile(const CacheLayout &c, int32_t t, int32_t *index, int32_t *at)
 {
-    if (t >= len)
-        return false;
-    int64_t i;
-    cache_place(c, (uint64_t)t, &i, at);
-    *page = table[i];
-    return *page >= 0 && *page < c.pages;
+    const uint32_t u = (uint32_t)t / kCacheTile;
+    const uint32_t i = c.magic32 ? (uint32_t)((uint64_t)u * c.magic32 >> 32) : u;
+    *index = (int32_t)i;
+    *at = (int32_t)((uint32_t)t - i * (uint32_t)c.page_size);
+}
+
+// That tile's page and place there.  Where the sequence of `len` tokens has none
+// at t, or the table names a page that there is not: false, and page 0.  The
+// table is read at no place but those of the sequence's own tokens; len > 0.
+template <typename Table>
+MHC_BOTH bool cache_page(const CacheLayout &c, Table table, int32_t len, int32_t t, int32_t *page, int32_t *at)
+{
+    int32_t index, last, skip;
+    cache_tile(c, t, &index, at);
+    cache_tile(c, (len - 1) / kCacheTile * kCacheTile, &last, &skip);
+    *page = table[index < last ? index : last];
+    const bool there = t < len && *page >= 0 && *page < c.pages;
+    if (!there)
+        *page = *at = 0;
+    return there;
 }
 
 }  // namespace mhc

@@ -33,6 +33,17 @@ int main()
             }
         }
     }
+    // and of a sequence's tokens, up to the last that there can be
+    for (int ps = 16; ps <= kCacheMaxPage; ps += 16) {
+        const CacheLayout c = cache_layout(1, 1, ps);
+        for (int64_t t0 : {int64_t(0), int64_t(1) << 20, int64_t(1234567) * 16, INT32_MAX - int64_t(5) * ps})
+            for (int64_t t = t0 / 16 * 16; t < t0 + 4 * ps; t += 16) {
+                int32_t index, at;
+                cache_tile(c, (int32_t)t, &index, &at);
+                if (index != t / ps || at != t % ps)
+                    return bad("index", ps, t);
+            }
+    }
     for (int D : {64, 128, 256})
         for (int ps : {16, 48, 512})
             for (int heads : {1, 3}) {
@@ -59,22 +70,30 @@ int main()
                         return bad("bytes", D, ps);
                 // tiles of a sequence: tables of exactly their width, with bad pages
                 const std::vector<int32_t> table{2, -1, 0, 3, INT32_MAX, INT32_MIN, 1};
-                const int64_t capacity = (int64_t)table.size() * ps;
-                for (int64_t len : {int64_t(0), int64_t(1), int64_t(ps), 2 * (int64_t)ps + 1, capacity})
-                    for (int64_t t = 0; t < capacity + 64; t += kCacheTile) {
-                        int64_t page;
-                        int32_t at;
-                        const bool there = cache_tile(c, table.data(), len, t, &page, &at);
+                const int capacity = (int)table.size() * ps;
+                for (int len : {1, 15, 16, 17, ps, 2 * ps + 1, capacity})
+                    for (int t = 0; t < capacity + 64; t += kCacheTile) {
+                        int32_t page, at;
+                        const bool there = cache_page(c, table.data(), len, t, &page, &at);
                         const bool want = t < len && table[t / ps] >= 0 && table[t / ps] < 3;
-                        if (there != want || (there && (page != table[t / ps] || at != t % ps)))
+                        if (there != want || (there ? page != table[t / ps] || at != t % ps : page || at))
                             return bad("tile", len, t);
-                        if (there)   // its last token's last bytes
-                            for (int kind = 0; kind < 2; ++kind) {
-                                uint8_t *base = cache.data() + cache_page_at(c, page, heads - 1, D);
-                                ++base[cache_codes(ps, D, kind) + (at + 15) * (D / 2) + D / 2 - 1];
-                                ++base[cache_scales(ps, D, kind) + (D / 32 - 1) * ps + at + 15];
-                            }
+                        // its last token's last bytes, also where it is not there
+                        for (int kind = 0; kind < 2; ++kind) {
+                            uint8_t *base = cache.data() + cache_page_at(c, page, heads - 1, D);
+                            ++base[cache_codes(ps, D, kind) + (at + 15) * (D / 2) + D / 2 - 1];
+                            ++base[cache_scales(ps, D, kind) + (D / 32 - 1) * ps + at + 15];
+                        }
                     }
+                // a table that holds no more than the sequence's pages
+                for (int len = 1; len < 3 * ps; ++len) {
+                    const std::vector<int32_t> own((len + ps - 1) / ps, 1);
+                    for (int t = 0; t < len + 4 * ps; t += kCacheTile) {
+                        int32_t page, at;
+                        if (cache_page(c, own.data(), len, t, &page, &at) != (t < len))
+                            return bad("own", len, t);
+                    }
+                }
             }
     printf("ok\n");
     return 0;
