@@ -650,7 +650,7 @@ int mhc_cache_read(const mhc_cache_args *args, void *stream);
  *              says.  Nothing has to be in it, nothing is kept in it; calls
  *              that may overlap need one each, and so do graphs that may
  * kv_heads divides q_heads, q_heads up to 4096; B up to 65535;
- * table_width * page_size < 2^31; pages * kv_heads < 2^31.
+ * table_width * page_size at most 2^30; pages * kv_heads < 2^31.
  * T == 0 or B == 0 does nothing.
  */
 typedef struct mhc_cache_attention_args {

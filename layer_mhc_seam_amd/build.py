@@ -17,6 +17,7 @@ SOURCES = [os.path.join(CSRC, "seam_kernels.hip"), os.path.join(CSRC, "head_kern
            os.path.join(CSRC, "block_kernels.hip"), os.path.join(CSRC, "int8_kernels.hip"),
            os.path.join(CSRC, "route_kernels.hip"), os.path.join(CSRC, "rope_kernels.hip"),
            os.path.join(CSRC, "cache_kernels.hip"), os.path.join(CSRC, "attention_kernels.hip"),
+           os.path.join(CSRC, "prompt_kernels.hip"),
            os.path.join(CSRC, "seam_runtime.cpp"), os.path.join(CSRC, "block_runtime.cpp"),
            os.path.join(CSRC, "cache_runtime.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -163,17 +163,23 @@ template <int D> __device__ __forceinline__ Page page_of(const AttentionParams &
     return {__builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)cache_page_bytes(P.c.page_size, D), 0x00027000)};
 }
 
-// Scores in base 2 of N products q . k: scaled, capped
+// N products q . k capped: their scores in base 2
+template <int N> __device__ __forceinline__ void cap(const AttentionParams &P, float v[N])
+{
+    const float in = P.scale / P.softcap, out = P.softcap * kLog2e;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // tanh x = 1 - 2 / (exp 2|x| + 1), its sign x's
+        const float e = __builtin_amdgcn_exp2f(fabsf(v[i] * in) * (2.0f * kLog2e));
+        v[i] = copysignf(out - 2.0f * out * __builtin_amdgcn_rcpf(e + 1.0f), v[i] * in);
+    }
+}
+
+// Or as they are: scaled
 template <int N> __device__ __forceinline__ void scores(const AttentionParams &P, float v[N])
 {
     if (P.softcap > 0) {
-        const float in = P.scale / P.softcap, out = P.softcap * kLog2e;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            // tanh x = 1 - 2 / (exp 2|x| + 1), its sign x's
-            const float e = __builtin_amdgcn_exp2f(fabsf(v[i] * in) * (2.0f * kLog2e));
-            v[i] = copysignf(out - 2.0f * out * __builtin_amdgcn_rcpf(e + 1.0f), v[i] * in);
-        }
+        cap<N>(P, v);
     } else {
         const float f = P.scale * kLog2e;
 #pragma unroll

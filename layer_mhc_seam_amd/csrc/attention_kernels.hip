@@ -659,6 +659,9 @@ bool balanced(int64_t T, int B, int q_heads, int kv_heads, int cus)
     return B <= kMostBalanced && most_blocks(T, B, q_heads / kv_heads, kRows, true) * kv_heads < (int64_t)cus * 16;
 }
 
+// Whether the sequences have rows enough, on average, for prompt_kernel
+bool prompts(int64_t T, int B, int group) { return T * group >= (int64_t)B * 64; }
+
 // Nor where the quanta's number might not fit 31 bits
 bool countable(const AttentionParams &p)
 {
@@ -670,7 +673,7 @@ bool countable(const AttentionParams &p)
 
 uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus)
 {
-    if (!balanced(T, B, q_heads, kv_heads, cus))
+    if (prompts(T, B, q_heads / kv_heads) || !balanced(T, B, q_heads, kv_heads, cus))
         return 0;
     return (uint64_t)workers_of(cus, head_dim) * 2 * kRows * (head_dim + 2) +
            (uint64_t)most_blocks(T, B, q_heads / kv_heads, kRows, true) * kv_heads * sizeof(Join) / 4;
@@ -678,6 +681,8 @@ uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads,
 
 hipError_t launch_attention(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
 {
+    if (prompts(a.T, a.B, a.group))
+        return launch_prompt(a, head_dim, dtype, s);
     AttentionParams p = a;
     p.blocks = most_blocks(p.T, p.B, p.group, kRows, p.q_starts != nullptr);
     p.workers = workers_of(cus, head_dim);

@@ -263,10 +263,10 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
     if (!half_type(a->dtype))
         return fail(MHC_SEAM_INVALID_ARG, "cache attention takes bf16 or f16");
     if (!page_known(a->page_size) || a->pages < 1 || a->pages > INT32_MAX / a->kv_heads || a->table_width < 1 ||
-        (int64_t)a->table_width * a->page_size > INT32_MAX)
+        (int64_t)a->table_width * a->page_size > (1 << 30))
         return fail(MHC_SEAM_INVALID_ARG,
                     "cache attention: page_size is a multiple of 16 up to %d, pages > 0, pages*kv_heads < 2^31, "
-                    "0 < table_width*page_size < 2^31", kCacheMaxPage);
+                    "0 < table_width*page_size <= 2^30", kCacheMaxPage);
     if (a->max_len < 0 || a->window < 0 || (a->causal != 0 && a->causal != 1))
         return fail(MHC_SEAM_INVALID_ARG, "max_len and window must not be negative, causal 0 or 1");
     if (!std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0)

@@ -1,0 +1,418 @@
+// prompt_kernels.hip -- attention over the 4-bit cache for many query rows a
+// sequence: prompts and chunks of them.
+//
+// The matrix cores bound it, 4 D operations a row and token.  A workgroup holds
+// kWaves * 32 * CT rows (query rows times heads of a kv head) and goes through
+// the tokens in tiles of 64, once: keys and values are turned from 4 bits into
+// the products' type on their way into LDS, by all waves for all of them, while
+// the tile before is worked on.  A wave's products are 32 x 32 x 16:
+//   S^T = K Q^T     lane (q, h), q = l % 32, h = l / 32, holds row q of Q, and of
+//                   the result tokens 8 b + 4 h + r, b and r 0 .. 3
+//   O^T += V^T P^T  P is the operand as it stands: k = 16 tokens, of which lane h
+//                   has 4 h + r and 8 + 4 h + r.  V lies in LDS in those groups
+//                   of eight tokens, for one channel after another.
+#include "attention_common.h"
+
+namespace mhc {
+namespace {
+
+constexpr int kTile = 64;                // tokens
+constexpr int kGroups = kTile / 8;       // of tokens, as a product's lane has them
+
+template <int D> struct PromptShared {
+    u32x4 k[2][D / 8][kTile];            // eight channels of a token
+    u32x4 v[2][kGroups][D];              // eight tokens of a channel; channel c D/32 + m at m 32 + c
+    u32 nan[2][8];                       // whether a wave met a NaN among a tile's values
+    u32 there[2][4];                     // whether a tile's 16 tokens have a page
+};
+
+// A thread's part of a tile on its way: units of 32 channels of a token's keys,
+// and of eight tokens' values, D/32 channels
+template <int D, int KU> struct Raw {
+    u32x4 k[KU];
+    u32 ks[KU];
+    u32 v[8];
+    u32 vs[2];
+};
+
+template <int DT, int D, int WAVES, int CT> struct Prompt {
+    typedef Half<DT> H;
+    typedef Softmax<DT> S;
+    static constexpr int kThreads = 64 * WAVES, kRows = 32 * CT * WAVES;
+    static constexpr int KC = D / 16, DC = D / 32;
+    static constexpr int kUnits = kTile * (D / 32);                 // of keys
+    static constexpr int KU = (kUnits + kThreads - 1) / kThreads;
+    static constexpr int kFirstV = kThreads - 256;                  // threads from here on take values
+
+    const AttentionParams &P;
+    PromptShared<D> &L;
+    const int lane, wave, q, h;
+    f32x16 o[CT][DC];
+    u32x4 qr[CT][KC];
+    float top[CT], sum[CT];
+    u32 nans[CT];
+    int lo[CT], hi[CT];
+
+    __device__ Prompt(const AttentionParams &p, PromptShared<D> &l)
+        : P(p), L(l), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), q(lane & 31),
+          h(lane >> 5)
+    {
+    }
+
+    // ------------------------------------------------------- a tile's way in
+
+    // Pages of the thread's tokens of the tile at t: of its keys' and of its values'
+    struct Pages {
+        int kp, ka, vp, va;              // page, or -1; place of the 16 tokens there
+    };
+
+    __device__ __forceinline__ int value_group() const { return ((int)threadIdx.x - kFirstV) / 32; }
+
+    __device__ Pages pages(Whole table, int len, int t) const
+    {
+        Pages g;
+        // units u, u + kThreads, .. of keys have one token: 64 divides kThreads
+        const bool k = cache_page(P.c, table, len, t + (int)(threadIdx.x % kTile) / 16 * 16, &g.kp, &g.ka);
+        const bool v = cache_page(P.c, table, len, t + max(value_group(), 0) / 2 * 16, &g.vp, &g.va);
+        g.kp = k ? g.kp : -1;
+        g.vp = v ? g.vp : -1;
+        return g;
+    }
+
+    __device__ __forceinline__ void load(Raw<D, KU> &x, const Pages &g, int head) const
+    {
+        const int ps = P.c.page_size;
+        {
+            const uint8_t *base = P.cache + cache_page_at(P.c, max(g.kp, 0), head, D);
+            const int token = g.ka + threadIdx.x % 16;
+#pragma unroll
+            for (int i = 0; i < KU; ++i) {
+                const int unit = threadIdx.x + i * kThreads, part = unit / kTile;
+                if (unit < kUnits) {
+                    x.k[i] = *(const u32x4 *)(base + token * (D / 2) + part * 16);
+                    x.ks[i] = base[cache_scales(ps, D, 0) + part * ps + token];
+                }
+            }
+        }
+        if ((int)threadIdx.x >= kFirstV) {
+            const uint8_t *base = P.cache + cache_page_at(P.c, max(g.vp, 0), head, D);
+            const int first = g.va + 4 * (value_group() & 1), c = threadIdx.x % 32;
+            const uint8_t *from = base + cache_codes(ps, D, 1) + first * (D / 2) + c * (D / 64);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint8_t *at = from + (i % 4 + i / 4 * 8) * (D / 2);
+                x.v[i] = D == 64 ? *at : D == 128 ? *(const uint16_t *)at : *(const u32 *)at;
+            }
+            const uint8_t *scales = base + cache_scales(ps, D, 1) + c * (D / 32) / 32 * ps + first;
+            x.vs[0] = *(const u32 *)scales;
+            x.vs[1] = *(const u32 *)(scales + 8);
+        }
+    }
+
+    // EDGE: some row sees only some of the tile's tokens.  A NaN among its values
+    // is then left out, and noted.
+    __device__ __forceinline__ void put(Raw<D, KU> &x, const Pages &g, int buf, int len, int t, bool edge)
+    {
+#pragma unroll
+        for (int i = 0; i < KU; ++i) {
+            const int unit = threadIdx.x + i * kThreads, part = unit / kTile, token = threadIdx.x % kTile;
+            if (unit < kUnits) {
+                const float f = scale_of(x.ks[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    L.k[buf][part * 4 + j][token] =
+                        u32x4{H::template from_fp4<0>(x.k[i][j], f), H::template from_fp4<1>(x.k[i][j], f),
+                              H::template from_fp4<2>(x.k[i][j], f), H::template from_fp4<3>(x.k[i][j], f)};
+                if (unit % 16 == 0 && unit < kTile)
+                    L.there[buf][unit / 16] = g.kp >= 0;
+            }
+        }
+        u32 odd = 0;
+        if ((int)threadIdx.x >= kFirstV) {
+            const int group = value_group(), c = threadIdx.x % 32;
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                u32 byte = x.vs[i / 4] >> (8 * (i % 4)) & 255;
+                if (edge || g.vp < 0) {
+                    const bool valid =
+                        g.vp >= 0 && t + group / 2 * 16 + 4 * (group & 1) + i % 4 + i / 4 * 8 < len;
+                    odd |= (u32)(byte == 255 && valid);
+                    x.v[i] = valid ? x.v[i] : 0;
+                    byte = byte == 255 || !valid ? 0 : byte;
+                }
+                f[i] = scale_of(byte);
+            }
+            values<0>(x, f, buf, group, c);
+            if constexpr (D >= 128)
+                values<1 % (D / 64)>(x, f, buf, group, c);
+            if constexpr (D >= 256) {
+                values<2 % (D / 64)>(x, f, buf, group, c);
+                values<3 % (D / 64)>(x, f, buf, group, c);
+            }
+        }
+        if (edge) {
+            const u32 any = __any(odd != 0);
+            if (lane == 0)
+                L.nan[buf][wave] = any;
+        }
+    }
+
+    template <int BYTE>
+    __device__ __forceinline__ void values(const Raw<D, KU> &x, const float f[8], int buf, int group, int c)
+    {
+        u32 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = H::template from_fp4<BYTE>(x.v[i], f[i]);
+        u32x4 a, b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x05040100);
+            b[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x07060302);
+        }
+        L.v[buf][group][(2 * BYTE) * 32 + c] = a;
+        L.v[buf][group][(2 * BYTE + 1) * 32 + c] = b;
+    }
+
+    // ------------------------------------------------------------ a tile's work
+
+    __device__ __forceinline__ void work(int buf, int t, Whole table, int head, bool edge)
+    {
+        f32x16 s[CT][2];
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+            s[i][0] = s[i][1] = f32x16{0};
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                const u32x4 a = L.k[buf][2 * k + h][32 * tt + q];
+#pragma unroll
+                for (int i = 0; i < CT; ++i)
+                    s[i][tt] = H::mfma32(a, qr[i][k], s[i][tt]);
+            }
+        u32 there = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            there |= L.there[buf][j] << j;
+        there = __builtin_amdgcn_readfirstlane(there);
+        u32x4 p[CT][4];
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = s[i][j / 16][j % 16];
+            // scale is not negative: q changed its sign for it
+            float f = fabsf(P.scale) * kLog2e;
+            if (P.softcap > 0) {
+                cap<32>(P, v);
+                f = 1.0f;
+            }
+            const bool masked = edge || there != 15;
+            u32 seen = ~0u;
+            if (masked) {
+                seen = 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int token = t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4;
+                    const bool sees = token >= lo[i] && token < hi[i] && (there >> (j / 8) & 1);
+                    seen |= (u32)sees << j;
+                    v[j] = sees ? v[j] : -__builtin_inff();
+                }
+                if (edge) {
+                    u32 odd = 0;
+#pragma unroll
+                    for (int w = 0; w < WAVES; ++w)
+                        odd |= L.nan[buf][w];
+                    if (__builtin_amdgcn_readfirstlane(odd))
+#pragma unroll 1
+                        for (int j = 0; j < 32; ++j)
+                            if (seen >> j & 1)
+                                nans[i] |= nan_groups<D>(P, table,
+                                                         t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4, head);
+                }
+            }
+            float most = v[0];
+#pragma unroll
+            for (int j = 1; j < 32; ++j)
+                most = fmaxf(most, v[j]);
+            most *= f;
+            if (__any(most > top[i] + S::kSlack)) {
+                const u32 x = __float_as_uint(most);
+                auto both = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+                const float now = fmaxf(top[i], fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])));
+                const float a = __builtin_amdgcn_exp2f(top[i] - now);
+                top[i] = now;
+                sum[i] *= a;
+#pragma unroll
+                for (int d = 0; d < DC; ++d)
+                    o[i][d] *= a;
+            }
+            const float zero = S::kShift - top[i];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = __builtin_amdgcn_exp2f(fmaf(v[j], f, zero));
+            if (masked && f == 0.0f) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = seen >> j & 1 ? v[j] : 0.0f;
+            }
+            float part[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                part[j % 4] += v[j];
+            sum[i] += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                p[i][c] = u32x4{H::pack(v[8 * c], v[8 * c + 1]), H::pack(v[8 * c + 2], v[8 * c + 3]),
+                                H::pack(v[8 * c + 4], v[8 * c + 5]), H::pack(v[8 * c + 6], v[8 * c + 7])};
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int d = 0; d < DC; ++d) {
+                const u32x4 a = L.v[buf][2 * c + h][d * 32 + q];
+#pragma unroll
+                for (int i = 0; i < CT; ++i)
+                    o[i][d] = H::mfma32(a, p[i][c], o[i][d]);
+            }
+    }
+};
+
+template <int DT, int D, int WAVES, int CT>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES / 4)))
+void prompt_kernel(const AttentionParams P)
+{
+    typedef Prompt<DT, D, WAVES, CT> A_;
+    typedef Half<DT> H;
+    __shared__ PromptShared<D> L;
+    constexpr int ROWS = A_::kRows;
+    const int64_t id = block_id() / P.c.heads;
+    const int head = (int)(block_id() - id * P.c.heads);
+    if (id >= P.blocks)
+        return;
+    const int64_t number = P.blocks - 1 - id;        // a prompt's last rows have the most to do
+    int64_t numbered;
+    const int b = sequence_of(P, number, ROWS, &numbered);
+    const int64_t first = row_start(P, b), n64 = row_start(P, b + 1) - first;
+    const int n = (int)max(n64, (int64_t)0);
+    const int64_t row = (number - numbered) * ROWS, rows = (int64_t)n * P.group;
+    if (number < numbered || row >= rows)
+        return;
+    const int len = length_of(P, b);
+    const Whole table = whole(P.tables + b * P.table_stride);
+    const int i0 = (int)(row / P.group), skip = (int)(row - (int64_t)i0 * P.group);
+
+    A_ A(P, L);
+    // tokens that some row, and that every row, of the block sees
+    int least_lo, most_lo, least_hi, most_hi;
+    row_sees(P, len, n, i0, &least_lo, &least_hi);
+    row_sees(P, len, n, min(i0 + (skip + ROWS - 1) / P.group, n - 1), &most_lo, &most_hi);
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+        const int r = skip + (A.wave * CT + i) * 32 + A.q, over = r / P.group;
+        row_sees(P, len, n, i0 + over, &A.lo[i], &A.hi[i]);
+        if (i0 + over >= n)
+            A.lo[i] = A.hi[i] = 0;
+        const uint16_t *at = P.q + (first + min(i0 + over, n - 1)) * P.q_token +
+                             (int64_t)(head * P.group + (r - over * P.group)) * P.q_head;
+        const u32 sign = P.softcap > 0 || P.scale >= 0 ? 0 : 0x80008000u;
+#pragma unroll
+        for (int k = 0; k < A.KC; ++k)
+            A.qr[i][k] = *(const u32x4 *)(at + 16 * k + 8 * A.h) ^ sign;
+        A.top[i] = kLowest;
+        A.sum[i] = 0.0f;
+        A.nans[i] = 0;
+#pragma unroll
+        for (int d = 0; d < A.DC; ++d)
+            A.o[i][d] = f32x16{0};
+    }
+
+    int t = least_lo / kTile * kTile;
+    if (t < most_hi) {
+        auto is_edge = [&](int at) { return at < most_lo || at + kTile > least_hi; };
+        Raw<D, A.KU> x;
+        typename A_::Pages g = A.pages(table, len, t);
+        A.load(x, g, head);
+        typename A_::Pages next = A.pages(table, len, t + kTile);
+        A.put(x, g, 0, len, t, is_edge(t));
+        __syncthreads();
+        int buf = 0;
+        while (true) {
+            // the next tile is asked for, this one worked on, the next one put beside it
+            g = next;
+            const bool more = t + kTile < most_hi;
+            if (more) {
+                A.load(x, g, head);
+                next = A.pages(table, len, t + 2 * kTile);
+            }
+            A.work(buf, t, table, head, is_edge(t));
+            if (!more)
+                break;
+            t += kTile;
+            buf ^= 1;
+            A.put(x, g, buf, len, t, is_edge(t));
+            __syncthreads();
+        }
+    }
+
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+        const u32 s = __float_as_uint(A.sum[i]);
+        auto sums = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+        const float sum = __uint_as_float(sums[0]) + __uint_as_float(sums[1]);
+        auto odd = __builtin_amdgcn_permlane32_swap(A.nans[i], A.nans[i], false, false);
+        const u32 nans = odd[0] | odd[1];
+        const int r = skip + (A.wave * CT + i) * 32 + A.q, over = r / P.group;
+        if (i0 + over >= n)
+            continue;
+        const int64_t at = (first + i0 + over) * P.q_heads + head * P.group + (r - over * P.group);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        // register j of the result is channels (8 (j / 4) + 4 h + j % 4) D/32 + d, d the product's number
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c0 = (8 * j + 4 * A.h) * A.DC;
+            u32 w[2 * A.DC];
+#pragma unroll
+            for (int e = 0; e < 4 * A.DC; e += 2)
+                w[e / 2] = H::pack(A.o[i][e % A.DC][4 * j + e / A.DC] * inv,
+                                   A.o[i][(e + 1) % A.DC][4 * j + (e + 1) / A.DC] * inv);
+            const bool odd_group = nans >> (c0 / 32) & 1;
+            uint16_t *to = P.out + at * D + c0;
+#pragma unroll
+            for (int e = 0; e < 2 * A.DC; e += 4) {
+                const u32 nan = DT == MHC_BF16 ? 0x7fc07fc0u : 0x7e007e00u;
+                const u32x4 v = odd_group ? u32x4{nan, nan, nan, nan} : u32x4{w[e], w[e + 1], w[e + 2], w[e + 3]};
+                *(u32x4 *)(to + 2 * e) = v;
+            }
+        }
+        if (P.lse && A.h == 0)
+            P.lse[at] = sum == 0.0f ? -__builtin_inff()
+                                    : (A.top[i] + __builtin_amdgcn_logf(sum) - Softmax<DT>::kShift) * kLn2;
+    }
+}
+
+template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
+{
+    constexpr int WAVES = 8, CT = 1;
+    AttentionParams q = p;
+    q.blocks = most_blocks(p.T, p.B, p.group, 32 * CT * WAVES, p.q_starts != nullptr);
+    prompt_kernel<DT, D, WAVES, CT><<<grid_of(q.blocks * p.c.heads), 64 * WAVES, 0, s>>>(q);
+    return hipGetLastError();
+}
+
+template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipStream_t s)
+{
+    return D == 64 ? launch<DT, 64>(p, s) : D == 128 ? launch<DT, 128>(p, s) : launch<DT, 256>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_prompt(const AttentionParams &p, int head_dim, int dtype, hipStream_t s)
+{
+    return dtype == MHC_BF16 ? launch_width<MHC_BF16>(p, head_dim, s) : launch_width<MHC_F16>(p, head_dim, s);
+}
+
+}  // namespace mhc

@@ -116,9 +116,22 @@ def test_prompts(T, L, Hq, Hk, dt):
 
 
 @pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal,window,softcap,scale", [(True, 0, 0.0, None), (False, 0, 0.0, None), (True, 50, 0.0, -0.2),
+                                                         (False, 70, 8.0, None), (True, 1, 30.0, -0.1),
+                                                         (True, 400, 5.0, None), (True, 0, 0.0, 0.0)])
+def test_prompt_masks(causal, window, softcap, scale, D, dt):
+    """Rows for several workgroups, of heads in threes and more, some with more rows than tokens."""
+    both([190, 130, 64, 5, 0, 333], [150, 130, 1, 90, 3, 0], 6, 2, D, 48, dt, causal=causal, window=window,
+         softcap=softcap, scale=scale)
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
 def test_sharp_scores(dt):
     """Scores far apart: a maximum that moves often, weights that vanish."""
     both([600, 50], [3, 50], 4, 2, 128, 16, dt, sharp=30.0)
+    both([600, 250], [100, 250], 4, 2, 128, 16, dt, sharp=30.0)
+    both([600], [90], 2, 1, 256, 16, dt, sharp=100.0)
     both([600, 50], [1, 1], 4, 2, 64, 16, dt, sharp=200.0)
     both([600, 50], [1, 1], 4, 2, 64, 16, dt, scale=-0.3)
     both([600, 50], [1, 1], 4, 2, 64, 16, dt, scale=0.0)
@@ -134,9 +147,11 @@ def test_rising_maximum():
         t = torch.arange(900)
         slots = d["tables"][0][t // 16].long() * 16 + t % 16
         d["cache"], hk, hv = ref.packed(k, v, slots, d["cache"].shape[0], 16)
-        d["q"] = torch.zeros(1, 1, 64, dtype=BF)
-        d["q"][0, 0, 0] = 1.0
-        check(run(d, scale=1.0), ref.attention(d["q"], [hk], [hv], [900], [0, 1], scale=1.0))
+        for n in (1, 100):
+            d["q"] = torch.zeros(n, 1, 64, dtype=BF)
+            d["q"][:, 0, 0] = 1.0
+            d["starts"] = [0, n]
+            check(run(d, scale=1.0), ref.attention(d["q"], [hk], [hv], [900], [0, n], scale=1.0))
 
 
 def test_many_tiny_weights():
@@ -150,11 +165,12 @@ def test_many_tiny_weights():
     t = torch.arange(n)
     slots = d["tables"][0][t // 512].long() * 512 + t % 512
     d["cache"], hk, hv = ref.packed(k, v, slots, d["cache"].shape[0], 512)
-    d["q"] = torch.zeros(1, 1, 64, dtype=F16)
-    for gap in (14.0, 17.0, 19.0):
-        d["q"][0, 0, 0] = gap
+    for gap, rows in ((14.0, 1), (17.0, 1), (19.0, 1), (17.0, 70)):
+        d["q"] = torch.zeros(rows, 1, 64, dtype=F16)
+        d["q"][:, 0, 0] = gap
+        d["starts"] = [0, rows]
         got = run(d, scale=1.0)
-        want = ref.attention(d["q"], [hk], [hv], [n], [0, 1], scale=1.0)
+        want = ref.attention(d["q"], [hk], [hv], [n], [0, rows], scale=1.0)
         check(got, want)
         assert ((got[0].cpu().double() / want[0] - 1).abs() < 2.0 ** -8).all() or want[0].max() < 2.0 ** -14
 
@@ -170,27 +186,30 @@ def put(d, b, t, kind, D, ps, block, byte=255):
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dt", [BF, F16])
-def test_nan_reaches_who_sees_it(D, dt):
+@pytest.mark.parametrize("lens,rows,window", [((70, 140, 300), (30, 4, 1), 0), ((170, 240, 300), (130, 100, 1), 0),
+                                              ((170, 240, 300), (130, 100, 1), 60)])
+def test_nan_reaches_who_sees_it(lens, rows, window, D, dt):
     """A NaN in a key makes the rows that see it NaN, one in a value only its 32 channels of them."""
-    lens, rows, ps = [70, 140, 300], [30, 4, 1], 16
+    ps = 16
     d, keys, values = batch(lens, rows, 4, 2, D, ps, dt, seed=9)
-    for b, t, kind, block in ((0, 45, 1, 1), (0, 60, 0, 0), (1, 138, 1, D // 32 - 1), (1, 139, 0, 1), (2, 20, 1, 0),
-                              (2, 133, 1, 1)):
+    for b, t, kind, block in ((0, lens[0] - 25, 1, 1), (0, lens[0] - 10, 0, 0), (1, lens[1] - 2, 1, D // 32 - 1),
+                              (1, lens[1] - 1, 0, 1), (2, 20, 1, 0), (2, 260, 1, 1), (1, 20, 1, 0)):
         put(d, b, t, kind, D, ps, block)
         (values if kind else keys)[b][t, :, block * 32:block * 32 + 32] = math.nan
-    got = run(d)
+    got = run(d, window=window)
     out, lse = got[0].cpu().to(F64), got[1].cpu().to(F64)
-    w, l, bound, lbound = ref.attention(d["q"], keys, values, lens, d["starts"])
+    w, l, bound, lbound = ref.attention(d["q"], keys, values, lens, d["starts"], window=window)
     assert torch.equal(out.isnan(), w.isnan()) and torch.equal(lse.isnan(), l.isnan())
-    assert w.isnan().any() and not w.isnan().all(dim=(1, 2))[:15].any()
+    assert w.isnan().any() and not w.isnan().all(dim=(1, 2)).all()
     fine = ~w.isnan()
     assert ((out - w).abs()[fine] <= bound[fine]).all()
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_what_nobody_sees_may_be_anything(D):
+@pytest.mark.parametrize("rows", [(1, 3, 1, 2), (70, 129, 1, 100)])
+def test_what_nobody_sees_may_be_anything(rows, D):
     """Bytes of 255 everywhere but in the tokens: behind the last one, in other pages, before a window."""
-    lens, rows, ps = [70, 129, 1, 260], [1, 3, 1, 2], 32
+    lens, ps = [70, 129, 1, 260], 32
     for kw in ({}, dict(window=40)):
         d, keys, values = batch(lens, rows, 4, 2, D, ps, BF, seed=2)
         clean = run(d, **kw)
@@ -206,10 +225,12 @@ def test_what_nobody_sees_may_be_anything(D):
         d["cache"] = dirty
         got = run(d, **kw)
         assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+        check(got, ref.attention(d["q"], keys, values, lens, d["starts"], **kw))
 
 
-def test_bad_pages_hide_their_tokens():
-    lens, rows, ps, D = [100, 64, 40], [3, 1, 1], 16, 128
+@pytest.mark.parametrize("rows", [(3, 1, 1), (80, 60, 33)])
+def test_bad_pages_hide_their_tokens(rows):
+    lens, ps, D = [100, 64, 40], 16, 128
     d, keys, values = batch(lens, rows, 4, 2, D, ps, BF, seed=4)
     seen = [torch.ones(n, dtype=torch.bool) for n in lens]
     pages = d["cache"].shape[0]
@@ -244,10 +265,15 @@ def test_lengths_and_rows_that_do_not_fit():
     w = ref.attention(q, keys, values, lens, [1, 3, 3, 4])
     check((out[1:4], lse[1:4]), tuple(x[1:4] for x in w))
     # falling starts, and ones outside the rows: nothing is written outside, nothing read
-    for bad in ([3, 1, 0, 2], [0, 9, 9, 9], [-4, 2, 1, 5], [2 ** 31 - 1, 0, 5, 2 ** 31 - 1], [-9, -8, -7, -6]):
-        S.cache_attention(q.cuda(), d["cache"].cuda(), d["tables"].cuda(), d["lens"].cuda(),
-                          q_starts=torch.tensor(bad, dtype=torch.int32).cuda())
-    torch.cuda.synchronize()
+    many = torch.randn(200, 4, D).to(BF)
+    for rows in (q, many):
+        T = len(rows)
+        guard = torch.full((T + 64, 4, D), 7.0, dtype=BF).cuda()
+        for bad in ([3, 1, 0, 2], [0, 9, 9, 9], [-4, 2, 1, 5], [2 ** 31 - 1, 0, 5, 2 ** 31 - 1], [-9, -8, -7, -6],
+                    [0, T, T // 2, 2 * T]):
+            S.cache_attention(rows.cuda(), d["cache"].cuda(), d["tables"].cuda(), d["lens"].cuda(), out=guard[32:T + 32],
+                              q_starts=torch.tensor(bad, dtype=torch.int32).cuda())
+        assert (guard[:32] == 7.0).all() and (guard[T + 32:] == 7.0).all()
 
 
 def test_slices():
