@@ -175,18 +175,5 @@ template <int N> __device__ __forceinline__ void cap(const AttentionParams &P, f
     }
 }
 
-// Or as they are: scaled
-template <int N> __device__ __forceinline__ void scores(const AttentionParams &P, float v[N])
-{
-    if (P.softcap > 0) {
-        cap<N>(P, v);
-    } else {
-        const float f = P.scale * kLog2e;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] *= f;
-    }
-}
-
 }  // namespace
 }  // namespace mhc

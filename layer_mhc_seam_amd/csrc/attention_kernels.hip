@@ -169,7 +169,7 @@ struct Rows {
     int most_lo, least_hi;   // that every row of the block sees
 };
 
-template <int DT, int D> struct Attention {
+template <int DT, int D, bool CAP> struct Attention {
     typedef Half<DT> H;
     typedef Softmax<DT> S;
     static constexpr int KC = D / 32;        // products of a score: 8 channels a lane each
@@ -311,7 +311,14 @@ template <int DT, int D> struct Attention {
             for (int i = 0; i < 4; ++i)
                 v[4 * h + i] = s[i];
         }
-        scores<8>(P, v);
+        if constexpr (CAP) {
+            cap<8>(P, v);
+        } else {
+            const float f = P.scale * kLog2e;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] *= f;
+        }
         if (!(t0 >= rows.most_lo && t0 + kStep <= rows.least_hi && x.there[0] && x.there[1]))
             mask(x, v, rows, len, table, t0, head);
         const float most =
@@ -421,7 +428,7 @@ __device__ __forceinline__ void store(const AttentionParams &P, int64_t i, int s
 
 // BALANCED: the workers share all quanta evenly, and a block that several have
 // parts of is put together by attention_join_kernel.  Otherwise a workgroup a block.
-template <int DT, int D, bool BALANCED>
+template <int DT, int D, bool CAP, bool BALANCED>
 __global__ __launch_bounds__(kAttnThreads)
     __attribute__((amdgpu_waves_per_eu(2))) void attention_kernel(const AttentionParams P)
 {
@@ -456,7 +463,7 @@ __global__ __launch_bounds__(kAttnThreads)
         at = 0;
         end = s.quanta;
     }
-    Attention<DT, D> A(P);
+    Attention<DT, D, CAP> A(P);
     const int begin = at;
     while (at < end) {
         int from = 0;
@@ -630,20 +637,26 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(const A
 
 int workers_of(int cus, int D) { return cus * (D == 256 ? 2 : 3); }
 
-template <int DT, int D> hipError_t launch(AttentionParams p, hipStream_t s)
+template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
 {
-    if (p.workspace) {
-        attention_kernel<DT, D, true><<<grid_of(p.workers), kAttnThreads, 0, s>>>(p);
-        // few blocks have many parts each
-        const int64_t segments = p.blocks * p.c.heads;
-        if (segments * 4 <= p.workers)
-            attention_join_kernel<DT, D, kJoinWaves><<<grid_of(segments * kRows), 64 * kJoinWaves, 0, s>>>(p);
-        else
-            attention_join_kernel<DT, D, 1>
-                <<<grid_of(segments * (kRows / kJoinWaves)), 64 * kJoinWaves, 0, s>>>(p);
-    } else {
-        attention_kernel<DT, D, false><<<grid_of(p.blocks * p.c.heads), kAttnThreads, 0, s>>>(p);
-    }
+    const int64_t segments = p.blocks * p.c.heads;
+    if (p.workspace)
+        attention_kernel<DT, D, CAP, true><<<grid_of(p.workers), kAttnThreads, 0, s>>>(p);
+    else
+        attention_kernel<DT, D, CAP, false><<<grid_of(segments), kAttnThreads, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
+{
+    const int64_t segments = p.blocks * p.c.heads;
+    const hipError_t e = p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
+    if (e != hipSuccess || !p.workspace)
+        return e;
+    if (segments * 4 <= p.workers)      // few blocks have many parts each
+        attention_join_kernel<DT, D, kJoinWaves><<<grid_of(segments * kRows), 64 * kJoinWaves, 0, s>>>(p);
+    else
+        attention_join_kernel<DT, D, 1><<<grid_of(segments * (kRows / kJoinWaves)), 64 * kJoinWaves, 0, s>>>(p);
     return hipGetLastError();
 }
 

@@ -33,9 +33,10 @@ template <int D, int KU> struct Raw {
     u32 ks[KU];
     u32 v[8];
     u32 vs[2];
+    bool k_there, v_there;
 };
 
-template <int DT, int D, int WAVES, int CT> struct Prompt {
+template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
     typedef Half<DT> H;
     typedef Softmax<DT> S;
     static constexpr int kThreads = 64 * WAVES, kRows = 32 * CT * WAVES;
@@ -50,6 +51,7 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
     f32x16 o[CT][DC];
     u32x4 qr[CT][KC];
     float top[CT], sum[CT];
+    float factor;                        // of the products, to scores in base 2; not negative
     u32 nans[CT];
     int lo[CT], hi[CT];
 
@@ -61,49 +63,67 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
 
     // ------------------------------------------------------- a tile's way in
 
-    // Pages of the thread's tokens of the tile at t: of its keys' and of its values'
+    // Pages of the thread's tokens of a tile, as the table has them: of its keys'
+    // and of its values'.  Nothing is done with them before they are used, a tile
+    // later.
     struct Pages {
-        int kp, ka, vp, va;              // page, or -1; place of the 16 tokens there
+        int k, v;
     };
 
     __device__ __forceinline__ int value_group() const { return ((int)threadIdx.x - kFirstV) / 32; }
+    // First of the 16 tokens that the thread's are of, in the tile.  Units u, u +
+    // kThreads, .. of keys have one token: 64 divides kThreads.
+    __device__ __forceinline__ int key_tile() const { return (int)(threadIdx.x % kTile) / 16 * 16; }
+    __device__ __forceinline__ int value_tile() const { return max(value_group(), 0) / 2 * 16; }
 
-    __device__ Pages pages(Whole table, int len, int t) const
+    __device__ __forceinline__ Pages pages(const int32_t *table, int last, int t) const
     {
-        Pages g;
-        // units u, u + kThreads, .. of keys have one token: 64 divides kThreads
-        const bool k = cache_page(P.c, table, len, t + (int)(threadIdx.x % kTile) / 16 * 16, &g.kp, &g.ka);
-        const bool v = cache_page(P.c, table, len, t + max(value_group(), 0) / 2 * 16, &g.vp, &g.va);
-        g.kp = k ? g.kp : -1;
-        g.vp = v ? g.vp : -1;
-        return g;
+        int k, v, at;
+        cache_tile(P.c, t + key_tile(), &k, &at);
+        cache_tile(P.c, t + value_tile(), &v, &at);
+        return {table[min(k, last)], table[min(v, last)]};
     }
 
-    __device__ __forceinline__ void load(Raw<D, KU> &x, const Pages &g, int head) const
+    // Whether that page is one, and tokens [t, t + 16) among the sequence's; the page
+    // and their place there, or page 0
+    __device__ __forceinline__ bool there(int raw, int len, int t, int *page, int *at) const
+    {
+        int index;
+        cache_tile(P.c, t, &index, at);
+        const bool ok = t < len && raw >= 0 && raw < P.c.pages;
+        *page = ok ? raw : 0;
+        *at = ok ? *at : 0;
+        return ok;
+    }
+
+    __device__ __forceinline__ void load(Raw<D, KU> &x, const Pages &g, int len, int t, int head) const
     {
         const int ps = P.c.page_size;
+        int page, at;
+        x.k_there = there(g.k, len, t + key_tile(), &page, &at);
         {
-            const uint8_t *base = P.cache + cache_page_at(P.c, max(g.kp, 0), head, D);
-            const int token = g.ka + threadIdx.x % 16;
+            const uint8_t *base = P.cache + cache_page_at(P.c, page, head, D);
+            const int token = at + threadIdx.x % 16;
 #pragma unroll
             for (int i = 0; i < KU; ++i) {
                 const int unit = threadIdx.x + i * kThreads, part = unit / kTile;
-                if (unit < kUnits) {
-                    x.k[i] = *(const u32x4 *)(base + token * (D / 2) + part * 16);
-                    x.ks[i] = base[cache_scales(ps, D, 0) + part * ps + token];
+                if (kUnits % kThreads == 0 || unit < kUnits) {
+                    x.k[i] = *(const u32x4 *)(base + (u32)(token * (D / 2) + part * 16));
+                    x.ks[i] = base[cache_scales(ps, D, 0) + (u32)(part * ps + token)];
                 }
             }
         }
-        if ((int)threadIdx.x >= kFirstV) {
-            const uint8_t *base = P.cache + cache_page_at(P.c, max(g.vp, 0), head, D);
-            const int first = g.va + 4 * (value_group() & 1), c = threadIdx.x % 32;
-            const uint8_t *from = base + cache_codes(ps, D, 1) + first * (D / 2) + c * (D / 64);
+        if (kFirstV == 0 || (int)threadIdx.x >= kFirstV) {
+            x.v_there = there(g.v, len, t + value_tile(), &page, &at);
+            const uint8_t *base = P.cache + cache_page_at(P.c, page, head, D);
+            const int first = at + 4 * (value_group() & 1), c = threadIdx.x % 32;
+            const uint8_t *from = base + (u32)(cache_codes(ps, D, 1) + first * (D / 2) + c * (D / 64));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint8_t *at = from + (i % 4 + i / 4 * 8) * (D / 2);
-                x.v[i] = D == 64 ? *at : D == 128 ? *(const uint16_t *)at : *(const u32 *)at;
+                const uint8_t *code = from + (i % 4 + i / 4 * 8) * (D / 2);
+                x.v[i] = D == 64 ? *code : D == 128 ? *(const uint16_t *)code : *(const u32 *)code;
             }
-            const uint8_t *scales = base + cache_scales(ps, D, 1) + c * (D / 32) / 32 * ps + first;
+            const uint8_t *scales = base + (u32)(cache_scales(ps, D, 1) + c * (D / 32) / 32 * ps + first);
             x.vs[0] = *(const u32 *)scales;
             x.vs[1] = *(const u32 *)(scales + 8);
         }
@@ -111,12 +131,12 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
 
     // EDGE: some row sees only some of the tile's tokens.  A NaN among its values
     // is then left out, and noted.
-    __device__ __forceinline__ void put(Raw<D, KU> &x, const Pages &g, int buf, int len, int t, bool edge)
+    __device__ __forceinline__ void put(Raw<D, KU> &x, int buf, int len, int t, bool edge)
     {
 #pragma unroll
         for (int i = 0; i < KU; ++i) {
             const int unit = threadIdx.x + i * kThreads, part = unit / kTile, token = threadIdx.x % kTile;
-            if (unit < kUnits) {
+            if (kUnits % kThreads == 0 || unit < kUnits) {
                 const float f = scale_of(x.ks[i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -124,19 +144,19 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
                         u32x4{H::template from_fp4<0>(x.k[i][j], f), H::template from_fp4<1>(x.k[i][j], f),
                               H::template from_fp4<2>(x.k[i][j], f), H::template from_fp4<3>(x.k[i][j], f)};
                 if (unit % 16 == 0 && unit < kTile)
-                    L.there[buf][unit / 16] = g.kp >= 0;
+                    L.there[buf][unit / 16] = x.k_there;
             }
         }
         u32 odd = 0;
-        if ((int)threadIdx.x >= kFirstV) {
+        if (kFirstV == 0 || (int)threadIdx.x >= kFirstV) {
             const int group = value_group(), c = threadIdx.x % 32;
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 u32 byte = x.vs[i / 4] >> (8 * (i % 4)) & 255;
-                if (edge || g.vp < 0) {
+                if (edge || !x.v_there) {
                     const bool valid =
-                        g.vp >= 0 && t + group / 2 * 16 + 4 * (group & 1) + i % 4 + i / 4 * 8 < len;
+                        x.v_there && t + group / 2 * 16 + 4 * (group & 1) + i % 4 + i / 4 * 8 < len;
                     odd |= (u32)(byte == 255 && valid);
                     x.v[i] = valid ? x.v[i] : 0;
                     byte = byte == 255 || !valid ? 0 : byte;
@@ -177,8 +197,46 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
 
     // ------------------------------------------------------------ a tile's work
 
+    // Whether the tile's 16 tokens have their pages, a bit each
+    __device__ __forceinline__ u32 pages_there(int buf) const
+    {
+        u32 there = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            there |= L.there[buf][j] << j;
+        return __builtin_amdgcn_readfirstlane(there);
+    }
+
+    // Hides what the lane's row does not see of the tile: edge, by the rows'
+    // bounds; there, for its page
+    __device__ __forceinline__ void mask(float v[32], int i, int buf, int t, Whole table, int head, bool edge,
+                                         u32 there)
+    {
+        u32 seen = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int token = t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4;
+            const bool sees = token >= lo[i] && token < hi[i] && (there >> (j / 8) & 1);
+            seen |= (u32)sees << j;
+            v[j] = sees ? v[j] : -__builtin_inff();
+        }
+        if (!edge)
+            return;
+        u32 odd = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            odd |= L.nan[buf][w];
+        if (__builtin_amdgcn_readfirstlane(odd))
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j)
+                if (seen >> j & 1)
+                    nans[i] |=
+                        nan_groups<D>(P, table, t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4, head);
+    }
+
     __device__ __forceinline__ void work(int buf, int t, Whole table, int head, bool edge)
     {
+        const u32 there = pages_there(buf);
         f32x16 s[CT][2];
 #pragma unroll
         for (int i = 0; i < CT; ++i)
@@ -192,11 +250,6 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
                 for (int i = 0; i < CT; ++i)
                     s[i][tt] = H::mfma32(a, qr[i][k], s[i][tt]);
             }
-        u32 there = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            there |= L.there[buf][j] << j;
-        there = __builtin_amdgcn_readfirstlane(there);
         u32x4 p[CT][4];
 #pragma unroll
         for (int i = 0; i < CT; ++i) {
@@ -204,41 +257,15 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 v[j] = s[i][j / 16][j % 16];
-            // scale is not negative: q changed its sign for it
-            float f = fabsf(P.scale) * kLog2e;
-            if (P.softcap > 0) {
+            if constexpr (CAP)
                 cap<32>(P, v);
-                f = 1.0f;
-            }
-            const bool masked = edge || there != 15;
-            u32 seen = ~0u;
-            if (masked) {
-                seen = 0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int token = t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4;
-                    const bool sees = token >= lo[i] && token < hi[i] && (there >> (j / 8) & 1);
-                    seen |= (u32)sees << j;
-                    v[j] = sees ? v[j] : -__builtin_inff();
-                }
-                if (edge) {
-                    u32 odd = 0;
-#pragma unroll
-                    for (int w = 0; w < WAVES; ++w)
-                        odd |= L.nan[buf][w];
-                    if (__builtin_amdgcn_readfirstlane(odd))
-#pragma unroll 1
-                        for (int j = 0; j < 32; ++j)
-                            if (seen >> j & 1)
-                                nans[i] |= nan_groups<D>(P, table,
-                                                         t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4, head);
-                }
-            }
+            if (edge || there != 15)
+                mask(v, i, buf, t, table, head, edge, there);
             float most = v[0];
 #pragma unroll
             for (int j = 1; j < 32; ++j)
                 most = fmaxf(most, v[j]);
-            most *= f;
+            most *= factor;
             if (__any(most > top[i] + S::kSlack)) {
                 const u32 x = __float_as_uint(most);
                 auto both = __builtin_amdgcn_permlane32_swap(x, x, false, false);
@@ -253,12 +280,7 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
             const float zero = S::kShift - top[i];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                v[j] = __builtin_amdgcn_exp2f(fmaf(v[j], f, zero));
-            if (masked && f == 0.0f) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    v[j] = seen >> j & 1 ? v[j] : 0.0f;
-            }
+                v[j] = __builtin_amdgcn_exp2f(fmaf(v[j], factor, zero));
             float part[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -281,11 +303,11 @@ template <int DT, int D, int WAVES, int CT> struct Prompt {
     }
 };
 
-template <int DT, int D, int WAVES, int CT>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES / 4)))
+template <int DT, int D, int WAVES, int CT, bool CAP>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 void prompt_kernel(const AttentionParams P)
 {
-    typedef Prompt<DT, D, WAVES, CT> A_;
+    typedef Prompt<DT, D, WAVES, CT, CAP> A_;
     typedef Half<DT> H;
     __shared__ PromptShared<D> L;
     constexpr int ROWS = A_::kRows;
@@ -306,6 +328,10 @@ void prompt_kernel(const AttentionParams P)
     const int i0 = (int)(row / P.group), skip = (int)(row - (int64_t)i0 * P.group);
 
     A_ A(P, L);
+    // a negative scale's sign goes to the queries, one of 0 makes them 0: the
+    // scores' order is that of their products, and -inf times the factor -inf
+    const u32 sign = CAP || P.scale >= 0 ? 0 : 0x80008000u, keep = CAP || P.scale != 0 ? ~0u : 0;
+    A.factor = CAP ? 1.0f : P.scale != 0 ? fabsf(P.scale) * kLog2e : 1.0f;
     // tokens that some row, and that every row, of the block sees
     int least_lo, most_lo, least_hi, most_hi;
     row_sees(P, len, n, i0, &least_lo, &least_hi);
@@ -318,10 +344,9 @@ void prompt_kernel(const AttentionParams P)
             A.lo[i] = A.hi[i] = 0;
         const uint16_t *at = P.q + (first + min(i0 + over, n - 1)) * P.q_token +
                              (int64_t)(head * P.group + (r - over * P.group)) * P.q_head;
-        const u32 sign = P.softcap > 0 || P.scale >= 0 ? 0 : 0x80008000u;
 #pragma unroll
         for (int k = 0; k < A.KC; ++k)
-            A.qr[i][k] = *(const u32x4 *)(at + 16 * k + 8 * A.h) ^ sign;
+            A.qr[i][k] = (*(const u32x4 *)(at + 16 * k + 8 * A.h) & keep) ^ sign;
         A.top[i] = kLowest;
         A.sum[i] = 0.0f;
         A.nans[i] = 0;
@@ -334,26 +359,28 @@ void prompt_kernel(const AttentionParams P)
     if (t < most_hi) {
         auto is_edge = [&](int at) { return at < most_lo || at + kTile > least_hi; };
         Raw<D, A.KU> x;
-        typename A_::Pages g = A.pages(table, len, t);
-        A.load(x, g, head);
-        typename A_::Pages next = A.pages(table, len, t + kTile);
-        A.put(x, g, 0, len, t, is_edge(t));
+        const int32_t *entries = P.tables + b * P.table_stride;
+        int last, none;
+        cache_tile(P.c, (len - 1) / kCacheTile * kCacheTile, &last, &none);
+        typename A_::Pages g = A.pages(entries, last, t);
+        A.load(x, g, len, t, head);
+        g = A.pages(entries, last, t + kTile);
+        A.put(x, 0, len, t, is_edge(t));
         __syncthreads();
         int buf = 0;
         while (true) {
             // the next tile is asked for, this one worked on, the next one put beside it
-            g = next;
             const bool more = t + kTile < most_hi;
             if (more) {
-                A.load(x, g, head);
-                next = A.pages(table, len, t + 2 * kTile);
+                A.load(x, g, len, t + kTile, head);
+                g = A.pages(entries, last, t + 2 * kTile);
             }
             A.work(buf, t, table, head, is_edge(t));
             if (!more)
                 break;
             t += kTile;
             buf ^= 1;
-            A.put(x, g, buf, len, t, is_edge(t));
+            A.put(x, buf, len, t, is_edge(t));
             __syncthreads();
         }
     }
@@ -394,13 +421,18 @@ void prompt_kernel(const AttentionParams P)
     }
 }
 
-template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
+template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
 {
-    constexpr int WAVES = 8, CT = 1;
+    constexpr int WAVES = 4, CT = 1;
     AttentionParams q = p;
     q.blocks = most_blocks(p.T, p.B, p.group, 32 * CT * WAVES, p.q_starts != nullptr);
-    prompt_kernel<DT, D, WAVES, CT><<<grid_of(q.blocks * p.c.heads), 64 * WAVES, 0, s>>>(q);
+    prompt_kernel<DT, D, WAVES, CT, CAP><<<grid_of(q.blocks * p.c.heads), 64 * WAVES, 0, s>>>(q);
     return hipGetLastError();
+}
+
+template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
+{
+    return p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
 }
 
 template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipStream_t s)
