@@ -120,7 +120,7 @@ __device__ u32 nan_groups(const AttentionParams &P, Whole table, int32_t t, int 
     int32_t page, at;
     if (!cache_page(P.c, table, t + 1, t / kCacheTile * kCacheTile, &page, &at))
         return 0;
-    const uint8_t *vs = P.cache + cache_page_at(P.c, page, head, D) + cache_scales(P.c.page_size, D, 1) + at +
+    const uint8_t *vs = P.cache + cache_page_near(P.c, page, head, D) + cache_scales(P.c.page_size, D, 1) + at +
                         t % kCacheTile;
     u32 bits = 0;
     for (int j = 0; j < D / 32; ++j)
@@ -159,7 +159,7 @@ struct Page {
 
 template <int D> __device__ __forceinline__ Page page_of(const AttentionParams &P, int page, int head)
 {
-    const uint8_t *base = P.cache + cache_page_at(P.c, page, head, D);
+    const uint8_t *base = P.cache + cache_page_near(P.c, page, head, D);
     return {__builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)cache_page_bytes(P.c.page_size, D), 0x00027000)};
 }
 

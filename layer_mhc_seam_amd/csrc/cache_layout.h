@@ -23,14 +23,14 @@ struct CacheLayout {
     int32_t heads;
     int32_t page_size;
     uint64_t magic;                  // ceil(2^63 / (page_size / 16))
-    uint32_t magic32;                // ceil(2^32 / (page_size / 16)), 0 for 2^32
+    uint32_t magic32, whole;         // ceil(2^32 / (page_size / 16)), or 0 and 1
 };
 
 MHC_BOTH CacheLayout cache_layout(int64_t pages, int32_t heads, int32_t page_size)
 {
     const uint64_t tiles = (uint64_t)page_size / kCacheTile;
     return {pages, heads, page_size, ((uint64_t(1) << 63) + tiles - 1) / tiles,
-            (uint32_t)(((uint64_t(1) << 32) + tiles - 1) / tiles)};
+            (uint32_t)(((uint64_t(1) << 32) + tiles - 1) / tiles), tiles == 1};
 }
 
 MHC_BOTH uint64_t high_product(uint64_t a, uint64_t b)
@@ -75,13 +75,19 @@ MHC_BOTH int64_t cache_page_at(const CacheLayout &c, int64_t page, int head, int
     return (page * c.heads + head) * (int64_t)cache_page_bytes(c.page_size, D);
 }
 
+// The same where pages * heads < 2^31
+MHC_BOTH uint64_t cache_page_near(const CacheLayout &c, int32_t page, int head, int D)
+{
+    return (uint64_t)(uint32_t)(page * c.heads + head) * cache_page_bytes(c.page_size, D);
+}
+
 // The page of a sequence, and the place there, that its tokens [t, t + 16), t a
 // multiple of 16 below 2^31, lie on.  Exact: u = t / 16 < 2^27 times magic32's
 // excess, below page_size / 16 <= 32, is below 2^32.
 MHC_BOTH void cache_tile(const CacheLayout &c, int32_t t, int32_t *index, int32_t *at)
 {
     const uint32_t u = (uint32_t)t / kCacheTile;
-    const uint32_t i = c.magic32 ? (uint32_t)((uint64_t)u * c.magic32 >> 32) : u;
+    const uint32_t i = (uint32_t)((uint64_t)u * c.magic32 >> 32) + u * c.whole;
     *index = (int32_t)i;
     *at = (int32_t)((uint32_t)t - i * (uint32_t)c.page_size);
 }

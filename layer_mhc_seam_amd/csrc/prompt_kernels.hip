@@ -21,20 +21,23 @@ constexpr int kGroups = kTile / 8;       // of tokens, as a product's lane has t
 
 template <int D> struct PromptShared {
     u32x4 k[2][D / 8][kTile];            // eight channels of a token
-    u32x4 v[2][kGroups][D];              // eight tokens of a channel; channel c D/32 + m at m 32 + c
+    u32x2 v[2][kGroups][D][2];           // eight tokens of a channel; channel c D/16 + m at m 16 + c
     u32 nan[2][8];                       // whether a wave met a NaN among a tile's values
     u32 there[2][4];                     // whether a tile's 16 tokens have a page
 };
 
 // A thread's part of a tile on its way: units of 32 channels of a token's keys,
-// and of eight tokens' values, D/32 channels
+// and four tokens' values, D/16 channels.  Short loads are of four bytes that
+// begin with theirs, for the compiler to have nothing to cut off behind them.
 template <int D, int KU> struct Raw {
     u32x4 k[KU];
     u32 ks[KU];
-    u32 v[8];
-    u32 vs[2];
+    u32 v[4][(D + 127) / 128];
+    u32 vs;
     bool k_there, v_there;
 };
+
+typedef u32 u32_any __attribute__((aligned(1)));
 
 template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
     typedef Half<DT> H;
@@ -67,7 +70,7 @@ template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
     // and of its values'.  Nothing is done with them before they are used, a tile
     // later.
     struct Pages {
-        int k, v;
+        int k, k_at, v, v_at;
     };
 
     __device__ __forceinline__ int value_group() const { return ((int)threadIdx.x - kFirstV) / 32; }
@@ -78,54 +81,58 @@ template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
 
     __device__ __forceinline__ Pages pages(const int32_t *table, int last, int t) const
     {
-        int k, v, at;
-        cache_tile(P.c, t + key_tile(), &k, &at);
-        cache_tile(P.c, t + value_tile(), &v, &at);
-        return {table[min(k, last)], table[min(v, last)]};
+        int k, v;
+        Pages g;
+        cache_tile(P.c, t + key_tile(), &k, &g.k_at);
+        cache_tile(P.c, t + value_tile(), &v, &g.v_at);
+        g.k = table[min(k, last)];
+        g.v = table[min(v, last)];
+        return g;
     }
 
-    // Whether that page is one, and tokens [t, t + 16) among the sequence's; the page
-    // and their place there, or page 0
-    __device__ __forceinline__ bool there(int raw, int len, int t, int *page, int *at) const
+    // Whether that page is one, and tokens [t, t + 16) are of the sequence's: if
+    // not, page 0 and its first tokens stand for them
+    __device__ __forceinline__ bool there(int &page, int &at, int len, int t) const
     {
-        int index;
-        cache_tile(P.c, t, &index, at);
-        const bool ok = t < len && raw >= 0 && raw < P.c.pages;
-        *page = ok ? raw : 0;
-        *at = ok ? *at : 0;
+        const bool ok = t < len && (u32)page < (u32)P.c.pages;
+        page = ok ? page : 0;
+        at = ok ? at : 0;
         return ok;
     }
 
-    __device__ __forceinline__ void load(Raw<D, KU> &x, const Pages &g, int len, int t, int head) const
+    __device__ __forceinline__ void load(Raw<D, KU> &x, Pages g, int len, int t, int head) const
     {
         const int ps = P.c.page_size;
-        int page, at;
-        x.k_there = there(g.k, len, t + key_tile(), &page, &at);
+        x.k_there = there(g.k, g.k_at, len, t + key_tile());
+        x.v_there = there(g.v, g.v_at, len, t + value_tile());
         {
-            const uint8_t *base = P.cache + cache_page_at(P.c, page, head, D);
-            const int token = at + threadIdx.x % 16;
+            const uint8_t *base = P.cache + cache_page_near(P.c, g.k, head, D);
+            const u32 token = g.k_at + threadIdx.x % 16;
 #pragma unroll
             for (int i = 0; i < KU; ++i) {
-                const int unit = threadIdx.x + i * kThreads, part = unit / kTile;
+                const u32 unit = threadIdx.x + i * kThreads, part = unit / kTile;
                 if (kUnits % kThreads == 0 || unit < kUnits) {
-                    x.k[i] = *(const u32x4 *)(base + (u32)(token * (D / 2) + part * 16));
-                    x.ks[i] = base[cache_scales(ps, D, 0) + (u32)(part * ps + token)];
+                    x.k[i] = *(const u32x4 *)(base + (token * (D / 2) + part * 16));
+                    x.ks[i] = *(const u32_any *)(base + (cache_scales(ps, D, 0) + part * ps + token));
                 }
             }
         }
         if (kFirstV == 0 || (int)threadIdx.x >= kFirstV) {
-            x.v_there = there(g.v, len, t + value_tile(), &page, &at);
-            const uint8_t *base = P.cache + cache_page_at(P.c, page, head, D);
-            const int first = at + 4 * (value_group() & 1), c = threadIdx.x % 32;
-            const uint8_t *from = base + (u32)(cache_codes(ps, D, 1) + first * (D / 2) + c * (D / 64));
+            const uint8_t *base = P.cache + cache_page_near(P.c, g.v, head, D);
+            const u32 first = g.v_at + 4 * (value_group() & 1) + 8 * (threadIdx.x & 1), c = threadIdx.x / 2 % 16;
+            const u32 code = cache_codes(ps, D, 1) + first * (D / 2) + c * (D / 32);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint8_t *code = from + (i % 4 + i / 4 * 8) * (D / 2);
-                x.v[i] = D == 64 ? *code : D == 128 ? *(const uint16_t *)code : *(const u32 *)code;
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *from = base + code + i * (D / 2);
+                if constexpr (D <= 128) {
+                    x.v[i][0] = *(const u32_any *)from;
+                } else {
+                    const u32x2 w = *(const u32x2 *)from;
+                    x.v[i][0] = w[0];
+                    x.v[i][1] = w[1];
+                }
             }
-            const uint8_t *scales = base + (u32)(cache_scales(ps, D, 1) + c * (D / 32) / 32 * ps + first);
-            x.vs[0] = *(const u32 *)scales;
-            x.vs[1] = *(const u32 *)(scales + 8);
+            x.vs = *(const u32 *)(base + (cache_scales(ps, D, 1) + c * (D / 16) / 32 * ps + first));
         }
     }
 
@@ -137,7 +144,7 @@ template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
         for (int i = 0; i < KU; ++i) {
             const int unit = threadIdx.x + i * kThreads, part = unit / kTile, token = threadIdx.x % kTile;
             if (kUnits % kThreads == 0 || unit < kUnits) {
-                const float f = scale_of(x.ks[i]);
+                const float f = scale_of(x.ks[i] & 255);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     L.k[buf][part * 4 + j][token] =
@@ -149,26 +156,32 @@ template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
         }
         u32 odd = 0;
         if (kFirstV == 0 || (int)threadIdx.x >= kFirstV) {
-            const int group = value_group(), c = threadIdx.x % 32;
-            float f[8];
+            float f[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                u32 byte = x.vs[i / 4] >> (8 * (i % 4)) & 255;
+            for (int i = 0; i < 4; ++i) {
+                u32 byte = x.vs >> (8 * i) & 255;
                 if (edge || !x.v_there) {
-                    const bool valid =
-                        x.v_there && t + group / 2 * 16 + 4 * (group & 1) + i % 4 + i / 4 * 8 < len;
+                    const bool valid = x.v_there && t + value_tile() + 4 * (value_group() & 1) +
+                                                           8 * (int)(threadIdx.x & 1) + i < len;
                     odd |= (u32)(byte == 255 && valid);
-                    x.v[i] = valid ? x.v[i] : 0;
+#pragma unroll
+                    for (int j = 0; j < (D + 127) / 128; ++j)
+                        x.v[i][j] = valid ? x.v[i][j] : 0;
                     byte = byte == 255 || !valid ? 0 : byte;
                 }
                 f[i] = scale_of(byte);
             }
-            values<0>(x, f, buf, group, c);
-            if constexpr (D >= 128)
-                values<1 % (D / 64)>(x, f, buf, group, c);
+            values<0>(x, f, buf);
+            values<1>(x, f, buf);
+            if constexpr (D >= 128) {
+                values<2>(x, f, buf);
+                values<3>(x, f, buf);
+            }
             if constexpr (D >= 256) {
-                values<2 % (D / 64)>(x, f, buf, group, c);
-                values<3 % (D / 64)>(x, f, buf, group, c);
+                values<4>(x, f, buf);
+                values<5>(x, f, buf);
+                values<6>(x, f, buf);
+                values<7>(x, f, buf);
             }
         }
         if (edge) {
@@ -179,20 +192,17 @@ template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
     }
 
     template <int BYTE>
-    __device__ __forceinline__ void values(const Raw<D, KU> &x, const float f[8], int buf, int group, int c)
+    __device__ __forceinline__ void values(const Raw<D, KU> &x, const float f[4], int buf)
     {
-        u32 w[8];
+        const int group = value_group(), c = threadIdx.x / 2 % 16, half = threadIdx.x & 1;
+        u32 w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = H::template from_fp4<BYTE>(x.v[i], f[i]);
-        u32x4 a, b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x05040100);
-            b[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x07060302);
-        }
-        L.v[buf][group][(2 * BYTE) * 32 + c] = a;
-        L.v[buf][group][(2 * BYTE + 1) * 32 + c] = b;
+        for (int i = 0; i < 4; ++i)
+            w[i] = H::template from_fp4<BYTE % 4>(x.v[i][BYTE / 4], f[i]);
+        L.v[buf][group][(2 * BYTE) * 16 + c][half] = u32x2{__builtin_amdgcn_perm(w[1], w[0], 0x05040100),
+                                                           __builtin_amdgcn_perm(w[3], w[2], 0x05040100)};
+        L.v[buf][group][(2 * BYTE + 1) * 16 + c][half] = u32x2{__builtin_amdgcn_perm(w[1], w[0], 0x07060302),
+                                                               __builtin_amdgcn_perm(w[3], w[2], 0x07060302)};
     }
 
     // ------------------------------------------------------------ a tile's work
@@ -295,7 +305,7 @@ template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
         for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int d = 0; d < DC; ++d) {
-                const u32x4 a = L.v[buf][2 * c + h][d * 32 + q];
+                const u32x4 a = *(const u32x4 *)L.v[buf][2 * c + h][d * 32 + q];
 #pragma unroll
                 for (int i = 0; i < CT; ++i)
                     o[i][d] = H::mfma32(a, p[i][c], o[i][d]);
@@ -397,24 +407,31 @@ void prompt_kernel(const AttentionParams P)
             continue;
         const int64_t at = (first + i0 + over) * P.q_heads + head * P.group + (r - over * P.group);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        // register j of the result is channels (8 (j / 4) + 4 h + j % 4) D/32 + d, d the product's number
+        // register i of product d is row r = 8 (i / 4) + 4 h + i % 4 of it, channel
+        // r % 16 D/16 + 2 d + r / 16: D/16 channels side by side in two registers
+        // of all the products
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c0 = (8 * j + 4 * A.h) * A.DC;
-            u32 w[2 * A.DC];
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4 * A.DC; e += 2)
-                w[e / 2] = H::pack(A.o[i][e % A.DC][4 * j + e / A.DC] * inv,
-                                   A.o[i][(e + 1) % A.DC][4 * j + (e + 1) / A.DC] * inv);
-            const bool odd_group = nans >> (c0 / 32) & 1;
-            uint16_t *to = P.out + at * D + c0;
+            for (int e = 0; e < 4; ++e) {
+                const int c0 = (8 * j + 4 * A.h + e) * (D / 16);
+                u32 w[A.DC];
 #pragma unroll
-            for (int e = 0; e < 2 * A.DC; e += 4) {
-                const u32 nan = DT == MHC_BF16 ? 0x7fc07fc0u : 0x7e007e00u;
-                const u32x4 v = odd_group ? u32x4{nan, nan, nan, nan} : u32x4{w[e], w[e + 1], w[e + 2], w[e + 3]};
-                *(u32x4 *)(to + 2 * e) = v;
+                for (int d = 0; d < A.DC; ++d)
+                    w[d] = H::pack(A.o[i][d][4 * j + e] * inv, A.o[i][d][4 * j + 8 + e] * inv);
+                if (nans >> (c0 / 32) & 1)
+#pragma unroll
+                    for (int d = 0; d < A.DC; ++d)
+                        w[d] = DT == MHC_BF16 ? 0x7fc07fc0u : 0x7e007e00u;
+                uint16_t *to = P.out + at * D + c0;
+                if constexpr (A.DC == 2) {
+                    *(u32x2 *)to = u32x2{w[0], w[1]};
+                } else {
+#pragma unroll
+                    for (int d = 0; d < A.DC; d += 4)
+                        *(u32x4 *)(to + 2 * d) = u32x4{w[d], w[d + 1], w[d + 2], w[d + 3]};
+                }
             }
-        }
         if (P.lse && A.h == 0)
             P.lse[at] = sum == 0.0f ? -__builtin_inff()
                                     : (A.top[i] + __builtin_amdgcn_logf(sum) - Softmax<DT>::kShift) * kLn2;
