@@ -135,14 +135,6 @@ __device__ u32 nan_groups(const AttentionParams &P, Whole table, int32_t t, int 
 // that share lines go through them (with all loads past them: 5.0).
 struct Page {
     __amdgpu_buffer_rsrc_t r;
-    __device__ __forceinline__ u32 load8(u32 lane, int wave) const
-    {
-        return __builtin_amdgcn_raw_buffer_load_b8(r, lane, wave, 0);
-    }
-    __device__ __forceinline__ u32 load16(u32 lane, int wave) const
-    {
-        return __builtin_amdgcn_raw_buffer_load_b16(r, lane, wave, 0);
-    }
     __device__ __forceinline__ u32 load32(u32 lane, int wave) const
     {
         return __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0);
@@ -154,6 +146,11 @@ struct Page {
     __device__ __forceinline__ u32x4 load128(u32 lane, int wave) const
     {
         return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, wave, 2));
+    }
+    // the same through the caches, for what other workgroups read too
+    __device__ __forceinline__ u32x4 load128_again(u32 lane, int wave) const
+    {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, wave, 0));
     }
 };
 

@@ -15,7 +15,7 @@
 // The values' pairs of channels become pairs of tokens by two byte permutes.
 #include <hip/hip_runtime.h>
 
-#include "attention_common.h"
+#include "attention_join.h"
 
 namespace mhc {
 namespace {
@@ -27,7 +27,6 @@ constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kQuantum = kStep * kAttnWaves;   // tokens that a workgroup's waves take side by side
 constexpr int kMostBalanced = 1024;       // sequences whose lengths a worker adds up
 constexpr int kLeastQuanta = 4;           // of a worker's share
-constexpr int kJoinWaves = 4;
 
 // A sequence's share of the work: blocks of rows, and the quanta of tokens that
 // some row of it sees, the same number for every block and kv head.
@@ -131,32 +130,9 @@ __device__ Share share(const AttentionParams &P, int worker)
     }
 }
 
-// A partial result: kRows maxima, kRows sums, [kRows][D] weighted values.  A
-// worker's share leaves at most two: of its first and of its last block.
-template <int D> __device__ __forceinline__ float *record(const AttentionParams &P, int64_t worker, bool first)
-{
-    return P.workspace + (2 * worker + (first ? 0 : 1)) * (int64_t)(kRows * (D + 2));
-}
-
-// What is to be joined of a block: its parts are those of workers `from` on.
-// parts is 0 where one worker has all of it.
-struct alignas(8) Join {
-    int from;
-    int parts;          // below 2^13; its top bit: the first part is all of its worker's share
-};
-
-constexpr int kWholeShare = 1 << 30;
-
-// Of the block with that number and that kv head
-template <int D>
-__device__ __forceinline__ Join *join_of(const AttentionParams &P, int64_t number, int head)
-{
-    return (Join *)(P.workspace + 2 * (int64_t)P.workers * (kRows * (D + 2))) + number * P.c.heads + head;
-}
-
 // 32 tokens of a kv head as a lane holds them
 template <int D> struct Tile {
-    u32 k[2][D / 32];                    // token c of each half, its quarter g of the channels
+    u32 k[2][D / 32];                    // token c of each half, its channels' piece g and, D = 256, g + 4
     u32 ks[2][(D + 127) / 128];
     u32 v[8][(D + 127) / 128];           // tokens 4g .. 4g + 3 of each half, chunk c of the channels
     u32 vs[2];
@@ -187,9 +163,9 @@ template <int DT, int D, bool CAP> struct Attention {
     __device__ Attention(const AttentionParams &p) : P(p), c(threadIdx.x & 15), g(threadIdx.x >> 4 & 3)
     {
         const int ps = P.c.page_size;
-        at_k = c * (D / 2) + g * (D / 8);
+        at_k = c * (D / 2) + g * (D == 64 ? 8 : 16);
         at_v = cache_codes(ps, D, 1) + 4 * g * (D / 2) + c * VB;
-        at_ks = cache_scales(ps, D, 0) + g * D / 128 * ps + c;
+        at_ks = cache_scales(ps, D, 0) + (D == 64 ? g / 2 : g) * ps + c;
         at_vs = cache_scales(ps, D, 1) + c * VC / 32 * ps + 4 * g;
     }
 
@@ -203,7 +179,7 @@ template <int DT, int D, bool CAP> struct Attention {
                 P.q + (s.first + i) * P.q_token + (int64_t)(head * P.group + (skip + c - over * P.group)) * P.q_head;
 #pragma unroll
             for (int j = 0; j < KC; ++j)
-                q[j] = *(const u32x4 *)(at + g * (D / 4) + j * 8);
+                q[j] = *(const u32x4 *)(at + (D == 64 ? 16 * g + 8 * j : 32 * (g + 4 * (j / 4)) + 8 * (j % 4)));
         } else {
 #pragma unroll
             for (int j = 0; j < KC; ++j)
@@ -239,7 +215,7 @@ template <int DT, int D, bool CAP> struct Attention {
             } else {
 #pragma unroll
                 for (int j = 0; j < KC / 4; ++j) {
-                    const u32x4 w = from.load128(at_k + 16 * j, codes);
+                    const u32x4 w = from.load128(at_k + 64 * j, codes);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         x.k[h][4 * j + i] = w[i];
@@ -247,12 +223,12 @@ template <int DT, int D, bool CAP> struct Attention {
             }
 #pragma unroll
             for (int j = 0; j < (D + 127) / 128; ++j)
-                x.ks[h][j] = from.load8(at_ks, at + j * P.c.page_size);
+                x.ks[h][j] = from.load32(at_ks, at + 4 * j * P.c.page_size);      // its low byte
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const u32 v = at_v + j * (D / 2);
                 if constexpr (D == 64) {
-                    x.v[4 * h + j][0] = from.load16(v, codes);
+                    x.v[4 * h + j][0] = from.load32(v, codes);      // its low half
                 } else if constexpr (D == 128) {
                     x.v[4 * h + j][0] = from.load32(v, codes);
                 } else {
@@ -301,7 +277,7 @@ template <int DT, int D, bool CAP> struct Attention {
             f32x4 s = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < KC; ++j) {
-                const float f = scale_of(x.ks[h][D == 256 ? j / 4 : 0]);
+                const float f = scale_of(x.ks[h][D == 256 ? j / 4 : 0] & 255);
                 const u32 w = x.k[h][j];
                 const u32x4 a = {H::template from_fp4<0>(w, f), H::template from_fp4<1>(w, f),
                                  H::template from_fp4<2>(w, f), H::template from_fp4<3>(w, f)};
@@ -411,21 +387,6 @@ template <int D> struct Shared {
     float o[kAttnWaves][kRows][D + 4];
 };
 
-// Four channels of a finished row: head `skip` behind those of query row i
-template <int DT, int D>
-__device__ __forceinline__ void store(const AttentionParams &P, int64_t i, int skip, int head, int d, float4 o,
-                                      float top, float sum)
-{
-    typedef Half<DT> H;
-    const int over = skip / P.group;
-    const int64_t at = (i + over) * P.q_heads + head * P.group + (skip - over * P.group);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const u32x2 w = {H::pack(o.x * inv, o.y * inv), H::pack(o.z * inv, o.w * inv)};
-    *(u32x2 *)(P.out + at * D + d) = w;
-    if (P.lse && d == 0)
-        P.lse[at] = sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum) - Softmax<DT>::kShift) * kLn2;
-}
-
 // BALANCED: the workers share all quanta evenly, and a block that several have
 // parts of is put together by attention_join_kernel.  Otherwise a workgroup a block.
 template <int DT, int D, bool CAP, bool BALANCED>
@@ -507,7 +468,7 @@ __global__ __launch_bounds__(kAttnThreads)
         __syncthreads();
         const bool whole = from == 0 && to == s.quanta;
         const int count = (int)min(s.rows - row, (int64_t)kRows);
-        float *rec = record<D>(P, id, at == begin);
+        float *rec = record<D, kRows>(P, id, at == begin);
         for (int e = threadIdx.x; e < count * (D / 4); e += kAttnThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float most = kLowest, all = 0.0f;
@@ -536,7 +497,7 @@ __global__ __launch_bounds__(kAttnThreads)
         }
         if constexpr (BALANCED)
             if (from == 0 && threadIdx.x == 0) {
-                Join *j = join_of<D>(P, first_number(P, b, s.first, kRows) + block, head);
+                Join *j = join_of<D, kRows>(P, first_number(P, b, s.first, kRows) + block, head);
                 j->from = (int)id;
                 j->parts = whole ? 0
                                  : (share_of(h.total, h.workers, at + s.quanta - 1) - (int)id + 1) |
@@ -544,94 +505,6 @@ __global__ __launch_bounds__(kAttnThreads)
             }
         __syncthreads();
         at += to - from;
-    }
-}
-
-// Puts together the blocks that several workers have parts of.  WAVES waves a
-// row, D/4 lanes a part, eight parts a lane at once.
-template <int DT, int D, int WAVES>
-__global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(const AttentionParams P)
-{
-    constexpr int ROWS = kJoinWaves / WAVES, LANES = D / 4, AT_ONCE = 64 / LANES * WAVES, BATCH = WAVES > 1 ? 8 : 2;
-    __shared__ float4 L[kJoinWaves][LANES];
-    __shared__ float2 M[kJoinWaves];
-    const int64_t id = block_id(), segment = id / (kRows / ROWS), number = segment / P.c.heads;
-    if (number >= P.blocks)
-        return;
-    const int head = (int)(segment - number * P.c.heads);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int row = (int)(id % (kRows / ROWS)) * ROWS + wave / WAVES;
-    const Join j = *join_of<D>(P, number, head);
-    int64_t first;
-    const int b = sequence_of(P, number, kRows, &first);
-    const Sequence s = sequence(P, b);
-    // every block's Join has been written, those of numbers that no block has not
-    if (number < first || number - first >= s.blocks)
-        return;
-    const int parts = j.parts & ~kWholeShare;
-    const int64_t at = (number - first) * kRows;
-    if (parts == 0 || (WAVES > 1 && at + row >= s.rows))      // the workgroup's all
-        return;
-    const int d = lane % LANES * 4;
-    float most = kLowest, all = 0.0f;
-    float4 o = {0, 0, 0, 0};
-    if (at + row < s.rows)
-        for (int i0 = wave % WAVES * (64 / LANES) + lane / LANES; i0 < parts; i0 += AT_ONCE * BATCH) {
-            float top[BATCH], sum[BATCH];
-            float4 x[BATCH];
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                // past the last: the last once more, with a weight of 0
-                const int i = min(i0 + k * AT_ONCE, parts - 1);
-                const float *rec = record<D>(P, j.from + i, i > 0 || (j.parts & kWholeShare));
-                top[k] = rec[row];
-                sum[k] = rec[kRows + row];
-                x[k] = *(const float4 *)(rec + 2 * kRows + row * D + d);
-            }
-            float now = most;
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k)
-                now = fmaxf(now, top[k]);
-            const float old = __builtin_amdgcn_exp2f(most - now);
-            most = now;
-            all *= old;
-            o = {o.x * old, o.y * old, o.z * old, o.w * old};
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                if (i0 + k * AT_ONCE >= parts)
-                    continue;
-                const float w = __builtin_amdgcn_exp2f(top[k] - now);
-                all += sum[k] * w;
-                o = {o.x + x[k].x * w, o.y + x[k].y * w, o.z + x[k].z * w, o.w + x[k].w * w};
-            }
-        }
-    auto add = [&](float top, float sum, const float4 &x) {
-        const float now = fmaxf(most, top);
-        const float a = __builtin_amdgcn_exp2f(most - now), c = __builtin_amdgcn_exp2f(top - now);
-        most = now;
-        all = all * a + sum * c;
-        o = {o.x * a + x.x * c, o.y * a + x.y * c, o.z * a + x.z * c, o.w * a + x.w * c};
-    };
-#pragma unroll
-    for (int x = LANES; x < 64; x <<= 1) {
-        const float top = __shfl_xor(most, x), sum = __shfl_xor(all, x);
-        const float4 v = {__shfl_xor(o.x, x), __shfl_xor(o.y, x), __shfl_xor(o.z, x), __shfl_xor(o.w, x)};
-        add(top, sum, v);
-    }
-    if constexpr (WAVES > 1) {
-        if (lane < LANES)
-            L[wave][lane] = o;
-        if (lane == 0)
-            M[wave] = {most, all};
-        __syncthreads();
-        if (wave > 0)
-            return;
-        for (int w = 1; w < WAVES; ++w)
-            add(M[w].x, M[w].y, L[w][lane % LANES]);
-    }
-    if (lane < LANES && at + row < s.rows) {
-        const int64_t i = at / P.group;
-        store<DT, D>(P, s.first + i, (int)(at - i * P.group) + row, head, d, o, most, all);
     }
 }
 
@@ -649,15 +522,10 @@ template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &
 
 template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
 {
-    const int64_t segments = p.blocks * p.c.heads;
     const hipError_t e = p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
     if (e != hipSuccess || !p.workspace)
         return e;
-    if (segments * 4 <= p.workers)      // few blocks have many parts each
-        attention_join_kernel<DT, D, kJoinWaves><<<grid_of(segments * kRows), 64 * kJoinWaves, 0, s>>>(p);
-    else
-        attention_join_kernel<DT, D, 1><<<grid_of(segments * (kRows / kJoinWaves)), 64 * kJoinWaves, 0, s>>>(p);
-    return hipGetLastError();
+    return launch_join<DT, D, kRows>(p, s);
 }
 
 template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipStream_t s)
@@ -686,16 +554,18 @@ bool countable(const AttentionParams &p)
 
 uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus)
 {
-    if (prompts(T, B, q_heads / kv_heads) || !balanced(T, B, q_heads, kv_heads, cus))
+    if (prompts(T, B, q_heads / kv_heads))
+        return prompt_workspace_floats(T, B, q_heads, kv_heads, head_dim, cus);
+    if (!balanced(T, B, q_heads, kv_heads, cus))
         return 0;
-    return (uint64_t)workers_of(cus, head_dim) * 2 * kRows * (head_dim + 2) +
-           (uint64_t)most_blocks(T, B, q_heads / kv_heads, kRows, true) * kv_heads * sizeof(Join) / 4;
+    return join_floats(workers_of(cus, head_dim), most_blocks(T, B, q_heads / kv_heads, kRows, true) * kv_heads,
+                       kRows, head_dim);
 }
 
 hipError_t launch_attention(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
 {
     if (prompts(a.T, a.B, a.group))
-        return launch_prompt(a, head_dim, dtype, s);
+        return launch_prompt(a, head_dim, dtype, cus, s);
     AttentionParams p = a;
     p.blocks = most_blocks(p.T, p.B, p.group, kRows, p.q_starts != nullptr);
     p.workers = workers_of(cus, head_dim);

@@ -11,190 +11,193 @@
 //   O^T += V^T P^T  P is the operand as it stands: k = 16 tokens, of which lane h
 //                   has 4 h + r and 8 + 4 h + r.  V lies in LDS in those groups
 //                   of eight tokens, for one channel after another.
-#include "attention_common.h"
+#include "attention_join.h"
 
 namespace mhc {
 namespace {
 
 constexpr int kTile = 64;                // tokens
+constexpr int kPromptWaves = 4, kPromptRows = 32 * kPromptWaves;
 constexpr int kGroups = kTile / 8;       // of tokens, as a product's lane has them
+constexpr int kLeastTiles = 4;           // of a worker's share, where a block has as many
 
 template <int D> struct PromptShared {
     u32x4 k[2][D / 8][kTile];            // eight channels of a token
     u32x2 v[2][kGroups][D][2];           // eight tokens of a channel; channel c D/16 + m at m 16 + c
-    u32 nan[2][8];                       // whether a wave met a NaN among a tile's values
+    u32 nan[2][4];                       // whether a wave met a NaN among a tile's values
     u32 there[2][4];                     // whether a tile's 16 tokens have a page
 };
 
-// A thread's part of a tile on its way: units of 32 channels of a token's keys,
-// and four tokens' values, D/16 channels.  Short loads are of four bytes that
-// begin with theirs, for the compiler to have nothing to cut off behind them.
-template <int D, int KU> struct Raw {
-    u32x4 k[KU];
-    u32 ks[KU];
-    u32 v[4][(D + 127) / 128];
-    u32 vs;
-    bool k_there, v_there;
+template <int N> struct Number {
+    static constexpr int value = N;
 };
 
-typedef u32 u32_any __attribute__((aligned(1)));
+// f(Number<0>) .. f(Number<N - 1>)
+template <int N, int I = 0, typename F> __device__ __forceinline__ void static_for(F f)
+{
+    if constexpr (I < N) {
+        f(Number<I>{});
+        static_for<N, I + 1>(f);
+    }
+}
 
-template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
+// 16 tokens' keys on their way: a lane has units of 32 channels of a token
+template <int D> struct RawKeys {
+    u32x4 k[(D + 127) / 128];
+    u32 scale[(D + 127) / 128];          // in the low byte
+    bool there;
+};
+
+// 16 tokens' values: a lane has D/16 channels of four tokens
+template <int D> struct RawValues {
+    u32 v[4][(D + 127) / 128];           // D = 64: in the low half
+    u32 scale;
+    bool there;
+};
+
+template <int DT, int D, bool CAP> struct Prompt {
     typedef Half<DT> H;
     typedef Softmax<DT> S;
-    static constexpr int kThreads = 64 * WAVES, kRows = 32 * CT * WAVES;
-    static constexpr int KC = D / 16, DC = D / 32;
-    static constexpr int kUnits = kTile * (D / 32);                 // of keys
-    static constexpr int KU = (kUnits + kThreads - 1) / kThreads;
-    static constexpr int kFirstV = kThreads - 256;                  // threads from here on take values
+    static constexpr int KC = D / 16, DC = D / 32, KU = (D + 127) / 128;
 
     const AttentionParams &P;
     PromptShared<D> &L;
     const int lane, wave, q, h;
-    f32x16 o[CT][DC];
-    u32x4 qr[CT][KC];
-    float top[CT], sum[CT];
+    u32 at_k, at_ks, at_v, at_vs;        // the lane's bytes in the wave's 16 tokens
+    f32x16 o[DC], s[2];
+    u32x4 qr[KC], p[4];
+    float top, sum;
     float factor;                        // of the products, to scores in base 2; not negative
-    u32 nans[CT];
-    int lo[CT], hi[CT];
+    u32 nans;                            // groups of channels that a NaN reaches in the lane's row
+    int lo, hi;                          // tokens that the lane's row sees
 
-    __device__ Prompt(const AttentionParams &p, PromptShared<D> &l)
-        : P(p), L(l), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), q(lane & 31),
+    __device__ Prompt(const AttentionParams &p_, PromptShared<D> &l)
+        : P(p_), L(l), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), q(lane & 31),
           h(lane >> 5)
     {
+        const int ps = P.c.page_size;
+        at_k = lane % 16 * (D / 2) + lane / 16 * 16;
+        at_ks = cache_scales(ps, D, 0) + lane / 16 * ps + lane % 16;
+        at_v = cache_codes(ps, D, 1) + value_token() * (D / 2) + value_chunk() * (D / 32);
+        at_vs = cache_scales(ps, D, 1) + value_chunk() * (D / 16) / 32 * ps + value_token();
+        if (D == 64 && lane >= 32)       // there are no third and fourth units: the first's once more
+            at_k -= 32, at_ks -= 2 * ps;
     }
 
     // ------------------------------------------------------- a tile's way in
+    //
+    // Wave w brings tokens 16 w .. 16 w + 15 of each tile: one page.
 
-    // Pages of the thread's tokens of a tile, as the table has them: of its keys'
-    // and of its values'.  Nothing is done with them before they are used, a tile
-    // later.
-    struct Pages {
-        int k, k_at, v, v_at;
-    };
+    // The lane's values: four tokens from this one on, of the wave's 16; a lane's
+    // eight tokens of a product are two lanes' halves
+    __device__ __forceinline__ int value_token() const { return 4 * (lane >> 5) + 8 * (lane & 1); }
+    __device__ __forceinline__ int value_chunk() const { return lane / 2 % 16; }
 
-    __device__ __forceinline__ int value_group() const { return ((int)threadIdx.x - kFirstV) / 32; }
-    // First of the 16 tokens that the thread's are of, in the tile.  Units u, u +
-    // kThreads, .. of keys have one token: 64 divides kThreads.
-    __device__ __forceinline__ int key_tile() const { return (int)(threadIdx.x % kTile) / 16 * 16; }
-    __device__ __forceinline__ int value_tile() const { return max(value_group(), 0) / 2 * 16; }
-
-    __device__ __forceinline__ Pages pages(const int32_t *table, int last, int t) const
+    // Page and place there of the wave's 16 tokens of the tile at t; page 0 for none
+    __device__ __forceinline__ bool place(Whole table, int len, int t, int *page, int *at) const
     {
-        int k, v;
-        Pages g;
-        cache_tile(P.c, t + key_tile(), &k, &g.k_at);
-        cache_tile(P.c, t + value_tile(), &v, &g.v_at);
-        g.k = table[min(k, last)];
-        g.v = table[min(v, last)];
-        return g;
+        return cache_page(P.c, table, len, t + 16 * wave, page, at);
     }
 
-    // Whether that page is one, and tokens [t, t + 16) are of the sequence's: if
-    // not, page 0 and its first tokens stand for them
-    __device__ __forceinline__ bool there(int &page, int &at, int len, int t) const
+    __device__ __forceinline__ void load(RawKeys<D> &x, Whole table, int len, int t, int head) const
     {
-        const bool ok = t < len && (u32)page < (u32)P.c.pages;
-        page = ok ? page : 0;
-        at = ok ? at : 0;
-        return ok;
-    }
-
-    __device__ __forceinline__ void load(Raw<D, KU> &x, Pages g, int len, int t, int head) const
-    {
-        const int ps = P.c.page_size;
-        x.k_there = there(g.k, g.k_at, len, t + key_tile());
-        x.v_there = there(g.v, g.v_at, len, t + value_tile());
-        {
-            const uint8_t *base = P.cache + cache_page_near(P.c, g.k, head, D);
-            const u32 token = g.k_at + threadIdx.x % 16;
-#pragma unroll
-            for (int i = 0; i < KU; ++i) {
-                const u32 unit = threadIdx.x + i * kThreads, part = unit / kTile;
-                if (kUnits % kThreads == 0 || unit < kUnits) {
-                    x.k[i] = *(const u32x4 *)(base + (token * (D / 2) + part * 16));
-                    x.ks[i] = *(const u32_any *)(base + (cache_scales(ps, D, 0) + part * ps + token));
-                }
-            }
-        }
-        if (kFirstV == 0 || (int)threadIdx.x >= kFirstV) {
-            const uint8_t *base = P.cache + cache_page_near(P.c, g.v, head, D);
-            const u32 first = g.v_at + 4 * (value_group() & 1) + 8 * (threadIdx.x & 1), c = threadIdx.x / 2 % 16;
-            const u32 code = cache_codes(ps, D, 1) + first * (D / 2) + c * (D / 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t *from = base + code + i * (D / 2);
-                if constexpr (D <= 128) {
-                    x.v[i][0] = *(const u32_any *)from;
-                } else {
-                    const u32x2 w = *(const u32x2 *)from;
-                    x.v[i][0] = w[0];
-                    x.v[i][1] = w[1];
-                }
-            }
-            x.vs = *(const u32 *)(base + (cache_scales(ps, D, 1) + c * (D / 16) / 32 * ps + first));
-        }
-    }
-
-    // EDGE: some row sees only some of the tile's tokens.  A NaN among its values
-    // is then left out, and noted.
-    __device__ __forceinline__ void put(Raw<D, KU> &x, int buf, int len, int t, bool edge)
-    {
+        int page, at;
+        x.there = place(table, len, t, &page, &at);
+        const Page from = page_of<D>(P, page, head);
 #pragma unroll
         for (int i = 0; i < KU; ++i) {
-            const int unit = threadIdx.x + i * kThreads, part = unit / kTile, token = threadIdx.x % kTile;
-            if (kUnits % kThreads == 0 || unit < kUnits) {
-                const float f = scale_of(x.ks[i] & 255);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    L.k[buf][part * 4 + j][token] =
-                        u32x4{H::template from_fp4<0>(x.k[i][j], f), H::template from_fp4<1>(x.k[i][j], f),
-                              H::template from_fp4<2>(x.k[i][j], f), H::template from_fp4<3>(x.k[i][j], f)};
-                if (unit % 16 == 0 && unit < kTile)
-                    L.there[buf][unit / 16] = x.k_there;
-            }
-        }
-        u32 odd = 0;
-        if (kFirstV == 0 || (int)threadIdx.x >= kFirstV) {
-            float f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u32 byte = x.vs >> (8 * i) & 255;
-                if (edge || !x.v_there) {
-                    const bool valid = x.v_there && t + value_tile() + 4 * (value_group() & 1) +
-                                                           8 * (int)(threadIdx.x & 1) + i < len;
-                    odd |= (u32)(byte == 255 && valid);
-#pragma unroll
-                    for (int j = 0; j < (D + 127) / 128; ++j)
-                        x.v[i][j] = valid ? x.v[i][j] : 0;
-                    byte = byte == 255 || !valid ? 0 : byte;
-                }
-                f[i] = scale_of(byte);
-            }
-            values<0>(x, f, buf);
-            values<1>(x, f, buf);
-            if constexpr (D >= 128) {
-                values<2>(x, f, buf);
-                values<3>(x, f, buf);
-            }
-            if constexpr (D >= 256) {
-                values<4>(x, f, buf);
-                values<5>(x, f, buf);
-                values<6>(x, f, buf);
-                values<7>(x, f, buf);
-            }
-        }
-        if (edge) {
-            const u32 any = __any(odd != 0);
-            if (lane == 0)
-                L.nan[buf][wave] = any;
+            x.k[i] = from.load128_again(at_k + 64 * i, at * (D / 2));
+            x.scale[i] = from.load32(at_ks + 4 * i * P.c.page_size, at);
         }
     }
 
-    template <int BYTE>
-    __device__ __forceinline__ void values(const Raw<D, KU> &x, const float f[4], int buf)
+    __device__ __forceinline__ void load(RawValues<D> &x, Whole table, int len, int t, int head) const
     {
-        const int group = value_group(), c = threadIdx.x / 2 % 16, half = threadIdx.x & 1;
+        int page, at;
+        x.there = place(table, len, t, &page, &at);
+        const Page from = page_of<D>(P, page, head);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (D <= 128) {
+                x.v[i][0] = from.load32(at_v + i * (D / 2), at * (D / 2));
+            } else {
+                const u32x2 w = from.load64(at_v + i * (D / 2), at * (D / 2));
+                x.v[i][0] = w[0];
+                x.v[i][1] = w[1];
+            }
+        }
+        x.scale = from.load32(at_vs, at);
+    }
+
+    // Channels 8 j .. 8 j + 7 of the lane's unit i
+    __device__ __forceinline__ void put_key(int i, int j, const RawKeys<D> &x, const float f[KU], int buf)
+    {
+        // D = 64: lanes l and l + 32 have the same and write it to the same place
+        L.k[buf][(lane / 16 % (D < 128 ? 2 : 4) + 4 * i) * 4 + j][16 * wave + lane % 16] =
+            u32x4{H::template from_fp4<0>(x.k[i][j], f[i]), H::template from_fp4<1>(x.k[i][j], f[i]),
+                  H::template from_fp4<2>(x.k[i][j], f[i]), H::template from_fp4<3>(x.k[i][j], f[i])};
+    }
+
+    __device__ __forceinline__ void put(const RawKeys<D> &x, int buf)
+    {
+        float f[KU];
+#pragma unroll
+        for (int i = 0; i < KU; ++i)
+            f[i] = scale_of(x.scale[i] & 255);
+#pragma unroll
+        for (int i = 0; i < KU; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                put_key(i, j, x, f, buf);
+        if (lane == 0)
+            L.there[buf][wave] = x.there;
+    }
+
+    // Where some row sees only some of the tile's tokens (edge) a NaN among its
+    // values is left out and noted; tokens that are not there are 0
+    __device__ __forceinline__ void clean(RawValues<D> &x, int buf, int len, int t, bool edge)
+    {
+        u32 odd = 0;
+        if (edge || !x.there) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool valid = x.there && t + 16 * wave + value_token() + i < len;
+                const u32 byte = x.scale >> (8 * i) & 255;
+                odd |= (u32)(byte == 255 && valid);
+#pragma unroll
+                for (int j = 0; j < KU; ++j)
+                    x.v[i][j] = valid ? x.v[i][j] : 0;
+                if (byte == 255 || !valid)
+                    x.scale &= ~(255u << (8 * i));
+            }
+            if (edge)
+                L.nan[buf][wave] = __any(odd != 0);
+        }
+    }
+
+    __device__ __forceinline__ void put(const RawValues<D> &x, int buf)
+    {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = scale_of(x.scale >> (8 * i) & 255);
+        values<0>(x, f, buf);
+        values<1>(x, f, buf);
+        if constexpr (D >= 128) {
+            values<2>(x, f, buf);
+            values<3>(x, f, buf);
+        }
+        if constexpr (D >= 256) {
+            values<4>(x, f, buf);
+            values<5>(x, f, buf);
+            values<6>(x, f, buf);
+            values<7>(x, f, buf);
+        }
+    }
+
+    template <int BYTE> __device__ __forceinline__ void values(const RawValues<D> &x, const float f[4], int buf)
+    {
+        const int group = 2 * wave + (lane >> 5), c = value_chunk(), half = lane & 1;
         u32 w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -207,249 +210,416 @@ template <int DT, int D, int WAVES, int CT, bool CAP> struct Prompt {
 
     // ------------------------------------------------------------ a tile's work
 
-    // Whether the tile's 16 tokens have their pages, a bit each
-    __device__ __forceinline__ u32 pages_there(int buf) const
+    __device__ __forceinline__ void products(f32x16 to[2], int buf) const
     {
+        to[0] = to[1] = f32x16{0};
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                to[i] = H::mfma32(L.k[buf][2 * k + h][32 * i + q], qr[k], to[i]);
+    }
+
+    // Token of the tile at t that register j of the scores is, 0 .. 31
+    __device__ __forceinline__ int token(int t, int j) const
+    {
+        return t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4;
+    }
+
+    // The products of the tile at t as scores to the factor, hidden where the
+    // lane's row does not see them, and the maximum brought up to them
+    __device__ __forceinline__ void settle(int buf, int t, bool edge)
+    {
+        if constexpr (CAP) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = s[j / 16][j % 16];
+            cap<32>(P, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                s[j / 16][j % 16] = v[j];
+        }
         u32 there = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             there |= L.there[buf][j] << j;
-        return __builtin_amdgcn_readfirstlane(there);
+        there = __builtin_amdgcn_readfirstlane(there);
+        if (edge || there != 15) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const bool sees = token(t, j) >= lo && token(t, j) < hi && (there >> (j / 8) & 1);
+                s[j / 16][j % 16] = sees ? s[j / 16][j % 16] : -__builtin_inff();
+            }
+        }
+        float most = s[0][0];
+#pragma unroll
+        for (int j = 1; j < 32; ++j)
+            most = fmaxf(most, s[j / 16][j % 16]);
+        most *= factor;
+        if (__any(most > top + S::kSlack)) {
+            const u32 x = __float_as_uint(most);
+            auto both = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+            const float now = fmaxf(top, fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])));
+            const float a = __builtin_amdgcn_exp2f(top - now);
+            top = now;
+            sum *= a;
+#pragma unroll
+            for (int d = 0; d < DC; ++d)
+                o[d] *= a;
+        }
     }
 
-    // Hides what the lane's row does not see of the tile: edge, by the rows'
-    // bounds; there, for its page
-    __device__ __forceinline__ void mask(float v[32], int i, int buf, int t, Whole table, int head, bool edge,
-                                         u32 there)
+    __device__ __forceinline__ void weigh()
     {
-        u32 seen = 0;
+        const float zero = S::kShift - top;
+        float part[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const int token = t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4;
-            const bool sees = token >= lo[i] && token < hi[i] && (there >> (j / 8) & 1);
-            seen |= (u32)sees << j;
-            v[j] = sees ? v[j] : -__builtin_inff();
+        for (int c = 0; c < 4; ++c) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = __builtin_amdgcn_exp2f(fmaf(s[c / 2][c % 2 * 8 + j], factor, zero));
+                part[j % 4] += v[j];
+            }
+            p[c] = u32x4{H::pack(v[0], v[1]), H::pack(v[2], v[3]), H::pack(v[4], v[5]), H::pack(v[6], v[7])};
         }
-        if (!edge)
-            return;
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+    }
+
+    __device__ __forceinline__ void add(int buf)
+    {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int d = 0; d < DC; ++d)
+                o[d] = H::mfma32(*(const u32x4 *)L.v[buf][2 * c + h][d * 32 + q], p[c], o[d]);
+    }
+
+    // One of the next tile's products with a part of this one's weights beside
+    // it, product after product: the compiler by itself puts the products first
+    __device__ __forceinline__ void products_and_weights(f32x16 next[2], int buf)
+    {
+        constexpr int N = 2 * KC, EACH = 32 / N, AHEAD = 4;
+        const float zero = S::kShift - top;
+        float part[2] = {0, 0}, v[8];
+        u32x4 a[AHEAD];
+        auto read = [&](int n) { return L.k[buf][2 * (n / 2) + h][32 * (n % 2) + q]; };
+        next[0] = next[1] = f32x16{0};
+#pragma unroll
+        for (int n = 0; n < AHEAD - 1; ++n)
+            a[n] = read(n);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if (n + AHEAD - 1 < N)
+                a[(n + AHEAD - 1) % AHEAD] = read(n + AHEAD - 1);
+            next[n % 2] = H::mfma32(a[n % AHEAD], qr[n / 2], next[n % 2]);
+#pragma unroll
+            for (int j = n * EACH; j < (n + 1) * EACH; ++j) {
+                v[j % 8] = __builtin_amdgcn_exp2f(fmaf(s[j / 16][j % 16], factor, zero));
+                part[j % 2] += v[j % 8];
+                if (j % 2) {
+                    u32 w = H::pack(v[j % 8 - 1], v[j % 8]);
+                    asm volatile("" : "+v"(w), "+v"(part[0]), "+v"(part[1]));    // here, and not behind all products
+                    p[j / 8][j % 8 / 2] = w;
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        sum += part[0] + part[1];
+    }
+
+    // Likewise this tile's values with what comes in
+    __device__ __forceinline__ void values_and_puts(int buf, const RawValues<D> &vals, const RawKeys<D> &keys)
+    {
+        constexpr int N = 4 * DC, CHUNKS = D / 32 + 4 * KU, AHEAD = 4;
+        u32x4 a[AHEAD];
+        auto read = [&](int n) { return *(const u32x4 *)L.v[buf][2 * (n / DC) + h][n % DC * 32 + q]; };
+        float f[4], fk[KU];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = scale_of(vals.scale >> (8 * i) & 255);
+#pragma unroll
+        for (int i = 0; i < KU; ++i)
+            fk[i] = scale_of(keys.scale[i] & 255);
+#pragma unroll
+        for (int n = 0; n < AHEAD - 1; ++n)
+            a[n] = read(n);
+        if (lane == 0)
+            L.there[buf][wave] = keys.there;
+        static_for<N>([&](auto n_) {
+            constexpr int n = n_.value;
+            if constexpr (n + AHEAD - 1 < N)
+                a[(n + AHEAD - 1) % AHEAD] = read(n + AHEAD - 1);
+            o[n % DC] = H::mfma32(a[n % AHEAD], p[n / DC], o[n % DC]);
+            if constexpr (n * CHUNKS / N != (n + 1) * CHUNKS / N) {
+                constexpr int c = n * CHUNKS / N;
+                if constexpr (c < D / 32)
+                    values<c>(vals, f, buf ^ 1);
+                else
+                    put_key((c - D / 32) / 4, (c - D / 32) % 4, keys, fk, buf);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    }
+
+    // NaN that were left out of the tile's values, for the rows that see them
+    __device__ __forceinline__ void note(int buf, Whole table, int t, int head)
+    {
         u32 odd = 0;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w)
+        for (int w = 0; w < 4; ++w)
             odd |= L.nan[buf][w];
         if (__builtin_amdgcn_readfirstlane(odd))
 #pragma unroll 1
             for (int j = 0; j < 32; ++j)
-                if (seen >> j & 1)
-                    nans[i] |=
-                        nan_groups<D>(P, table, t + 32 * (j / 16) + 8 * (j % 16 / 4) + 4 * h + j % 4, head);
-    }
-
-    __device__ __forceinline__ void work(int buf, int t, Whole table, int head, bool edge)
-    {
-        const u32 there = pages_there(buf);
-        f32x16 s[CT][2];
-#pragma unroll
-        for (int i = 0; i < CT; ++i)
-            s[i][0] = s[i][1] = f32x16{0};
-#pragma unroll
-        for (int k = 0; k < KC; ++k)
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                const u32x4 a = L.k[buf][2 * k + h][32 * tt + q];
-#pragma unroll
-                for (int i = 0; i < CT; ++i)
-                    s[i][tt] = H::mfma32(a, qr[i][k], s[i][tt]);
-            }
-        u32x4 p[CT][4];
-#pragma unroll
-        for (int i = 0; i < CT; ++i) {
-            float v[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v[j] = s[i][j / 16][j % 16];
-            if constexpr (CAP)
-                cap<32>(P, v);
-            if (edge || there != 15)
-                mask(v, i, buf, t, table, head, edge, there);
-            float most = v[0];
-#pragma unroll
-            for (int j = 1; j < 32; ++j)
-                most = fmaxf(most, v[j]);
-            most *= factor;
-            if (__any(most > top[i] + S::kSlack)) {
-                const u32 x = __float_as_uint(most);
-                auto both = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-                const float now = fmaxf(top[i], fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])));
-                const float a = __builtin_amdgcn_exp2f(top[i] - now);
-                top[i] = now;
-                sum[i] *= a;
-#pragma unroll
-                for (int d = 0; d < DC; ++d)
-                    o[i][d] *= a;
-            }
-            const float zero = S::kShift - top[i];
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v[j] = __builtin_amdgcn_exp2f(fmaf(v[j], factor, zero));
-            float part[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                part[j % 4] += v[j];
-            sum[i] += (part[0] + part[1]) + (part[2] + part[3]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                p[i][c] = u32x4{H::pack(v[8 * c], v[8 * c + 1]), H::pack(v[8 * c + 2], v[8 * c + 3]),
-                                H::pack(v[8 * c + 4], v[8 * c + 5]), H::pack(v[8 * c + 6], v[8 * c + 7])};
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int d = 0; d < DC; ++d) {
-                const u32x4 a = *(const u32x4 *)L.v[buf][2 * c + h][d * 32 + q];
-#pragma unroll
-                for (int i = 0; i < CT; ++i)
-                    o[i][d] = H::mfma32(a, p[i][c], o[i][d]);
-            }
+                if (token(t, j) >= lo && token(t, j) < hi)
+                    nans |= nan_groups<D>(P, table, token(t, j), head);
     }
 };
 
-template <int DT, int D, int WAVES, int CT, bool CAP>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
+// A block of rows and the tokens it sees
+struct Block {
+    int64_t first;          // its sequence's first query row
+    int b, n, len;
+    int i0, skip;           // begins with head `skip` of the sequence's query row i0
+    int rows;               // 0: the number is no block's
+    int least_lo, most_lo, least_hi, most_hi;   // tokens that some row, and that every row sees
+    int begin, tiles;       // the first tile's first token; 1 tile at least
+};
+
+template <int ROWS> __device__ __forceinline__ Block block_of(const AttentionParams &P, int64_t number)
+{
+    Block k;
+    int64_t numbered;
+    k.rows = k.tiles = 0;
+    k.b = sequence_of(P, number, ROWS, &numbered);
+    k.first = row_start(P, k.b);
+    k.n = (int)max(row_start(P, k.b + 1) - k.first, (int64_t)0);
+    const int64_t row = (number - numbered) * ROWS, rows = (int64_t)k.n * P.group;
+    if (number < numbered || row >= rows)
+        return k;
+    k.rows = (int)min(rows - row, (int64_t)ROWS);
+    k.len = length_of(P, k.b);
+    k.i0 = (int)(row / P.group);
+    k.skip = (int)(row - (int64_t)k.i0 * P.group);
+    row_sees(P, k.len, k.n, k.i0, &k.least_lo, &k.least_hi);
+    row_sees(P, k.len, k.n, k.i0 + (k.skip + k.rows - 1) / P.group, &k.most_lo, &k.most_hi);
+    k.begin = k.least_lo / kTile * kTile;
+    k.tiles = max((k.most_hi - k.begin + kTile - 1) / kTile, 1);
+    return k;
+}
+
+__device__ __forceinline__ int64_t wave_sum64(int64_t v)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+        const u32 lo = __shfl_xor((u32)(u64)v, d), hi = __shfl_xor((u32)((u64)v >> 32), d);
+        v += (int64_t)((u64)hi << 32 | lo);
+    }
+    return (int64_t)((u64)read_lane((u32)((u64)v >> 32), 0) << 32 | read_lane((u32)(u64)v, 0));
+}
+
+// The workers share all tiles evenly: those of kv head after kv head, of block
+// after block in it.  Worker w has the tiles from total * w / workers on.
+// Consecutive shares go to one XCD, whose L2 then holds the heads they read.
+template <int DT, int D, bool CAP>
+__global__ __launch_bounds__(64 * kPromptWaves) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 void prompt_kernel(const AttentionParams P)
 {
-    typedef Prompt<DT, D, WAVES, CT, CAP> A_;
+    typedef Prompt<DT, D, CAP> A_;
     typedef Half<DT> H;
     __shared__ PromptShared<D> L;
-    constexpr int ROWS = A_::kRows;
-    const int64_t id = block_id() / P.c.heads;
-    const int head = (int)(block_id() - id * P.c.heads);
-    if (id >= P.blocks)
+    constexpr int ROWS = kPromptRows;
+    const int lane = threadIdx.x & 63, id = (int)block_id();
+    if (id >= P.workers)
         return;
-    const int64_t number = P.blocks - 1 - id;        // a prompt's last rows have the most to do
-    int64_t numbered;
-    const int b = sequence_of(P, number, ROWS, &numbered);
-    const int64_t first = row_start(P, b), n64 = row_start(P, b + 1) - first;
-    const int n = (int)max(n64, (int64_t)0);
-    const int64_t row = (number - numbered) * ROWS, rows = (int64_t)n * P.group;
-    if (number < numbered || row >= rows)
+    const int worker = P.workers % 8 ? id : id % 8 * (P.workers / 8) + id / 8;
+    int64_t mine = 0, shares = 0;
+    for (int64_t number = lane; number < P.blocks; number += 64) {
+        const int tiles = block_of<ROWS>(P, number).tiles;
+        mine += tiles;
+        shares += (tiles + kLeastTiles - 1) / kLeastTiles;
+    }
+    const int64_t of_head = wave_sum64(mine), total = of_head * P.c.heads;
+    const int64_t workers = max(min(wave_sum64(shares) * P.c.heads, (int64_t)P.workers), (int64_t)1);
+    if (worker >= workers || total == 0)
         return;
-    const int len = length_of(P, b);
-    const Whole table = whole(P.tables + b * P.table_stride);
-    const int i0 = (int)(row / P.group), skip = (int)(row - (int64_t)i0 * P.group);
+    int64_t at = total * worker / workers;
+    const int64_t end = total * (worker + 1) / workers, begin = at;
+    int head = (int)(at / of_head);
+    // the block that tile `at` is of, and its first tile
+    int64_t number = 0, start = head * of_head;
+    while (true) {
+        int tiles = number + lane < P.blocks ? block_of<ROWS>(P, number + lane).tiles : 0;
+        int upto = tiles;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int x = __shfl_up(upto, d);
+            upto += lane >= d ? x : 0;
+        }
+        const u64 past = __ballot(start + upto > at);
+        if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            number += l;
+            start += (int)read_lane((u32)(upto - tiles), l);
+            break;
+        }
+        start += (int)read_lane((u32)upto, 63);
+        number += 64;
+    }
 
     A_ A(P, L);
     // a negative scale's sign goes to the queries, one of 0 makes them 0: the
     // scores' order is that of their products, and -inf times the factor -inf
     const u32 sign = CAP || P.scale >= 0 ? 0 : 0x80008000u, keep = CAP || P.scale != 0 ? ~0u : 0;
     A.factor = CAP ? 1.0f : P.scale != 0 ? fabsf(P.scale) * kLog2e : 1.0f;
-    // tokens that some row, and that every row, of the block sees
-    int least_lo, most_lo, least_hi, most_hi;
-    row_sees(P, len, n, i0, &least_lo, &least_hi);
-    row_sees(P, len, n, min(i0 + (skip + ROWS - 1) / P.group, n - 1), &most_lo, &most_hi);
+    while (at < end) {
+        Block k = block_of<ROWS>(P, number);
+        while (k.tiles == 0 || at - start >= k.tiles) {
+            start += k.tiles;
+            if (++number >= P.blocks) {
+                number = 0;
+                ++head;
+            }
+            k = block_of<ROWS>(P, number);
+        }
+        const int from = (int)(at - start), to = (int)min((int64_t)k.tiles, from + (end - at));
+        const Whole table = whole(P.tables + k.b * P.table_stride);
+        const int r = A.wave * 32 + A.q, over = (k.skip + r) / P.group;
+        row_sees(P, k.len, k.n, k.i0 + over, &A.lo, &A.hi);
+        if (k.i0 + over >= k.n)
+            A.lo = A.hi = 0;
+        const uint16_t *from_q = P.q + (k.first + min(k.i0 + over, k.n - 1)) * P.q_token +
+                                 (int64_t)(head * P.group + (k.skip + r - over * P.group)) * P.q_head;
 #pragma unroll
-    for (int i = 0; i < CT; ++i) {
-        const int r = skip + (A.wave * CT + i) * 32 + A.q, over = r / P.group;
-        row_sees(P, len, n, i0 + over, &A.lo[i], &A.hi[i]);
-        if (i0 + over >= n)
-            A.lo[i] = A.hi[i] = 0;
-        const uint16_t *at = P.q + (first + min(i0 + over, n - 1)) * P.q_token +
-                             (int64_t)(head * P.group + (r - over * P.group)) * P.q_head;
-#pragma unroll
-        for (int k = 0; k < A.KC; ++k)
-            A.qr[i][k] = (*(const u32x4 *)(at + 16 * k + 8 * A.h) & keep) ^ sign;
-        A.top[i] = kLowest;
-        A.sum[i] = 0.0f;
-        A.nans[i] = 0;
+        for (int c = 0; c < A.KC; ++c)
+            A.qr[c] = (*(const u32x4 *)(from_q + 16 * c + 8 * A.h) & keep) ^ sign;
+        A.top = kLowest;
+        A.sum = 0.0f;
+        A.nans = 0;
 #pragma unroll
         for (int d = 0; d < A.DC; ++d)
-            A.o[i][d] = f32x16{0};
-    }
+            A.o[d] = f32x16{0};
 
-    int t = least_lo / kTile * kTile;
-    if (t < most_hi) {
-        auto is_edge = [&](int at) { return at < most_lo || at + kTile > least_hi; };
-        Raw<D, A.KU> x;
-        const int32_t *entries = P.tables + b * P.table_stride;
-        int last, none;
-        cache_tile(P.c, (len - 1) / kCacheTile * kCacheTile, &last, &none);
-        typename A_::Pages g = A.pages(entries, last, t);
-        A.load(x, g, len, t, head);
-        g = A.pages(entries, last, t + kTile);
-        A.put(x, 0, len, t, is_edge(t));
-        __syncthreads();
-        int buf = 0;
-        while (true) {
-            // the next tile is asked for, this one worked on, the next one put beside it
-            const bool more = t + kTile < most_hi;
-            if (more) {
-                A.load(x, g, len, t + kTile, head);
-                g = A.pages(entries, last, t + 2 * kTile);
-            }
-            A.work(buf, t, table, head, is_edge(t));
-            if (!more)
-                break;
-            t += kTile;
-            buf ^= 1;
-            A.put(x, buf, len, t, is_edge(t));
+        int t = k.begin + from * kTile;
+        const int past = min(k.most_hi, k.begin + to * kTile);
+        if (t < past) {
+            auto is_edge = [&](int x) { return x < k.most_lo || x + kTile > k.least_hi; };
+            RawKeys<D> keys;
+            RawValues<D> vals;
+            A.load(keys, table, k.len, t, head);
+            A.load(vals, table, k.len, t, head);
+            __syncthreads();             // the block before is done with LDS
+            A.put(keys, 0);
+            A.clean(vals, 0, k.len, t, is_edge(t));
+            A.put(vals, 0);
+            A.load(keys, table, k.len, t + kTile, head);
+            A.put(keys, 1);
+            A.load(keys, table, k.len, t + 2 * kTile, head);
+            A.load(vals, table, k.len, t + kTile, head);
             __syncthreads();
+            A.products(A.s, 0);
+            A.settle(0, t, is_edge(t));
+            __syncthreads();
+            int buf = 0;
+            // A step has the weights and values of the tile at t and the products of
+            // the next one: these while the weights are taken, the values while what
+            // comes in, the one after's keys and the next one's values, goes to LDS.
+            while (t + kTile < past) {
+                if (is_edge(t))
+                    A.note(buf, table, t, head);
+                A.clean(vals, buf ^ 1, k.len, t + kTile, is_edge(t + kTile));
+                f32x16 next[2];
+                A.products_and_weights(next, buf ^ 1);
+                A.values_and_puts(buf, vals, keys);
+                t += kTile;
+                buf ^= 1;
+                A.load(keys, table, k.len, t + 2 * kTile, head);
+                A.load(vals, table, k.len, t + kTile, head);
+                A.s[0] = next[0];
+                A.s[1] = next[1];
+                A.settle(buf, t, is_edge(t));
+                __syncthreads();
+            }
+            if (is_edge(t))
+                A.note(buf, table, t, head);
+            A.weigh();
+            A.add(buf);
         }
-    }
 
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-        const u32 s = __float_as_uint(A.sum[i]);
-        auto sums = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+        const bool all = from == 0 && to == k.tiles;
+        float *rec = record<D, ROWS>(P, worker, at == begin);
+        const u32 bits = __float_as_uint(A.sum);
+        auto sums = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
         const float sum = __uint_as_float(sums[0]) + __uint_as_float(sums[1]);
-        auto odd = __builtin_amdgcn_permlane32_swap(A.nans[i], A.nans[i], false, false);
+        auto odd = __builtin_amdgcn_permlane32_swap(A.nans, A.nans, false, false);
         const u32 nans = odd[0] | odd[1];
-        const int r = skip + (A.wave * CT + i) * 32 + A.q, over = r / P.group;
-        if (i0 + over >= n)
-            continue;
-        const int64_t at = (first + i0 + over) * P.q_heads + head * P.group + (r - over * P.group);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        // register i of product d is row r = 8 (i / 4) + 4 h + i % 4 of it, channel
-        // r % 16 D/16 + 2 d + r / 16: D/16 channels side by side in two registers
-        // of all the products
+        if (r < k.rows) {
+            const int64_t row = (k.first + k.i0 + over) * P.q_heads + head * P.group + (k.skip + r - over * P.group);
+            const float inv = !all ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+            // register i of product d is row x = 8 (i / 4) + 4 h + i % 4 of it, channel
+            // x % 16 D/16 + 2 d + x / 16: D/16 channels side by side in two registers
+            // of all the products
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c0 = (8 * j + 4 * A.h + e) * (D / 16);
-                u32 w[A.DC];
+                for (int e = 0; e < 4; ++e) {
+                    const int c0 = (8 * j + 4 * A.h + e) * (D / 16);
+                    const float nan = nans >> (c0 / 32) & 1 ? __builtin_nanf("") : 0.0f;
+                    float v[2 * A.DC];
 #pragma unroll
-                for (int d = 0; d < A.DC; ++d)
-                    w[d] = H::pack(A.o[i][d][4 * j + e] * inv, A.o[i][d][4 * j + 8 + e] * inv);
-                if (nans >> (c0 / 32) & 1)
+                    for (int d = 0; d < A.DC; ++d) {
+                        v[2 * d] = A.o[d][4 * j + e] * inv + nan;
+                        v[2 * d + 1] = A.o[d][4 * j + 8 + e] * inv + nan;
+                    }
+                    if (!all) {
+                        float *out = rec + 2 * ROWS + r * D + c0;
 #pragma unroll
-                    for (int d = 0; d < A.DC; ++d)
-                        w[d] = DT == MHC_BF16 ? 0x7fc07fc0u : 0x7e007e00u;
-                uint16_t *to = P.out + at * D + c0;
-                if constexpr (A.DC == 2) {
-                    *(u32x2 *)to = u32x2{w[0], w[1]};
-                } else {
+                        for (int d = 0; d < 2 * A.DC; d += 4)
+                            *(float4 *)(out + d) = float4{v[d], v[d + 1], v[d + 2], v[d + 3]};
+                        continue;
+                    }
+                    uint16_t *out = P.out + row * D + c0;
 #pragma unroll
-                    for (int d = 0; d < A.DC; d += 4)
-                        *(u32x4 *)(to + 2 * d) = u32x4{w[d], w[d + 1], w[d + 2], w[d + 3]};
+                    for (int d = 0; d < 2 * A.DC; d += 4)
+                        *(u32x2 *)(out + d) = u32x2{H::pack(v[d], v[d + 1]), H::pack(v[d + 2], v[d + 3])};
+                }
+            if (A.h == 0) {
+                if (!all) {
+                    rec[r] = A.top;
+                    rec[ROWS + r] = sum;
+                } else if (P.lse) {
+                    P.lse[row] = sum == 0.0f
+                                     ? -__builtin_inff()
+                                     : (A.top + __builtin_amdgcn_logf(sum) - Softmax<DT>::kShift) * kLn2;
                 }
             }
-        if (P.lse && A.h == 0)
-            P.lse[at] = sum == 0.0f ? -__builtin_inff()
-                                    : (A.top[i] + __builtin_amdgcn_logf(sum) - Softmax<DT>::kShift) * kLn2;
+        }
+        if (from == 0 && threadIdx.x == 0) {
+            Join *j = join_of<D, ROWS>(P, number, head);
+            j->from = worker;
+            j->parts = 0;
+            if (!all)
+                j->parts = (int)((workers * (at + k.tiles) - 1) / total) - worker + 1 |
+                           (at == begin ? kWholeShare : 0);
+        }
+        at += to - from;
     }
 }
 
+int prompt_workers(int cus, int D) { return cus * (D == 256 ? 1 : 2); }
+
 template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
 {
-    constexpr int WAVES = 4, CT = 1;
-    AttentionParams q = p;
-    q.blocks = most_blocks(p.T, p.B, p.group, 32 * CT * WAVES, p.q_starts != nullptr);
-    prompt_kernel<DT, D, WAVES, CT, CAP><<<grid_of(q.blocks * p.c.heads), 64 * WAVES, 0, s>>>(q);
+    prompt_kernel<DT, D, CAP><<<grid_of(p.workers), 64 * kPromptWaves, 0, s>>>(p);
     return hipGetLastError();
 }
 
 template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
 {
-    return p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
+    const hipError_t e = p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
+    return e != hipSuccess ? e : launch_join<DT, D, kPromptRows>(p, s);
 }
 
 template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipStream_t s)
@@ -459,8 +629,17 @@ template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipSt
 
 }  // namespace
 
-hipError_t launch_prompt(const AttentionParams &p, int head_dim, int dtype, hipStream_t s)
+uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus)
 {
+    return join_floats(prompt_workers(cus, head_dim),
+                       most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads, kPromptRows, head_dim);
+}
+
+hipError_t launch_prompt(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
+{
+    AttentionParams p = a;
+    p.blocks = most_blocks(p.T, p.B, p.group, kPromptRows, p.q_starts != nullptr);
+    p.workers = prompt_workers(cus, head_dim);
     return dtype == MHC_BF16 ? launch_width<MHC_BF16>(p, head_dim, s) : launch_width<MHC_F16>(p, head_dim, s);
 }
 

@@ -193,7 +193,8 @@ struct AttentionParams {
 uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus);
 hipError_t launch_attention(const AttentionParams &p, int head_dim, int dtype, int cus, hipStream_t s);
 // The same for many query rows a sequence (prompt_kernels.hip)
-hipError_t launch_prompt(const AttentionParams &p, int head_dim, int dtype, hipStream_t s);
+uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus);
+hipError_t launch_prompt(const AttentionParams &p, int head_dim, int dtype, int cus, hipStream_t s);
 
 hipError_t launch_quantize(const uint16_t *src, int rows, int H, int group, uint8_t *codes,
                            uint8_t *scales, uint16_t *grid, hipStream_t s);
