@@ -112,6 +112,25 @@ inline int64_t most_blocks(int64_t T, int B, int group, int rows, bool ragged)
     return ragged ? T * group / rows + B : (int64_t)B * ((group + rows - 1) / rows);
 }
 
+// Sum of v over the lanes up to this one: inside rows of 16, then over the rows
+__device__ __forceinline__ int sum_upto(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // lanes 1, 2, 4, 8 before
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // lane 15 to the next row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // lane 31 to the last two
+    return v;
+}
+
+// Sum over the lanes of v, not negative and below 2^48
+__device__ __forceinline__ int64_t sum_of_lanes(int64_t v)
+{
+    const int low = (int)read_lane((u32)sum_upto((int)(v & 0xffffff)), 63);
+    return ((int64_t)(int)read_lane((u32)sum_upto((int)(v >> 24)), 63) << 24) + low;
+}
+
 // Which groups of 32 channels of a token's values are NaN, by their scales.  The
 // token is there.
 template <int D>

@@ -32,19 +32,43 @@ __device__ __forceinline__ Join *join_of(const AttentionParams &P, int64_t numbe
     return (Join *)(P.workspace + 2 * (int64_t)P.workers * (ROWS * (D + 2))) + number * P.c.heads + head;
 }
 
-// Four channels of a finished row: head `skip` behind those of query row i
+// What is to be joined of the block that begins in a worker's share and ends in
+// another's: its first part is that worker's, the others the next ones'.
+// count is as Join's parts.
+struct alignas(16) Parts {
+    int64_t row;        // the block's first output row, a head's of a query row
+    int skip, rows;     // its first head in that query row's group; how many rows
+    int count, none[3];
+};
+
+// Behind the joins of all blocks, as many as the batch may have
+template <int D, int ROWS> __device__ __forceinline__ Parts *parts_of(const AttentionParams &P, int worker)
+{
+    const int64_t joins = 2 * P.blocks * P.c.heads;
+    return (Parts *)(P.workspace + 2 * (int64_t)P.workers * (ROWS * (D + 2)) + (joins + 3) / 4 * 4) + worker;
+}
+
+inline uint64_t parts_floats(int workers) { return (uint64_t)workers * sizeof(Parts) / 4 + 4; }
+
+// Four channels of a finished row of the output
 template <int DT, int D>
-__device__ __forceinline__ void store(const AttentionParams &P, int64_t i, int skip, int head, int d, float4 o,
-                                      float top, float sum)
+__device__ __forceinline__ void store_row(const AttentionParams &P, int64_t at, int d, float4 o, float top, float sum)
 {
     typedef Half<DT> H;
-    const int over = skip / P.group;
-    const int64_t at = (i + over) * P.q_heads + head * P.group + (skip - over * P.group);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const u32x2 w = {H::pack(o.x * inv, o.y * inv), H::pack(o.z * inv, o.w * inv)};
     *(u32x2 *)(P.out + at * D + d) = w;
     if (P.lse && d == 0)
         P.lse[at] = sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum) - Softmax<DT>::kShift) * kLn2;
+}
+
+// The same, head `skip` behind those of query row i
+template <int DT, int D>
+__device__ __forceinline__ void store(const AttentionParams &P, int64_t i, int skip, int head, int d, float4 o,
+                                      float top, float sum)
+{
+    const int over = skip / P.group;
+    store_row<DT, D>(P, (i + over) * P.q_heads + head * P.group + (skip - over * P.group), d, o, top, sum);
 }
 
 // Puts together the blocks that several workers have parts of.  WAVES waves a
@@ -135,6 +159,56 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(const A
     }
 }
 
+// The same where most blocks have few parts: D/4 lanes a row, 16 rows a workgroup
+template <int DT, int D, int BLOCK>
+__global__ __launch_bounds__(256) void attention_join_shares_kernel(const AttentionParams P)
+{
+    constexpr int LANES = D / 4, ROWS = 256 / LANES, BATCH = 4, GROUP = 16;
+    const int64_t id = block_id();
+    const int worker = (int)(id / (BLOCK / GROUP));
+    if (worker >= P.workers)
+        return;
+    const Parts j = *parts_of<D, BLOCK>(P, worker);
+    const int count = j.count & ~kWholeShare, d = threadIdx.x % LANES * 4;
+    if (count == 0)
+        return;
+    const int first = (int)(id % (BLOCK / GROUP)) * GROUP;
+    for (int row = first + threadIdx.x / LANES; row < min(first + GROUP, j.rows); row += ROWS) {
+        float most = kLowest, all = 0.0f;
+        float4 o = {0, 0, 0, 0};
+        for (int i0 = 0; i0 < count; i0 += BATCH) {
+            float top[BATCH], sum[BATCH];
+            float4 x[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int i = min(i0 + k, count - 1);
+                const float *rec = record<D, BLOCK>(P, worker + i, i > 0 || (j.count & kWholeShare));
+                top[k] = rec[row];
+                sum[k] = rec[BLOCK + row];
+                x[k] = *(const float4 *)(rec + 2 * BLOCK + row * D + d);
+            }
+            float now = most;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                now = fmaxf(now, top[k]);
+            const float old = __builtin_amdgcn_exp2f(most - now);
+            most = now;
+            all *= old;
+            o = {o.x * old, o.y * old, o.z * old, o.w * old};
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                if (i0 + k >= count)
+                    continue;
+                const float w = __builtin_amdgcn_exp2f(top[k] - now);
+                all += sum[k] * w;
+                o = {o.x + x[k].x * w, o.y + x[k].y * w, o.z + x[k].z * w, o.w + x[k].w * w};
+            }
+        }
+        const int over = (j.skip + row) / P.group;
+        store_row<DT, D>(P, j.row + (int64_t)over * P.q_heads + (j.skip + row - over * P.group), d, o, most, all);
+    }
+}
+
 // Floats of workspace for that many workers and blocks of `rows` rows
 inline uint64_t join_floats(int workers, int64_t blocks, int rows, int D)
 {
@@ -149,6 +223,17 @@ template <int DT, int D, int BLOCK> hipError_t launch_join(const AttentionParams
     else
         attention_join_kernel<DT, D, BLOCK, 1>
             <<<grid_of(segments * (BLOCK / kJoinWaves)), 64 * kJoinWaves, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+// Few blocks may have many parts each: the kernel for those
+template <int DT, int D, int BLOCK> hipError_t launch_join_shares(const AttentionParams &p, hipStream_t s)
+{
+    const int64_t segments = p.blocks * p.c.heads;
+    if (segments * 8 <= p.workers)
+        attention_join_kernel<DT, D, BLOCK, kJoinWaves><<<grid_of(segments * BLOCK), 64 * kJoinWaves, 0, s>>>(p);
+    else
+        attention_join_shares_kernel<DT, D, BLOCK><<<grid_of((int64_t)p.workers * (BLOCK / 16)), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 

@@ -74,18 +74,6 @@ __device__ __forceinline__ int quanta_of(const AttentionParams &P, int b, int *s
     return s.blocks * s.quanta * P.c.heads;
 }
 
-// Sum of v over the lanes up to this one: inside rows of 16, then over the rows
-__device__ __forceinline__ int sum_upto(int v)
-{
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // lanes 1, 2, 4, 8 before
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // lane 15 to the next row
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // lane 31 to the last two
-    return v;
-}
-
 __device__ __forceinline__ int share_start(int total, int workers, int w)
 {
     return (int)((int64_t)total * w / workers);
@@ -541,7 +529,10 @@ bool balanced(int64_t T, int B, int q_heads, int kv_heads, int cus)
 }
 
 // Whether the sequences have rows enough, on average, for prompt_kernel
-bool prompts(int64_t T, int B, int group) { return T * group >= (int64_t)B * 64; }
+bool prompts(int64_t T, int B, int group)
+{
+    return T * group >= (int64_t)B * 64 && T * group + (int64_t)B * 128 < INT32_MAX;
+}
 
 // Nor where the quanta's number might not fit 31 bits
 bool countable(const AttentionParams &p)

@@ -388,36 +388,46 @@ struct Block {
     int begin, tiles;       // the first tile's first token; 1 tile at least
 };
 
-template <int ROWS> __device__ __forceinline__ Block block_of(const AttentionParams &P, int64_t number)
+// Rows times heads of a kv head number below 2^31 in these kernels
+__device__ __forceinline__ Block block_of(const AttentionParams &P, int number)
 {
+    constexpr int ROWS = kPromptRows;
     Block k;
-    int64_t numbered;
     k.rows = k.tiles = 0;
-    k.b = sequence_of(P, number, ROWS, &numbered);
-    k.first = row_start(P, k.b);
-    k.n = (int)max(row_start(P, k.b + 1) - k.first, (int64_t)0);
-    const int64_t row = (number - numbered) * ROWS, rows = (int64_t)k.n * P.group;
-    if (number < numbered || row >= rows)
+    int row;                // of the sequence's
+    if (!P.q_starts) {
+        const int each = (P.group + ROWS - 1) / ROWS;
+        k.b = number / each;
+        k.first = k.b;
+        k.n = 1;
+        row = (number - k.b * each) * ROWS;
+    } else {
+        auto numbered = [&](int64_t start, int b) { return (int)start * P.group / ROWS + b; };
+        int low = 0, high = P.B;
+        while (high - low > 1) {
+            const int mid = (low + high) / 2;
+            if (numbered(row_start(P, mid), mid) <= number)
+                low = mid;
+            else
+                high = mid;
+        }
+        k.b = low;
+        k.first = row_start(P, low);
+        k.n = max((int)(row_start(P, low + 1) - k.first), 0);
+        row = (number - numbered(k.first, low)) * ROWS;
+    }
+    const int rows = k.n * P.group;
+    if (row < 0 || row >= rows)
         return k;
-    k.rows = (int)min(rows - row, (int64_t)ROWS);
+    k.rows = min(rows - row, ROWS);
     k.len = length_of(P, k.b);
-    k.i0 = (int)(row / P.group);
-    k.skip = (int)(row - (int64_t)k.i0 * P.group);
+    k.i0 = row / P.group;
+    k.skip = row - k.i0 * P.group;
     row_sees(P, k.len, k.n, k.i0, &k.least_lo, &k.least_hi);
     row_sees(P, k.len, k.n, k.i0 + (k.skip + k.rows - 1) / P.group, &k.most_lo, &k.most_hi);
     k.begin = k.least_lo / kTile * kTile;
     k.tiles = max((k.most_hi - k.begin + kTile - 1) / kTile, 1);
     return k;
-}
-
-__device__ __forceinline__ int64_t wave_sum64(int64_t v)
-{
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const u32 lo = __shfl_xor((u32)(u64)v, d), hi = __shfl_xor((u32)((u64)v >> 32), d);
-        v += (int64_t)((u64)hi << 32 | lo);
-    }
-    return (int64_t)((u64)read_lane((u32)((u64)v >> 32), 0) << 32 | read_lane((u32)(u64)v, 0));
 }
 
 // The workers share all tiles evenly: those of kv head after kv head, of block
@@ -435,29 +445,30 @@ void prompt_kernel(const AttentionParams P)
     if (id >= P.workers)
         return;
     const int worker = P.workers % 8 ? id : id % 8 * (P.workers / 8) + id / 8;
+    // the block that begins in this share and ends in another's, if there is one
+    Parts *parts = parts_of<D, ROWS>(P, worker);
+    if (threadIdx.x == 0)
+        parts->count = 0;
+    const int blocks = (int)P.blocks;
     int64_t mine = 0, shares = 0;
-    for (int64_t number = lane; number < P.blocks; number += 64) {
-        const int tiles = block_of<ROWS>(P, number).tiles;
+    for (int number = lane; number < blocks; number += 64) {
+        const int tiles = block_of(P, number).tiles;
         mine += tiles;
         shares += (tiles + kLeastTiles - 1) / kLeastTiles;
     }
-    const int64_t of_head = wave_sum64(mine), total = of_head * P.c.heads;
-    const int64_t workers = max(min(wave_sum64(shares) * P.c.heads, (int64_t)P.workers), (int64_t)1);
+    const int64_t of_head = sum_of_lanes(mine), total = of_head * P.c.heads;
+    const int64_t workers = max(min(sum_of_lanes(shares) * P.c.heads, (int64_t)P.workers), (int64_t)1);
     if (worker >= workers || total == 0)
         return;
     int64_t at = total * worker / workers;
     const int64_t end = total * (worker + 1) / workers, begin = at;
     int head = (int)(at / of_head);
     // the block that tile `at` is of, and its first tile
-    int64_t number = 0, start = head * of_head;
+    int number = 0;
+    int64_t start = head * of_head;
     while (true) {
-        int tiles = number + lane < P.blocks ? block_of<ROWS>(P, number + lane).tiles : 0;
-        int upto = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int x = __shfl_up(upto, d);
-            upto += lane >= d ? x : 0;
-        }
+        const int tiles = number + lane < blocks ? block_of(P, number + lane).tiles : 0;
+        const int upto = sum_upto(tiles);
         const u64 past = __ballot(start + upto > at);
         if (past) {
             const int l = __ffsll((unsigned long long)past) - 1;
@@ -475,14 +486,14 @@ void prompt_kernel(const AttentionParams P)
     const u32 sign = CAP || P.scale >= 0 ? 0 : 0x80008000u, keep = CAP || P.scale != 0 ? ~0u : 0;
     A.factor = CAP ? 1.0f : P.scale != 0 ? fabsf(P.scale) * kLog2e : 1.0f;
     while (at < end) {
-        Block k = block_of<ROWS>(P, number);
+        Block k = block_of(P, number);
         while (k.tiles == 0 || at - start >= k.tiles) {
             start += k.tiles;
-            if (++number >= P.blocks) {
+            if (++number >= blocks) {
                 number = 0;
                 ++head;
             }
-            k = block_of<ROWS>(P, number);
+            k = block_of(P, number);
         }
         const int from = (int)(at - start), to = (int)min((int64_t)k.tiles, from + (end - at));
         const Whole table = whole(P.tables + k.b * P.table_stride);
@@ -600,9 +611,14 @@ void prompt_kernel(const AttentionParams P)
             Join *j = join_of<D, ROWS>(P, number, head);
             j->from = worker;
             j->parts = 0;
-            if (!all)
+            if (!all) {
                 j->parts = (int)((workers * (at + k.tiles) - 1) / total) - worker + 1 |
                            (at == begin ? kWholeShare : 0);
+                parts->row = (k.first + k.i0) * P.q_heads + head * P.group;
+                parts->skip = k.skip;
+                parts->rows = k.rows;
+                parts->count = j->parts;
+            }
         }
         at += to - from;
     }
@@ -619,7 +635,7 @@ template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &
 template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
 {
     const hipError_t e = p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
-    return e != hipSuccess ? e : launch_join<DT, D, kPromptRows>(p, s);
+    return e != hipSuccess ? e : launch_join_shares<DT, D, kPromptRows>(p, s);
 }
 
 template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipStream_t s)
@@ -632,7 +648,8 @@ template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipSt
 uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus)
 {
     return join_floats(prompt_workers(cus, head_dim),
-                       most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads, kPromptRows, head_dim);
+                       most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads, kPromptRows, head_dim) +
+           parts_floats(prompt_workers(cus, head_dim));
 }
 
 hipError_t launch_prompt(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
