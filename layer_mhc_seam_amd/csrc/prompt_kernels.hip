@@ -2,8 +2,7 @@
 // sequence: prompts and chunks of them.
 //
 // The matrix cores bound it, 4 D operations a row and token.  A workgroup holds
-// kWaves * 32 * CT rows (query rows times heads of a kv head) and goes through
-// the tokens in tiles of 64, once: keys and values are turned from 4 bits into
+// 128 rows (query rows times heads of a kv head) and goes through the tokens in tiles of 64, once: keys and values are turned from 4 bits into
 // the products' type on their way into LDS, by all waves for all of them, while
 // the tile before is worked on.  A wave's products are 32 x 32 x 16:
 //   S^T = K Q^T     lane (q, h), q = l % 32, h = l / 32, holds row q of Q, and of
@@ -20,6 +19,7 @@ constexpr int kTile = 64;                // tokens
 constexpr int kPromptWaves = 4, kPromptRows = 32 * kPromptWaves;
 constexpr int kGroups = kTile / 8;       // of tokens, as a product's lane has them
 constexpr int kLeastTiles = 4;           // of a worker's share, where a block has as many
+constexpr int kSharedTokens = 2048;      // of sequences whose tiles are shared out
 
 template <int D> struct PromptShared {
     u32x4 k[2][D / 8][kTile];            // eight channels of a token
@@ -64,12 +64,12 @@ template <int DT, int D, bool CAP> struct Prompt {
     PromptShared<D> &L;
     const int lane, wave, q, h;
     u32 at_k, at_ks, at_v, at_vs;        // the lane's bytes in the wave's 16 tokens
-    f32x16 o[DC], s[2];
+    f32x16 o[DC], s[2];                  // of the lane's row, as all below
     u32x4 qr[KC], p[4];
     float top, sum;
+    u32 nans;                            // groups of channels that a NaN reaches
+    int lo, hi;                          // tokens that it sees
     float factor;                        // of the products, to scores in base 2; not negative
-    u32 nans;                            // groups of channels that a NaN reaches in the lane's row
-    int lo, hi;                          // tokens that the lane's row sees
 
     __device__ Prompt(const AttentionParams &p_, PromptShared<D> &l)
         : P(p_), L(l), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), q(lane & 31),
@@ -210,14 +210,14 @@ template <int DT, int D, bool CAP> struct Prompt {
 
     // ------------------------------------------------------------ a tile's work
 
-    __device__ __forceinline__ void products(f32x16 to[2], int buf) const
+    __device__ __forceinline__ void products(int buf)
     {
-        to[0] = to[1] = f32x16{0};
+        s[0] = s[1] = f32x16{0};
 #pragma unroll
         for (int k = 0; k < KC; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                to[i] = H::mfma32(L.k[buf][2 * k + h][32 * i + q], qr[k], to[i]);
+                s[i] = H::mfma32(L.k[buf][2 * k + h][32 * i + q], qr[k], s[i]);
     }
 
     // Token of the tile at t that register j of the scores is, 0 .. 31
@@ -270,39 +270,43 @@ template <int DT, int D, bool CAP> struct Prompt {
         }
     }
 
-    __device__ __forceinline__ void weigh()
+    // Score j as a weight; every second one packs two
+    __device__ __forceinline__ void weigh(int j, float v[2], float part[2], float zero)
     {
-        const float zero = S::kShift - top;
-        float part[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = __builtin_amdgcn_exp2f(fmaf(s[c / 2][c % 2 * 8 + j], factor, zero));
-                part[j % 4] += v[j];
-            }
-            p[c] = u32x4{H::pack(v[0], v[1]), H::pack(v[2], v[3]), H::pack(v[4], v[5]), H::pack(v[6], v[7])};
+        v[j % 2] = __builtin_amdgcn_exp2f(fmaf(s[j / 16][j % 16], factor, zero));
+        part[j % 2] += v[j % 2];
+        if (j % 2) {
+            u32 w = H::pack(v[0], v[1]);
+            asm volatile("" : "+v"(w), "+v"(part[0]), "+v"(part[1]));    // here, and not behind all products
+            p[j / 8][j % 8 / 2] = w;
         }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
+    }
+
+    __device__ __forceinline__ void weights()
+    {
+        float part[2] = {0, 0}, v[2];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            weigh(j, v, part, S::kShift - top);
+        sum += part[0] + part[1];
     }
 
     __device__ __forceinline__ void add(int buf)
     {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int d = 0; d < DC; ++d)
-                o[d] = H::mfma32(*(const u32x4 *)L.v[buf][2 * c + h][d * 32 + q], p[c], o[d]);
+                o[d] = H::mfma32(*(const u32x4 *)L.v[buf][2 * n + h][d * 32 + q], p[n], o[d]);
     }
 
-    // One of the next tile's products with a part of this one's weights beside
-    // it, product after product: the compiler by itself puts the products first
+    // The next tile's products with this one's weights beside them, product after
+    // product: the compiler by itself puts all products first
     __device__ __forceinline__ void products_and_weights(f32x16 next[2], int buf)
     {
         constexpr int N = 2 * KC, EACH = 32 / N, AHEAD = 4;
         const float zero = S::kShift - top;
-        float part[2] = {0, 0}, v[8];
+        float part[2] = {0, 0}, v[2];
         u32x4 a[AHEAD];
         auto read = [&](int n) { return L.k[buf][2 * (n / 2) + h][32 * (n % 2) + q]; };
         next[0] = next[1] = f32x16{0};
@@ -315,15 +319,8 @@ template <int DT, int D, bool CAP> struct Prompt {
                 a[(n + AHEAD - 1) % AHEAD] = read(n + AHEAD - 1);
             next[n % 2] = H::mfma32(a[n % AHEAD], qr[n / 2], next[n % 2]);
 #pragma unroll
-            for (int j = n * EACH; j < (n + 1) * EACH; ++j) {
-                v[j % 8] = __builtin_amdgcn_exp2f(fmaf(s[j / 16][j % 16], factor, zero));
-                part[j % 2] += v[j % 8];
-                if (j % 2) {
-                    u32 w = H::pack(v[j % 8 - 1], v[j % 8]);
-                    asm volatile("" : "+v"(w), "+v"(part[0]), "+v"(part[1]));    // here, and not behind all products
-                    p[j / 8][j % 8 / 2] = w;
-                }
-            }
+            for (int j = n * EACH; j < (n + 1) * EACH; ++j)
+                weigh(j, v, part, zero);
             __builtin_amdgcn_sched_barrier(0);
         }
         sum += part[0] + part[1];
@@ -353,11 +350,11 @@ template <int DT, int D, bool CAP> struct Prompt {
                 a[(n + AHEAD - 1) % AHEAD] = read(n + AHEAD - 1);
             o[n % DC] = H::mfma32(a[n % AHEAD], p[n / DC], o[n % DC]);
             if constexpr (n * CHUNKS / N != (n + 1) * CHUNKS / N) {
-                constexpr int c = n * CHUNKS / N;
-                if constexpr (c < D / 32)
-                    values<c>(vals, f, buf ^ 1);
+                constexpr int chunk = n * CHUNKS / N;
+                if constexpr (chunk < D / 32)
+                    values<chunk>(vals, f, buf ^ 1);
                 else
-                    put_key((c - D / 32) / 4, (c - D / 32) % 4, keys, fk, buf);
+                    put_key((chunk - D / 32) / 4, (chunk - D / 32) % 4, keys, fk, buf);
             }
             __builtin_amdgcn_sched_barrier(0);
         });
@@ -368,7 +365,7 @@ template <int DT, int D, bool CAP> struct Prompt {
     {
         u32 odd = 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+        for (int w = 0; w < kPromptWaves; ++w)
             odd |= L.nan[buf][w];
         if (__builtin_amdgcn_readfirstlane(odd))
 #pragma unroll 1
@@ -430,10 +427,12 @@ __device__ __forceinline__ Block block_of(const AttentionParams &P, int number)
     return k;
 }
 
-// The workers share all tiles evenly: those of kv head after kv head, of block
-// after block in it.  Worker w has the tiles from total * w / workers on.
-// Consecutive shares go to one XCD, whose L2 then holds the heads they read.
-template <int DT, int D, bool CAP>
+// SHARED: the workers share all tiles evenly: those of kv head after kv head, of
+// block after block in it.  Worker w has the tiles from total * w / workers on,
+// consecutive shares go to one XCD, and a block that several have parts of is
+// put together by a join kernel.  Otherwise a workgroup a block, those of a
+// prompt's last rows, which have the most to do, first.
+template <int DT, int D, bool CAP, bool SHARED>
 __global__ __launch_bounds__(64 * kPromptWaves) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 void prompt_kernel(const AttentionParams P)
 {
@@ -441,44 +440,59 @@ void prompt_kernel(const AttentionParams P)
     typedef Half<DT> H;
     __shared__ PromptShared<D> L;
     constexpr int ROWS = kPromptRows;
-    const int lane = threadIdx.x & 63, id = (int)block_id();
-    if (id >= P.workers)
-        return;
-    const int worker = P.workers % 8 ? id : id % 8 * (P.workers / 8) + id / 8;
-    // the block that begins in this share and ends in another's, if there is one
-    Parts *parts = parts_of<D, ROWS>(P, worker);
-    if (threadIdx.x == 0)
-        parts->count = 0;
     const int blocks = (int)P.blocks;
-    int64_t mine = 0, shares = 0;
-    for (int number = lane; number < blocks; number += 64) {
-        const int tiles = block_of(P, number).tiles;
-        mine += tiles;
-        shares += (tiles + kLeastTiles - 1) / kLeastTiles;
-    }
-    const int64_t of_head = sum_of_lanes(mine), total = of_head * P.c.heads;
-    const int64_t workers = max(min(sum_of_lanes(shares) * P.c.heads, (int64_t)P.workers), (int64_t)1);
-    if (worker >= workers || total == 0)
-        return;
-    int64_t at = total * worker / workers;
-    const int64_t end = total * (worker + 1) / workers, begin = at;
-    int head = (int)(at / of_head);
-    // the block that tile `at` is of, and its first tile
-    int number = 0;
-    int64_t start = head * of_head;
-    while (true) {
-        const int tiles = number + lane < blocks ? block_of(P, number + lane).tiles : 0;
-        const int upto = sum_upto(tiles);
-        const u64 past = __ballot(start + upto > at);
-        if (past) {
-            const int l = __ffsll((unsigned long long)past) - 1;
-            number += l;
-            start += (int)read_lane((u32)(upto - tiles), l);
-            break;
+    int head, number, worker = 0;
+    int64_t at, end, start, total = 0, workers = 0;
+    Parts *parts = nullptr;
+    if constexpr (SHARED) {
+        const int lane = threadIdx.x & 63, id = (int)block_id();
+        if (id >= P.workers)
+            return;
+        worker = P.workers % 8 ? id : id % 8 * (P.workers / 8) + id / 8;
+        // the block that begins in this share and ends in another's, if there is one
+        parts = parts_of<D, ROWS>(P, worker);
+        if (threadIdx.x == 0)
+            parts->count = 0;
+        int64_t mine = 0, shares = 0;
+        for (int n = lane; n < blocks; n += 64) {
+            const int tiles = block_of(P, n).tiles;
+            mine += tiles;
+            shares += (tiles + kLeastTiles - 1) / kLeastTiles;
         }
-        start += (int)read_lane((u32)upto, 63);
-        number += 64;
+        const int64_t of_head = sum_of_lanes(mine);
+        total = of_head * P.c.heads;
+        workers = max(min(sum_of_lanes(shares) * P.c.heads, (int64_t)P.workers), (int64_t)1);
+        if (worker >= workers || total == 0)
+            return;
+        at = total * worker / workers;
+        end = total * (worker + 1) / workers;
+        head = (int)(at / of_head);
+        // the block that tile `at` is of, and its first tile
+        number = 0;
+        start = head * of_head;
+        while (true) {
+            const int tiles = number + lane < blocks ? block_of(P, number + lane).tiles : 0;
+            const int upto = sum_upto(tiles);
+            const u64 past = __ballot(start + upto > at);
+            if (past) {
+                const int l = __ffsll((unsigned long long)past) - 1;
+                number += l;
+                start += (int)read_lane((u32)(upto - tiles), l);
+                break;
+            }
+            start += (int)read_lane((u32)upto, 63);
+            number += 64;
+        }
+    } else {
+        const int64_t id = block_id(), behind = id / P.c.heads;
+        if (behind >= blocks)
+            return;
+        head = (int)(id - behind * P.c.heads);
+        number = blocks - 1 - (int)behind;
+        at = start = 0;
+        end = block_of(P, number).tiles;
     }
+    const int64_t begin = at;
 
     A_ A(P, L);
     // a negative scale's sign goes to the queries, one of 0 makes them 0: the
@@ -504,8 +518,8 @@ void prompt_kernel(const AttentionParams P)
         const uint16_t *from_q = P.q + (k.first + min(k.i0 + over, k.n - 1)) * P.q_token +
                                  (int64_t)(head * P.group + (k.skip + r - over * P.group)) * P.q_head;
 #pragma unroll
-        for (int c = 0; c < A.KC; ++c)
-            A.qr[c] = (*(const u32x4 *)(from_q + 16 * c + 8 * A.h) & keep) ^ sign;
+        for (int i = 0; i < A.KC; ++i)
+            A.qr[i] = (*(const u32x4 *)(from_q + 16 * i + 8 * A.h) & keep) ^ sign;
         A.top = kLowest;
         A.sum = 0.0f;
         A.nans = 0;
@@ -530,7 +544,7 @@ void prompt_kernel(const AttentionParams P)
             A.load(keys, table, k.len, t + 2 * kTile, head);
             A.load(vals, table, k.len, t + kTile, head);
             __syncthreads();
-            A.products(A.s, 0);
+            A.products(0);
             A.settle(0, t, is_edge(t));
             __syncthreads();
             int buf = 0;
@@ -555,12 +569,12 @@ void prompt_kernel(const AttentionParams P)
             }
             if (is_edge(t))
                 A.note(buf, table, t, head);
-            A.weigh();
+            A.weights();
             A.add(buf);
         }
 
-        const bool all = from == 0 && to == k.tiles;
-        float *rec = record<D, ROWS>(P, worker, at == begin);
+        const bool all = !SHARED || (from == 0 && to == k.tiles);
+        float *rec = SHARED ? record<D, ROWS>(P, worker, at == begin) : nullptr;
         const u32 bits = __float_as_uint(A.sum);
         auto sums = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
         const float sum = __uint_as_float(sums[0]) + __uint_as_float(sums[1]);
@@ -607,7 +621,7 @@ void prompt_kernel(const AttentionParams P)
                 }
             }
         }
-        if (from == 0 && threadIdx.x == 0) {
+        if (SHARED && from == 0 && threadIdx.x == 0) {
             Join *j = join_of<D, ROWS>(P, number, head);
             j->from = worker;
             j->parts = 0;
@@ -626,16 +640,27 @@ void prompt_kernel(const AttentionParams P)
 
 int prompt_workers(int cus, int D) { return cus * (D == 256 ? 1 : 2); }
 
+// Whether the tiles may be shared out: where the blocks leave half of the CUs'
+// places empty
+bool prompt_shared(int64_t T, int B, int q_heads, int kv_heads, int D, int cus)
+{
+    return most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads * 2 <= prompt_workers(cus, D);
+}
+
 template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
 {
-    prompt_kernel<DT, D, CAP><<<grid_of(p.workers), 64 * kPromptWaves, 0, s>>>(p);
-    return hipGetLastError();
+    if (!p.workspace) {
+        prompt_kernel<DT, D, CAP, false><<<grid_of(p.blocks * p.c.heads), 64 * kPromptWaves, 0, s>>>(p);
+        return hipGetLastError();
+    }
+    prompt_kernel<DT, D, CAP, true><<<grid_of(p.workers), 64 * kPromptWaves, 0, s>>>(p);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_join_shares<DT, D, kPromptRows>(p, s);
 }
 
 template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
 {
-    const hipError_t e = p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
-    return e != hipSuccess ? e : launch_join_shares<DT, D, kPromptRows>(p, s);
+    return p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
 }
 
 template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipStream_t s)
@@ -647,9 +672,12 @@ template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipSt
 
 uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus)
 {
-    return join_floats(prompt_workers(cus, head_dim),
-                       most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads, kPromptRows, head_dim) +
-           parts_floats(prompt_workers(cus, head_dim));
+    if (!prompt_shared(T, B, q_heads, kv_heads, head_dim, cus))
+        return 0;
+    const int workers = prompt_workers(cus, head_dim);
+    return join_floats(workers, most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads, kPromptRows,
+                       head_dim) +
+           parts_floats(workers);
 }
 
 hipError_t launch_prompt(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
@@ -657,6 +685,9 @@ hipError_t launch_prompt(const AttentionParams &a, int head_dim, int dtype, int 
     AttentionParams p = a;
     p.blocks = most_blocks(p.T, p.B, p.group, kPromptRows, p.q_starts != nullptr);
     p.workers = prompt_workers(cus, head_dim);
+    // nor are short sequences': joining costs as much as ten tiles
+    if (p.max_len < kSharedTokens || !prompt_shared(p.T, p.B, p.q_heads, p.c.heads, head_dim, cus))
+        p.workspace = nullptr;
     return dtype == MHC_BF16 ? launch_width<MHC_BF16>(p, head_dim, s) : launch_width<MHC_F16>(p, head_dim, s);
 }
 

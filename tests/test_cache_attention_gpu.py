@@ -120,10 +120,21 @@ def test_prompts(T, L, Hq, Hk, dt):
 @pytest.mark.parametrize("causal,window,softcap,scale", [(True, 0, 0.0, None), (False, 0, 0.0, None), (True, 50, 0.0, -0.2),
                                                          (False, 70, 8.0, None), (True, 1, 30.0, -0.1),
                                                          (True, 400, 5.0, None), (True, 0, 0.0, 0.0)])
-def test_prompt_masks(causal, window, softcap, scale, D, dt):
-    """Rows for several workgroups, of heads in threes and more, some with more rows than tokens."""
+@pytest.mark.parametrize("width", [None, 64])
+def test_prompt_masks(causal, window, softcap, scale, width, D, dt):
+    """Rows for several workgroups, of heads in threes and more, some with more rows than tokens; tables short, and
+    long enough for tiles to be shared out."""
     both([190, 130, 64, 5, 0, 333], [150, 130, 1, 90, 3, 0], 6, 2, D, 48, dt, causal=causal, window=window,
-         softcap=softcap, scale=scale)
+         softcap=softcap, scale=scale, width=width)
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,rows,window", [([5000], [70], 0), ([100, 3000, 0, 2100], [1, 100, 2, 260], 0),
+                                              ([2500, 2500], [300, 90], 700), ([3000, 1, 40, 700], [70, 1, 40, 300], 0)])
+def test_prompt_shares(lens, rows, window, D, dt):
+    """Few blocks of long sequences, whose tiles several workers share."""
+    both(lens, rows, 3, 1, D, 64, dt, window=window, width=80)
 
 
 @pytest.mark.parametrize("dt", [BF, F16])
@@ -186,12 +197,13 @@ def put(d, b, t, kind, D, ps, block, byte=255):
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dt", [BF, F16])
-@pytest.mark.parametrize("lens,rows,window", [((70, 140, 300), (30, 4, 1), 0), ((170, 240, 300), (130, 100, 1), 0),
-                                              ((170, 240, 300), (130, 100, 1), 60)])
-def test_nan_reaches_who_sees_it(lens, rows, window, D, dt):
+@pytest.mark.parametrize("lens,rows,window,width", [
+    ((70, 140, 300), (30, 4, 1), 0, None), ((170, 240, 300), (130, 100, 1), 0, None),
+    ((170, 240, 300), (130, 100, 1), 60, None), ((170, 240, 300), (130, 100, 1), 0, 130)])
+def test_nan_reaches_who_sees_it(lens, rows, window, width, D, dt):
     """A NaN in a key makes the rows that see it NaN, one in a value only its 32 channels of them."""
     ps = 16
-    d, keys, values = batch(lens, rows, 4, 2, D, ps, dt, seed=9)
+    d, keys, values = batch(lens, rows, 4, 2, D, ps, dt, seed=9, width=width)
     for b, t, kind, block in ((0, lens[0] - 25, 1, 1), (0, lens[0] - 10, 0, 0), (1, lens[1] - 2, 1, D // 32 - 1),
                               (1, lens[1] - 1, 0, 1), (2, 20, 1, 0), (2, 260, 1, 1), (1, 20, 1, 0)):
         put(d, b, t, kind, D, ps, block)
@@ -223,6 +235,10 @@ def test_what_nobody_sees_may_be_anything(rows, D):
                     dirty[page, :, c:c + D // 2] = d["cache"][page, :, c:c + D // 2]
                     dirty[page, :, s] = d["cache"][page, :, s]
         d["cache"] = dirty
+        wide = torch.full((len(lens), 100), 2 ** 31 - 1, dtype=torch.int32)
+        wide[:, :d["tables"].shape[1]] = d["tables"]
+        long = run(dict(d, tables=wide), **kw)
+        check(long, ref.attention(d["q"], keys, values, lens, d["starts"], **kw))
         got = run(d, **kw)
         assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
         check(got, ref.attention(d["q"], keys, values, lens, d["starts"], **kw))
@@ -230,8 +246,13 @@ def test_what_nobody_sees_may_be_anything(rows, D):
 
 @pytest.mark.parametrize("rows", [(3, 1, 1), (80, 60, 33)])
 def test_bad_pages_hide_their_tokens(rows):
+    for width in (None, 200):
+        bad_pages(rows, width)
+
+
+def bad_pages(rows, width):
     lens, ps, D = [100, 64, 40], 16, 128
-    d, keys, values = batch(lens, rows, 4, 2, D, ps, BF, seed=4)
+    d, keys, values = batch(lens, rows, 4, 2, D, ps, BF, seed=4, width=width)
     seen = [torch.ones(n, dtype=torch.bool) for n in lens]
     pages = d["cache"].shape[0]
     for b, page, bad in ((0, 2, -1), (0, 6, pages), (1, 0, 2 ** 31 - 1), (1, 3, -2 ** 31), (2, 0, pages + 5),
