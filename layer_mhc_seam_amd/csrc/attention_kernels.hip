@@ -26,7 +26,8 @@ constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kQuantum = kStep * kAttnWaves;   // tokens that a workgroup's waves take side by side
 constexpr int kMostBalanced = 1024;       // sequences whose lengths a worker adds up
-constexpr int kLeastQuanta = 4;           // of a worker's share
+constexpr int kLeastQuanta = 4;           // of a worker's share, where a block has as many
+constexpr int kAloneTokens = 1024;        // of sequences whose blocks a workgroup each has alone
 
 // A sequence's share of the work: blocks of rows, and the quanta of tokens that
 // some row of it sees, the same number for every block and kv head.
@@ -521,36 +522,29 @@ template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipSt
     return D == 64 ? launch<DT, 64>(p, s) : D == 128 ? launch<DT, 128>(p, s) : launch<DT, 256>(p, s);
 }
 
-// Whether a batch's quanta may be shared out: not where there are blocks for
-// every CU many times over, or more sequences than a worker adds up
-bool balanced(int64_t T, int B, int q_heads, int kv_heads, int cus)
-{
-    return B <= kMostBalanced && most_blocks(T, B, q_heads / kv_heads, kRows, true) * kv_heads < (int64_t)cus * 16;
-}
-
 // Whether the sequences have rows enough, on average, for prompt_kernel
 bool prompts(int64_t T, int B, int group)
 {
     return T * group >= (int64_t)B * 64 && T * group + (int64_t)B * 128 < INT32_MAX;
 }
 
-// Nor where the quanta's number might not fit 31 bits
-bool countable(const AttentionParams &p)
-{
-    const int64_t blocks = most_blocks(p.T, p.B, p.group, kRows, true) * p.c.heads;
-    return blocks * (p.max_len / kQuantum + 1) <= INT32_MAX;
-}
-
 }  // namespace
 
-uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus)
+uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus,
+                                    int64_t max_len)
 {
-    if (prompts(T, B, q_heads / kv_heads))
-        return prompt_workspace_floats(T, B, q_heads, kv_heads, head_dim, cus);
-    if (!balanced(T, B, q_heads, kv_heads, cus))
+    const int group = q_heads / kv_heads;
+    if (prompts(T, B, group))
+        return prompt_workspace_floats(T, B, q_heads, kv_heads, head_dim, cus, max_len);
+    // quanta are shared out but where there are blocks for every CU many times
+    // over, more sequences than a worker adds up, more quanta than 31 bits hold,
+    // or sequences so short that a block's own waves are soon done (a second
+    // launch costs as much as 1000 tokens)
+    const int64_t blocks = most_blocks(T, B, group, kRows, true) * kv_heads;
+    if (B > kMostBalanced || blocks >= (int64_t)cus * 16 || max_len <= kAloneTokens ||
+        blocks * (max_len / kQuantum + 1) > INT32_MAX)
         return 0;
-    return join_floats(workers_of(cus, head_dim), most_blocks(T, B, q_heads / kv_heads, kRows, true) * kv_heads,
-                       kRows, head_dim);
+    return join_floats(workers_of(cus, head_dim), blocks, kRows, head_dim);
 }
 
 hipError_t launch_attention(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
@@ -560,8 +554,6 @@ hipError_t launch_attention(const AttentionParams &a, int head_dim, int dtype, i
     AttentionParams p = a;
     p.blocks = most_blocks(p.T, p.B, p.group, kRows, p.q_starts != nullptr);
     p.workers = workers_of(cus, head_dim);
-    if (!balanced(p.T, p.B, p.q_heads, p.c.heads, cus) || !countable(p))
-        p.workspace = nullptr;
     return dtype == MHC_BF16 ? launch_width<MHC_BF16>(p, head_dim, s) : launch_width<MHC_F16>(p, head_dim, s);
 }
 

@@ -243,11 +243,12 @@ int mhc_cache_write(const mhc_cache_args *a, void *stream) { return run_cache(a,
 int mhc_cache_read(const mhc_cache_args *a, void *stream) { return run_cache(a, false, stream); }
 
 int mhc_cache_attention_workspace(int64_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                                  int32_t cu_count, uint64_t *bytes)
+                                  int32_t cu_count, int64_t max_len, uint64_t *bytes)
 {
-    if (!attention_sizes(T, B, q_heads, kv_heads, head_dim) || cu_count < 1 || cu_count > 4096 || !bytes)
+    if (!attention_sizes(T, B, q_heads, kv_heads, head_dim) || cu_count < 1 || cu_count > 4096 || max_len < 0 ||
+        max_len > (1 << 30) || !bytes)
         return fail(MHC_SEAM_INVALID_ARG, "workspace of cache attention: sizes out of range");
-    *bytes = T && B ? 4 * attention_workspace_floats(T, B, q_heads, kv_heads, head_dim, cu_count) : 0;
+    *bytes = T && B ? 4 * attention_workspace_floats(T, B, q_heads, kv_heads, head_dim, cu_count, max_len) : 0;
     return MHC_SEAM_OK;
 }
 
@@ -292,7 +293,10 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
     hipError_t e = compute_units(&cus);
     if (e != hipSuccess)
         return hip_fail(e, "device attributes");
-    const uint64_t floats = attention_workspace_floats(T, a->B, a->q_heads, a->kv_heads, a->head_dim, cus);
+    int64_t max_len = (int64_t)a->table_width * a->page_size;
+    if (a->max_len > 0 && a->max_len < max_len)
+        max_len = a->max_len;
+    const uint64_t floats = attention_workspace_floats(T, a->B, a->q_heads, a->kv_heads, a->head_dim, cus, max_len);
     if (floats && (!a->workspace || a->workspace_bytes < 4 * floats))
         return fail(MHC_SEAM_INVALID_ARG, "cache attention needs a workspace of %llu bytes",
                     (unsigned long long)(4 * floats));
@@ -309,9 +313,7 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
     AttentionParams p{};
     p.c = cache_layout(a->pages, a->kv_heads, a->page_size);
     p.T = T;
-    p.max_len = (int64_t)a->table_width * a->page_size;
-    if (a->max_len > 0 && a->max_len < p.max_len)
-        p.max_len = a->max_len;
+    p.max_len = max_len;
     p.q_token = a->q_token;
     p.q_head = a->q_head;
     p.table_stride = a->table_stride;
@@ -329,7 +331,7 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
     p.q_starts = a->q_starts;
     p.out = (uint16_t *)a->out;
     p.lse = a->lse;
-    p.workspace = (float *)a->workspace;
+    p.workspace = floats ? (float *)a->workspace : nullptr;
     e = launch_attention(p, a->head_dim, a->dtype, cus, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess)
         return hip_fail(e, "cache attention launch");

@@ -640,13 +640,6 @@ void prompt_kernel(const AttentionParams P)
 
 int prompt_workers(int cus, int D) { return cus * (D == 256 ? 1 : 2); }
 
-// Whether the tiles may be shared out: where the blocks leave half of the CUs'
-// places empty
-bool prompt_shared(int64_t T, int B, int q_heads, int kv_heads, int D, int cus)
-{
-    return most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads * 2 <= prompt_workers(cus, D);
-}
-
 template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
 {
     if (!p.workspace) {
@@ -670,14 +663,15 @@ template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipSt
 
 }  // namespace
 
-uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus)
+uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus, int64_t max_len)
 {
-    if (!prompt_shared(T, B, q_heads, kv_heads, head_dim, cus))
-        return 0;
     const int workers = prompt_workers(cus, head_dim);
-    return join_floats(workers, most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads, kPromptRows,
-                       head_dim) +
-           parts_floats(workers);
+    const int64_t blocks = most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads;
+    // tiles are shared out where the blocks leave half of the CUs' places empty
+    // and sequences may be long: joining costs as much as ten tiles
+    if (blocks * 2 > workers || max_len < kSharedTokens)
+        return 0;
+    return join_floats(workers, blocks, kPromptRows, head_dim) + parts_floats(workers);
 }
 
 hipError_t launch_prompt(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
@@ -685,9 +679,6 @@ hipError_t launch_prompt(const AttentionParams &a, int head_dim, int dtype, int 
     AttentionParams p = a;
     p.blocks = most_blocks(p.T, p.B, p.group, kPromptRows, p.q_starts != nullptr);
     p.workers = prompt_workers(cus, head_dim);
-    // nor are short sequences': joining costs as much as ten tiles
-    if (p.max_len < kSharedTokens || !prompt_shared(p.T, p.B, p.q_heads, p.c.heads, head_dim, cus))
-        p.workspace = nullptr;
     return dtype == MHC_BF16 ? launch_width<MHC_BF16>(p, head_dim, s) : launch_width<MHC_F16>(p, head_dim, s);
 }
 

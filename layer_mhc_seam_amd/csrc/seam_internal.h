@@ -189,11 +189,12 @@ struct AttentionParams {
     int workers;
     int64_t blocks;           // row blocks that the batch may have
 };
-// Floats of workspace and the launch, which takes as many
-uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus);
+// Floats of workspace, 0 for none, and the launch, which takes them as a plan
+uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus,
+                                    int64_t max_len);
 hipError_t launch_attention(const AttentionParams &p, int head_dim, int dtype, int cus, hipStream_t s);
 // The same for many query rows a sequence (prompt_kernels.hip)
-uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus);
+uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, int head_dim, int cus, int64_t max_len);
 hipError_t launch_prompt(const AttentionParams &p, int head_dim, int dtype, int cus, hipStream_t s);
 
 hipError_t launch_quantize(const uint16_t *src, int rows, int H, int group, uint8_t *codes,

@@ -164,7 +164,7 @@ def lib():
     L.mhc_cache_read.argtypes = [ctypes.POINTER(CacheArgs), _P]
     L.mhc_cache_attention.argtypes = [ctypes.POINTER(CacheAttentionArgs), _P]
     L.mhc_cache_attention_workspace.argtypes = [ctypes.c_int64, *[ctypes.c_int32] * 5,
-                                                ctypes.POINTER(ctypes.c_uint64)]
+                                                ctypes.c_int64, ctypes.POINTER(ctypes.c_uint64)]
     for name in ("mhc_block_norm", "mhc_int8_quantize", "mhc_int8_gemm", "mhc_int8_gemm_blocks",
                  "mhc_route", "mhc_rope", "mhc_cache_write", "mhc_cache_read",
                  "mhc_cache_attention", "mhc_cache_attention_workspace"):
@@ -727,6 +727,15 @@ def _head_strides(name, t, dtype, shape, index):
     return token, head
 
 
+def _dense_like(t):
+    """An uninitialised dense tensor of t's type and [T, heads, D] shape."""
+    import torch
+    if t.is_contiguous():
+        return torch.empty_like(t)
+    T, H, D = t.shape
+    return torch.empty_strided((T, H, D), (H * D, D, 1), dtype=t.dtype, device=t.device)
+
+
 @functools.lru_cache(maxsize=64)
 def _pair_axes(axes, pairs, most):
     """axes, one for each pair, as the library's bytes."""
@@ -793,8 +802,7 @@ def rope(q, k, positions, inv_freq, *, axes=None, interleaved=False, inverse=Fal
         if Hk == 0:
             raise ValueError("k has no heads: give None")
     if out is None:
-        qo = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-        ko = None if k is None else torch.empty((T, Hk, D), dtype=dt, device=q.device)
+        qo, ko = _dense_like(q), None if k is None else _dense_like(k)
         qos, kos = (Hq * D, D), (Hk * D, D)
     else:
         qo, ko = out
@@ -822,17 +830,25 @@ def kv_cache(pages, heads, head_dim, page_size=64, *, device="cuda"):
                        device=device)
 
 
-def _cache_sizes(cache, heads, D, index):
-    """(pages, page_size) of a cache for those heads."""
-    import torch
-    if cache.dim() != 3:
+@functools.lru_cache(maxsize=256)
+def _pages_of(shape, heads, D):
+    """(pages, page_size) of a cache of that shape for those heads."""
+    if len(shape) != 3:
         raise ValueError("cache must be [pages, heads, bytes of a page]")
-    pages, H, each = cache.shape
+    pages, H, each = shape
     token = D + D // 16
-    if H != heads or each == 0 or each % (16 * token):    # pages of whole 16 tokens
-        raise ValueError(f"cache {tuple(cache.shape)} does not hold {heads} heads of {D} channels")
-    _need("cache", cache, torch.uint8, cache.shape, index)
+    if H != heads or D < 1 or each == 0 or each % (16 * token):     # pages of whole 16 tokens
+        raise ValueError(f"cache {tuple(shape)} does not hold {heads} heads of {D} channels")
     return pages, each // token
+
+
+def _cache_sizes(cache, heads, D, index):
+    """(pages, page_size) of a cache for those heads, on that device."""
+    import torch
+    sizes = _pages_of(cache.shape, heads, D)
+    if cache.dtype is not torch.uint8 or cache.get_device() != index or not cache.is_contiguous():
+        _need("cache", cache, torch.uint8, cache.shape, index)
+    return sizes
 
 
 def cache_write(cache, k, v, slots, *, stream=None):
@@ -878,9 +894,10 @@ def cache_read(cache, slots, head_dim, *, dtype="bf16", out=None, stream=None):
     _need("slots", slots, slots.dtype, (T,), index)
     dt, shape = _types()[0][dtype], (T, H, head_dim)
     if out is None:
-        k = torch.empty(shape, dtype=dt, device=cache.device)
-        v = torch.empty(shape, dtype=dt, device=cache.device)
         ks = vs = (H * head_dim, head_dim)
+        where = cache.device
+        k = torch.empty_strided(shape, (*ks, 1), dtype=dt, device=where)
+        v = torch.empty_strided(shape, (*ks, 1), dtype=dt, device=where)
     else:
         k, v = out
         ks, vs = _head_strides("k", k, dt, shape, index), _head_strides("v", v, dt, shape, index)
@@ -897,12 +914,12 @@ def _compute_units(index):
 
 
 @functools.lru_cache(maxsize=4096)
-def cache_attention_workspace(T, B, q_heads, kv_heads, head_dim, cu_count=256):
+def cache_attention_workspace(T, B, q_heads, kv_heads, head_dim, cu_count=256, max_len=1 << 30):
     """Bytes of workspace that cache_attention takes for T query rows in B
-    sequences (host only)."""
+    sequences of up to max_len tokens (host only)."""
     _fits(B | q_heads | kv_heads | head_dim | cu_count)
     n = ctypes.c_uint64()
-    _check(lib().mhc_cache_attention_workspace(T, B, q_heads, kv_heads, head_dim, cu_count,
+    _check(lib().mhc_cache_attention_workspace(T, B, q_heads, kv_heads, head_dim, cu_count, max_len,
                                                ctypes.byref(n)))
     return n.value
 
@@ -950,7 +967,7 @@ def cache_attention(q, cache, tables, lens, *, q_starts=None, scale=None, causal
         raise ValueError("max_len must be positive")
     sums = None
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=q.device)
+        out = _dense_like(q)
         if lse:
             sums = _new(T, Hq, torch.float32, q.device)
     else:
@@ -958,8 +975,8 @@ def cache_attention(q, cache, tables, lens, *, q_starts=None, scale=None, causal
             out, sums = out
             _need("lse", sums, torch.float32, (T, Hq), index)
         _need("out", out, dt, shape, index)
-    size = cache_attention_workspace(T, B, Hq, Hk, D, _compute_units(index))
-    space = torch.empty((size,), dtype=torch.uint8, device=q.device) if size else None
+    size = cache_attention_workspace(T, B, Hq, Hk, D, _compute_units(index), most or width * ps)
+    space = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=q.device) if size else None
     a = CacheAttentionArgs(T, most, pages, *qs, tables.stride(0) if B > 1 else width, B, Hq, Hk, D, ps,
                            width, _types()[1][dt], bool(causal), window,
                            D ** -0.5 if scale is None else scale, softcap, 0, q.data_ptr(),

@@ -163,8 +163,12 @@ def test_attention_workspace():
     for bad in ((-1, 1, 8, 2, 128), (1, 1, 8, 3, 128), (1, 1, 8, 2, 96), (1, 1, 8, 0, 128), (1, -1, 8, 2, 128)):
         with pytest.raises(S.SeamError):
             S.cache_attention_workspace(*bad)
-    with pytest.raises(S.SeamError):
-        S.cache_attention_workspace(1, 1, 8, 2, 128, 0)
+    for bad in (dict(cu_count=0), dict(cu_count=5000), dict(max_len=-1), dict(max_len=(1 << 30) + 1)):
+        with pytest.raises(S.SeamError):
+            S.cache_attention_workspace(1, 1, 8, 2, 128, **bad)
+    for rows, B in ((1, 1), (64, 64), (300, 2), (5, 5)):       # not falling with the longest length
+        sizes = [S.cache_attention_workspace(rows, B, 8, 2, 128, 256, n) for n in (0, 100, 1024, 4096, 1 << 20, 1 << 30)]
+        assert sizes == sorted(sizes) and sizes[0] == 0
     with pytest.raises(ValueError, match="out of range"):
         S.cache_attention_workspace(1, 2 ** 32 + 1, 8, 2, 128)
 
