@@ -69,10 +69,10 @@ __device__ __forceinline__ void row_sees(const AttentionParams &P, int len, int 
     *lo = P.window > 0 ? max(max(p, -1) + 1 - P.window, 0) : 0;
 }
 
-// First query row of sequence b and past its last
-__device__ __forceinline__ int64_t row_start(const AttentionParams &P, int b)
+// First query row of sequence b, and past the last of b - 1
+__device__ __forceinline__ int row_start(const AttentionParams &P, int b)
 {
-    return P.q_starts ? min((int64_t)max(whole(P.q_starts)[b], 0), P.T) : b;
+    return P.q_starts ? min(max(whole(P.q_starts)[b], 0), (int)P.T) : b;
 }
 
 __device__ __forceinline__ int length_of(const AttentionParams &P, int b)
@@ -81,18 +81,19 @@ __device__ __forceinline__ int length_of(const AttentionParams &P, int b)
 }
 
 // Row blocks of `rows` rows: those of sequence b have the numbers from
-// first_number on, of which there may be more than it has blocks.
-__device__ __forceinline__ int64_t first_number(const AttentionParams &P, int b, int64_t start, int rows)
+// first_number on, of which there may be more than it has blocks.  Rows times
+// heads of a kv head number below 2^31, and so do these.
+__device__ __forceinline__ int first_number(const AttentionParams &P, int b, int start, int rows)
 {
-    return P.q_starts ? start * P.group / rows + b : (int64_t)b * ((P.group + rows - 1) / rows);
+    return P.q_starts ? start * P.group / rows + b : b * ((P.group + rows - 1) / rows);
 }
 
 // The sequence that number `id` is one of, and its first number
-__device__ __forceinline__ int sequence_of(const AttentionParams &P, int64_t id, int rows, int64_t *first)
+__device__ __forceinline__ int sequence_of(const AttentionParams &P, int id, int rows, int *first)
 {
     int low = 0, high = P.B;
     if (!P.q_starts) {
-        low = (int)(id / ((P.group + rows - 1) / rows));
+        low = id / ((P.group + rows - 1) / rows);
     } else {
         while (high - low > 1) {
             const int mid = (low + high) / 2;

@@ -27,9 +27,9 @@ constexpr int kWholeShare = 1 << 30;
 
 // Of the block with that number and that kv head
 template <int D, int ROWS>
-__device__ __forceinline__ Join *join_of(const AttentionParams &P, int64_t number, int head)
+__device__ __forceinline__ Join *join_of(const AttentionParams &P, int number, int head)
 {
-    return (Join *)(P.workspace + 2 * (int64_t)P.workers * (ROWS * (D + 2))) + number * P.c.heads + head;
+    return (Join *)(P.workspace + 2 * (int64_t)P.workers * (ROWS * (D + 2))) + (int64_t)number * P.c.heads + head;
 }
 
 // What is to be joined of the block that begins in a worker's share and ends in
@@ -79,21 +79,21 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(const A
     constexpr int ROWS = kJoinWaves / WAVES, LANES = D / 4, AT_ONCE = 64 / LANES * WAVES, BATCH = WAVES > 1 ? 8 : 2;
     __shared__ float4 L[kJoinWaves][LANES];
     __shared__ float2 M[kJoinWaves];
-    const int64_t id = block_id(), segment = id / (BLOCK / ROWS), number = segment / P.c.heads;
-    if (number >= P.blocks)
+    const int64_t id = block_id(), segment = id / (BLOCK / ROWS), behind = segment / P.c.heads;
+    if (behind >= P.blocks)
         return;
-    const int head = (int)(segment - number * P.c.heads);
+    const int number = (int)behind, head = (int)(segment - behind * P.c.heads);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int row = (int)(id % (BLOCK / ROWS)) * ROWS + wave / WAVES;
     const Join j = *join_of<D, BLOCK>(P, number, head);
-    int64_t first;
+    int first;
     const int b = sequence_of(P, number, BLOCK, &first);
-    const int64_t from = row_start(P, b), rows = (row_start(P, b + 1) - from) * P.group;
+    const int from = row_start(P, b), rows = (row_start(P, b + 1) - from) * P.group;
     // every block's Join has been written, those of numbers that no block has not
     if (number < first || (number - first) * BLOCK >= rows)
         return;
     const int parts = j.parts & ~kWholeShare;
-    const int64_t at = (number - first) * BLOCK;
+    const int at = (number - first) * BLOCK;
     if (parts == 0 || (WAVES > 1 && at + row >= rows))      // the workgroup's all
         return;
     const int d = lane % LANES * 4;
@@ -154,8 +154,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(const A
             add(M[w].x, M[w].y, L[w][lane % LANES]);
     }
     if (lane < LANES && at + row < rows) {
-        const int64_t i = at / P.group;
-        store<DT, D>(P, from + i, (int)(at - i * P.group) + row, head, d, o, most, all);
+        const int i = at / P.group;
+        store<DT, D>(P, from + i, at - i * P.group + row, head, d, o, most, all);
     }
 }
 

@@ -27,14 +27,14 @@ constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kQuantum = kStep * kAttnWaves;   // tokens that a workgroup's waves take side by side
 constexpr int kMostBalanced = 1024;       // sequences whose lengths a worker adds up
 constexpr int kLeastQuanta = 4;           // of a worker's share, where a block has as many
-constexpr int kAloneTokens = 1024;        // of sequences whose blocks a workgroup each has alone
+constexpr int kAloneTokens = 2048;        // of sequences whose blocks a workgroup each has alone
 
 // A sequence's share of the work: blocks of rows, and the quanta of tokens that
 // some row of it sees, the same number for every block and kv head.
 struct Sequence {
-    int64_t first;      // its first query row
-    int64_t rows;       // query rows times heads of a kv head
+    int first;          // its first query row
     int n;              // query rows
+    int rows;           // times heads of a kv head
     int len;            // cached tokens
     int lo;             // first quantum's first token
     int blocks;         // of kRows rows
@@ -44,15 +44,14 @@ struct Sequence {
 __device__ __forceinline__ Sequence sequence(const AttentionParams &P, int b)
 {
     Sequence s;
-    const int64_t from = row_start(P, b), to = row_start(P, b + 1);
-    s.first = from;
-    s.n = (int)max(to - from, (int64_t)0);
-    s.rows = (int64_t)s.n * P.group;
+    s.first = row_start(P, b);
+    s.n = max(row_start(P, b + 1) - s.first, 0);
+    s.rows = s.n * P.group;
     s.len = length_of(P, b);
     int hi;
     row_sees(P, s.len, s.n, 0, &s.lo, &hi);
     s.lo = s.lo / kStep * kStep;
-    s.blocks = (int)((s.rows + kRows - 1) / kRows);
+    s.blocks = (s.rows + kRows - 1) / kRows;
     s.quanta = max((s.len - s.lo + kQuantum - 1) / kQuantum, 1);
     return s;
 }
@@ -61,7 +60,7 @@ __device__ __forceinline__ Sequence sequence(const AttentionParams &P, int b)
 // kv head after kv head in it, of block after block.  Their number is below 2^31.
 struct Share {
     int begin, end;
-    int total, workers;
+    int each, over;     // quanta of a worker; workers that have one more
     int b;              // the sequence of quantum `begin`
     int start;          // that sequence's first quantum
 };
@@ -75,15 +74,14 @@ __device__ __forceinline__ int quanta_of(const AttentionParams &P, int b, int *s
     return s.blocks * s.quanta * P.c.heads;
 }
 
-__device__ __forceinline__ int share_start(int total, int workers, int w)
-{
-    return (int)((int64_t)total * w / workers);
-}
+// The first `over` workers have one quantum more than the others' `each`
+__device__ __forceinline__ int share_start(const Share &h, int w) { return w * h.each + min(w, h.over); }
 
 // The worker whose share holds that quantum
-__device__ __forceinline__ int share_of(int total, int workers, int quantum)
+__device__ __forceinline__ int share_of(const Share &h, int quantum)
 {
-    return (int)(((int64_t)workers * (quantum + 1) - 1) / total);
+    const int more = h.over * (h.each + 1);
+    return quantum < more ? quantum / (h.each + 1) : h.over + (quantum - more) / h.each;
 }
 
 __device__ Share share(const AttentionParams &P, int worker)
@@ -92,13 +90,15 @@ __device__ Share share(const AttentionParams &P, int worker)
     Share h;
     // a worker for kLeastQuanta quanta of a block, if there are as many
     int shares = 0, own = quanta_of(P, lane, &shares), upto = sum_upto(own);
-    h.total = (int)read_lane((u32)upto, 63);
+    int total = (int)read_lane((u32)upto, 63);
     for (int b0 = 64; b0 < P.B; b0 += 64)
-        h.total += (int)read_lane((u32)sum_upto(quanta_of(P, b0 + lane, &shares)), 63);
+        total += (int)read_lane((u32)sum_upto(quanta_of(P, b0 + lane, &shares)), 63);
     shares = (int)read_lane((u32)sum_upto(shares), 63);
-    h.workers = max(min(shares, P.workers), 1);
-    h.begin = worker < h.workers ? share_start(h.total, h.workers, worker) : h.total;
-    h.end = worker < h.workers ? share_start(h.total, h.workers, worker + 1) : h.total;
+    const int workers = max(min(shares, P.workers), 1);
+    h.each = total / workers;
+    h.over = total - h.each * workers;
+    h.begin = worker < workers ? share_start(h, worker) : total;
+    h.end = worker < workers ? share_start(h, worker + 1) : total;
     h.b = h.start = 0;
     if (h.begin == h.end)
         return h;
@@ -165,7 +165,7 @@ template <int DT, int D, bool CAP> struct Attention {
         const int over = (skip + c) / P.group, i = i0 + over;
         if (i < s.n) {
             const uint16_t *at =
-                P.q + (s.first + i) * P.q_token + (int64_t)(head * P.group + (skip + c - over * P.group)) * P.q_head;
+                P.q + (int64_t)(s.first + i) * P.q_token + (int64_t)(head * P.group + (skip + c - over * P.group)) * P.q_head;
 #pragma unroll
             for (int j = 0; j < KC; ++j)
                 q[j] = *(const u32x4 *)(at + (D == 64 ? 16 * g + 8 * j : 32 * (g + 4 * (j / 4)) + 8 * (j % 4)));
@@ -400,16 +400,17 @@ __global__ __launch_bounds__(kAttnThreads)
             return;
         s = sequence(P, b);
     } else {
-        const int64_t number = id / P.c.heads;
-        if (number >= P.blocks)
+        const int64_t behind = id / P.c.heads;
+        if (behind >= P.blocks)
             return;
-        int64_t first;
+        const int number = (int)behind;
+        int first;
         b = sequence_of(P, number, kRows, &first);
         s = sequence(P, b);
         if (number < first || number - first >= s.blocks)
             return;
-        head = (int)(id - number * P.c.heads);
-        block = (int)(number - first);
+        head = (int)(id - behind * P.c.heads);
+        block = number - first;
         at = 0;
         end = s.quanta;
     }
@@ -428,8 +429,7 @@ __global__ __launch_bounds__(kAttnThreads)
             block = index - head * s.blocks;
         }
         const int to = min(s.quanta, from + (end - at));
-        const int64_t row = (int64_t)block * kRows;
-        const int i0 = (int)(row / P.group), skip = (int)(row - (int64_t)i0 * P.group);
+        const int row = block * kRows, i0 = row / P.group, skip = row - i0 * P.group;
         const Rows rows = A.rows_of(s, i0, skip);
         A.load_q(s, i0, skip, head);
         A.run(s, rows, whole(P.tables + b * P.table_stride), head, from, to, wave);
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(kAttnThreads)
             }
         __syncthreads();
         const bool whole = from == 0 && to == s.quanta;
-        const int count = (int)min(s.rows - row, (int64_t)kRows);
+        const int count = min(s.rows - row, kRows);
         float *rec = record<D, kRows>(P, id, at == begin);
         for (int e = threadIdx.x; e < count * (D / 4); e += kAttnThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(kAttnThreads)
                 Join *j = join_of<D, kRows>(P, first_number(P, b, s.first, kRows) + block, head);
                 j->from = (int)id;
                 j->parts = whole ? 0
-                                 : (share_of(h.total, h.workers, at + s.quanta - 1) - (int)id + 1) |
+                                 : (share_of(h, at + s.quanta - 1) - (int)id + 1) |
                                        (at == begin ? kWholeShare : 0);
             }
         __syncthreads();
@@ -523,10 +523,7 @@ template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipSt
 }
 
 // Whether the sequences have rows enough, on average, for prompt_kernel
-bool prompts(int64_t T, int B, int group)
-{
-    return T * group >= (int64_t)B * 64 && T * group + (int64_t)B * 128 < INT32_MAX;
-}
+bool prompts(int64_t T, int B, int group) { return T * group >= (int64_t)B * 64; }
 
 }  // namespace
 
@@ -539,7 +536,7 @@ uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads,
     // quanta are shared out but where there are blocks for every CU many times
     // over, more sequences than a worker adds up, more quanta than 31 bits hold,
     // or sequences so short that a block's own waves are soon done (a second
-    // launch costs as much as 1000 tokens)
+    // launch and its parts cost as much as 2000 tokens)
     const int64_t blocks = most_blocks(T, B, group, kRows, true) * kv_heads;
     if (B > kMostBalanced || blocks >= (int64_t)cus * 16 || max_len <= kAloneTokens ||
         blocks * (max_len / kQuantum + 1) > INT32_MAX)

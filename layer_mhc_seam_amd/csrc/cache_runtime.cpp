@@ -128,7 +128,8 @@ int run_cache(const mhc_cache_args *a, bool write, void *stream)
 bool attention_sizes(int64_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t D)
 {
     return T >= 0 && T <= INT32_MAX && B >= 0 && B <= 65535 && kv_heads >= 1 && q_heads >= kv_heads &&
-           q_heads <= kMaxHeads && q_heads % kv_heads == 0 && width_known(D) && T * q_heads < (int64_t(1) << 34);
+           q_heads <= kMaxHeads && q_heads % kv_heads == 0 && width_known(D) &&
+           T * (q_heads / kv_heads) + 128 * (int64_t)B < INT32_MAX && T * q_heads < (int64_t(1) << 34);
 }
 
 }  // namespace
@@ -260,7 +261,7 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
     if (!attention_sizes(T, a->B, a->q_heads, a->kv_heads, a->head_dim))
         return fail(MHC_SEAM_INVALID_ARG,
                     "cache attention needs 0 <= T < 2^31, 0 <= B < 2^16, kv_heads that divide q_heads (up to %d), "
-                    "head_dim 64, 128 or 256, T*q_heads < 2^34", kMaxHeads);
+                    "head_dim 64, 128 or 256, T*q_heads/kv_heads + 128*B < 2^31, T*q_heads < 2^34", kMaxHeads);
     if (!half_type(a->dtype))
         return fail(MHC_SEAM_INVALID_ARG, "cache attention takes bf16 or f16");
     if (!page_known(a->page_size) || a->pages < 1 || a->pages > INT32_MAX / a->kv_heads || a->table_width < 1 ||

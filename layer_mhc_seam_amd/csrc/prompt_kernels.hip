@@ -377,7 +377,7 @@ template <int DT, int D, bool CAP> struct Prompt {
 
 // A block of rows and the tokens it sees
 struct Block {
-    int64_t first;          // its sequence's first query row
+    int first;              // its sequence's first query row
     int b, n, len;
     int i0, skip;           // begins with head `skip` of the sequence's query row i0
     int rows;               // 0: the number is no block's
@@ -385,34 +385,16 @@ struct Block {
     int begin, tiles;       // the first tile's first token; 1 tile at least
 };
 
-// Rows times heads of a kv head number below 2^31 in these kernels
 __device__ __forceinline__ Block block_of(const AttentionParams &P, int number)
 {
     constexpr int ROWS = kPromptRows;
     Block k;
+    int numbered;
     k.rows = k.tiles = 0;
-    int row;                // of the sequence's
-    if (!P.q_starts) {
-        const int each = (P.group + ROWS - 1) / ROWS;
-        k.b = number / each;
-        k.first = k.b;
-        k.n = 1;
-        row = (number - k.b * each) * ROWS;
-    } else {
-        auto numbered = [&](int64_t start, int b) { return (int)start * P.group / ROWS + b; };
-        int low = 0, high = P.B;
-        while (high - low > 1) {
-            const int mid = (low + high) / 2;
-            if (numbered(row_start(P, mid), mid) <= number)
-                low = mid;
-            else
-                high = mid;
-        }
-        k.b = low;
-        k.first = row_start(P, low);
-        k.n = max((int)(row_start(P, low + 1) - k.first), 0);
-        row = (number - numbered(k.first, low)) * ROWS;
-    }
+    k.b = sequence_of(P, number, ROWS, &numbered);
+    k.first = row_start(P, k.b);
+    k.n = max(row_start(P, k.b + 1) - k.first, 0);
+    const int row = (number - numbered) * ROWS;          // of the sequence's
     const int rows = k.n * P.group;
     if (row < 0 || row >= rows)
         return k;
@@ -515,7 +497,7 @@ void prompt_kernel(const AttentionParams P)
         row_sees(P, k.len, k.n, k.i0 + over, &A.lo, &A.hi);
         if (k.i0 + over >= k.n)
             A.lo = A.hi = 0;
-        const uint16_t *from_q = P.q + (k.first + min(k.i0 + over, k.n - 1)) * P.q_token +
+        const uint16_t *from_q = P.q + (int64_t)(k.first + min(k.i0 + over, k.n - 1)) * P.q_token +
                                  (int64_t)(head * P.group + (k.skip + r - over * P.group)) * P.q_head;
 #pragma unroll
         for (int i = 0; i < A.KC; ++i)
@@ -581,7 +563,7 @@ void prompt_kernel(const AttentionParams P)
         auto odd = __builtin_amdgcn_permlane32_swap(A.nans, A.nans, false, false);
         const u32 nans = odd[0] | odd[1];
         if (r < k.rows) {
-            const int64_t row = (k.first + k.i0 + over) * P.q_heads + head * P.group + (k.skip + r - over * P.group);
+            const int64_t row = (int64_t)(k.first + k.i0 + over) * P.q_heads + head * P.group + (k.skip + r - over * P.group);
             const float inv = !all ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
             // register i of product d is row x = 8 (i / 4) + 4 h + i % 4 of it, channel
             // x % 16 D/16 + 2 d + x / 16: D/16 channels side by side in two registers
@@ -628,7 +610,7 @@ void prompt_kernel(const AttentionParams P)
             if (!all) {
                 j->parts = (int)((workers * (at + k.tiles) - 1) / total) - worker + 1 |
                            (at == begin ? kWholeShare : 0);
-                parts->row = (k.first + k.i0) * P.q_heads + head * P.group;
+                parts->row = (int64_t)(k.first + k.i0) * P.q_heads + head * P.group;
                 parts->skip = k.skip;
                 parts->rows = k.rows;
                 parts->count = j->parts;

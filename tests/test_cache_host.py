@@ -137,7 +137,7 @@ def attention_args(T=4, B=4, Hq=8, Hk=2, D=128, ps=64, pages=8, width=4, **kw):
 
 @pytest.mark.parametrize("kw", [
     dict(T=-1), dict(T=1 << 31), dict(B=-1), dict(B=65536), dict(Hq=0), dict(Hq=7), dict(Hk=0), dict(Hq=1),
-    dict(Hq=8192), dict(D=80), dict(D=512), dict(dtype=2), dict(ps=8), dict(ps=100), dict(ps=1024), dict(pages=0),
+    dict(Hq=8192), dict(T=1 << 29, q_starts=slot(4)), dict(T=(1 << 31) - (1 << 22), Hq=2, q_starts=slot(4), B=65535), dict(D=80), dict(D=512), dict(dtype=2), dict(ps=8), dict(ps=100), dict(ps=1024), dict(pages=0),
     dict(pages=1 << 31), dict(width=0), dict(width=1 << 26), dict(max_len=-1), dict(window=-1), dict(causal=2),
     dict(scale=INF), dict(scale=NAN), dict(softcap=-1.0), dict(softcap=NAN), dict(softcap=INF), dict(reserved=3),
     dict(T=5), dict(q=None), dict(cache=None), dict(tables=None), dict(lens=None), dict(out=None),
