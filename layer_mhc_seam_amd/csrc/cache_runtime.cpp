@@ -119,7 +119,11 @@ int run_cache(const mhc_cache_args *a, bool write, void *stream)
     p.slots = a->slots;
     p.k = a->k;
     p.v = a->v;
-    const hipError_t e = launch_cache(p, a->head_dim, a->dtype, write, reinterpret_cast<hipStream_t>(stream));
+    int cus = 0;
+    hipError_t e = compute_units(&cus);
+    if (e != hipSuccess)
+        return hip_fail(e, "device attributes");
+    e = launch_cache(p, a->head_dim, a->dtype, write, cus, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess)
         return hip_fail(e, write ? "cache write launch" : "cache read launch");
     return MHC_SEAM_OK;

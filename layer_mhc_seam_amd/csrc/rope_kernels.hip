@@ -48,6 +48,15 @@ template <int DT> __device__ __forceinline__ uint16_t half_of(float v)
     return __builtin_bit_cast(uint16_t, (typename Half<DT>::type)v);
 }
 
+// Long vectors past the caches: T = 16384, 48 heads of 128 channels 6% faster
+template <int N> __device__ __forceinline__ void store(uint16_t *to, const Vec<N> &v)
+{
+    if constexpr (N == 8)
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), (u32x4 *)to);
+    else
+        *(Vec<N> *)to = v;
+}
+
 // A thread's unit: NP pairs, or 2 NP channels past the rotary ones to copy.
 template <int DT, int NP, bool INTER>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeParams P)
@@ -104,9 +113,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeParams P)
                 y = half_of<DT>(rounded(fmaf(w, cosine[j], u * sine[j])));
             }
         }
-        *(Vec<NP> *)(dst + at0) = a;
+        store(dst + at0, a);
         if (second)
-            *(Vec<NP> *)(dst + at1) = b;
+            store(dst + at1, b);
     }
 }
 

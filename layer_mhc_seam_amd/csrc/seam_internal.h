@@ -168,7 +168,7 @@ struct CacheParams {
     void *k;
     void *v;
 };
-hipError_t launch_cache(const CacheParams &p, int head_dim, int dtype, bool write, hipStream_t s);
+hipError_t launch_cache(const CacheParams &p, int head_dim, int dtype, bool write, int cus, hipStream_t s);
 
 // Attention over it (attention_kernels.hip)
 struct AttentionParams {
