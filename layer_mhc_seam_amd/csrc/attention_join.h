@@ -85,14 +85,16 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attention_join_kernel(const A
     const int number = (int)behind, head = (int)(segment - behind * P.c.heads);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int row = (int)(id % (BLOCK / ROWS)) * ROWS + wave / WAVES;
-    const Join j = *join_of<D, BLOCK>(P, number, head);
+    // starts that fall give a block to two workers, or to none: in range all the same
+    Join j = *join_of<D, BLOCK>(P, number, head);
+    j.from = min(max(j.from, 0), P.workers - 1);
     int first;
     const int b = sequence_of(P, number, BLOCK, &first);
     const int from = row_start(P, b), rows = (row_start(P, b + 1) - from) * P.group;
     // every block's Join has been written, those of numbers that no block has not
     if (number < first || (number - first) * BLOCK >= rows)
         return;
-    const int parts = j.parts & ~kWholeShare;
+    const int parts = min(j.parts & (kWholeShare - 1), P.workers - j.from);
     const int at = (number - first) * BLOCK;
     if (parts == 0 || (WAVES > 1 && at + row >= rows))      // the workgroup's all
         return;

@@ -57,7 +57,8 @@ __device__ __forceinline__ Sequence sequence(const AttentionParams &P, int b)
 }
 
 // A worker's share of all quanta, which are those of sequence after sequence, of
-// kv head after kv head in it, of block after block.  Their number is below 2^31.
+// kv head after kv head in it, of block after block.  Their number is below 2^31,
+// unless starts fall: then nobody has any.
 struct Share {
     int begin, end;
     int each, over;     // quanta of a worker; workers that have one more
@@ -90,10 +91,17 @@ __device__ Share share(const AttentionParams &P, int worker)
     Share h;
     // a worker for kLeastQuanta quanta of a block, if there are as many
     int shares = 0, own = quanta_of(P, lane, &shares), upto = sum_upto(own);
-    int total = (int)read_lane((u32)upto, 63);
-    for (int b0 = 64; b0 < P.B; b0 += 64)
-        total += (int)read_lane((u32)sum_upto(quanta_of(P, b0 + lane, &shares)), 63);
+    int total = (int)read_lane((u32)upto, 63), many = own >> 12;
+    for (int b0 = 64; b0 < P.B; b0 += 64) {
+        const int next = quanta_of(P, b0 + lane, &shares);
+        total = (int)((u32)total + read_lane((u32)sum_upto(next), 63));
+        many += next >> 12;
+    }
     shares = (int)read_lane((u32)sum_upto(shares), 63);
+    // a lane's `many` is below 2^23; with their sum at most 2^19 the total is below
+    // 2^31 + 2^12 kMostBalanced
+    if ((int)read_lane((u32)sum_upto(many), 63) > 1 << 19 || total < 0)
+        total = 0;
     const int workers = max(min(shares, P.workers), 1);
     h.each = total / workers;
     h.over = total - h.each * workers;

@@ -392,3 +392,25 @@ def test_nothing_to_do():
     out = S.cache_attention(d["q"][:0].cuda(), d["cache"].cuda(), d["tables"].cuda(), d["lens"].cuda(),
                             q_starts=torch.zeros(2, dtype=torch.int32).cuda())
     assert out.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("T,B", [(5, 3), (40, 64), (300, 4), (300, 40), (2000, 130)])
+def test_starts_that_fall_where_work_is_shared(T, B):
+    """Tables for 4096 tokens, starts to and fro: blocks that two sequences have, or none, and more work than there
+    are rows for.  Whatever the rows hold then, nothing is written outside of them and the call ends."""
+    from layer_mhc_seam_amd import seam as S
+    g = torch.Generator().manual_seed(T)
+    ps, D, pages = 16, 64, 300
+    cache = S.kv_cache(pages, 2, D, ps)
+    cache.fill_(0)
+    tables = torch.randint(-2, pages + 2, (B, 256), generator=g).to(torch.int32).cuda()
+    lens = torch.randint(0, 4097, (B,), generator=g).to(torch.int32).cuda()
+    q = torch.randn(T, 4, D, generator=g).to(BF).cuda()
+    guard = torch.full((T + 64, 4, D), 7.0, dtype=BF).cuda()
+    sums = torch.full((T + 64, 4), 9.0).cuda()
+    for starts in ([0, T] * (B // 2 + 1), [T, 0, T // 2] * B, torch.randint(-3, T + 4, (B + 1,), generator=g).tolist()):
+        S.cache_attention(q, cache, tables, lens, q_starts=torch.tensor(starts[:B + 1], dtype=torch.int32).cuda(),
+                          lse=True, out=(guard[32:T + 32], sums[32:T + 32]))
+    torch.cuda.synchronize()
+    assert (guard[:32] == 7.0).all() and (guard[T + 32:] == 7.0).all()
+    assert (sums[:32] == 9.0).all() and (sums[T + 32:] == 9.0).all()
