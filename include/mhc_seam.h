@@ -648,7 +648,7 @@ int mhc_cache_read(const mhc_cache_args *args, void *stream);
  *   lse        f32 [T][q_heads] or NULL
  *   workspace  16-byte aligned, as many bytes as mhc_cache_attention_workspace
  *              says.  Nothing has to be in it, nothing is kept in it; calls
- *              that may overlap need one each, and so do graphs that may
+ *              that may overlap need one each, and so do graphs that may.
  * kv_heads divides q_heads, q_heads up to 4096; B up to 65535; T * q_heads <
  * 2^34, T * q_heads / kv_heads + 128 * B < 2^31;
  * table_width * page_size at most 2^30; pages * kv_heads < 2^31.

@@ -28,6 +28,8 @@ constexpr int kQuantum = kStep * kAttnWaves;   // tokens that a workgroup's wave
 constexpr int kMostBalanced = 1024;       // sequences whose lengths a worker adds up
 constexpr int kLeastQuanta = 4;           // of a worker's share, where a block has as many
 constexpr int kAloneTokens = 2048;        // of sequences whose blocks a workgroup each has alone
+constexpr int kAloneBlocks = 8;           // a CU, of which each has a workgroup alone
+constexpr int64_t kPromptWork = 3 << 23;  // rows times heads times tokens
 
 // A sequence's share of the work: blocks of rows, and the quanta of tokens that
 // some row of it sees, the same number for every block and kv head.
@@ -530,8 +532,16 @@ template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipSt
     return D == 64 ? launch<DT, 64>(p, s) : D == 128 ? launch<DT, 128>(p, s) : launch<DT, 256>(p, s);
 }
 
-// Whether the sequences have rows enough, on average, for prompt_kernel
-bool prompts(int64_t T, int B, int group) { return T * group >= (int64_t)B * 64; }
+// Whether it is prompt_kernel's: sequences of 64 rows on average (64 sequences of
+// 4096 tokens, 8 kv heads of 128 channels: at 40 rows each 144 us by blocks of 16
+// rows and 162 by 128, at 80 243 and 213), and work enough for its tiles of 128
+// rows to fill the chip, rows times heads times tokens (8 kv heads, 5 heads each: 64
+// rows over 1024 tokens 11 and 29 us, 512 31.3 and 30.8; 64 over 4096 30 and 37, 256
+// 59 and 57; 32 over 16384 40.7 and 40.4; 8 times 64 over 1024 30.8 and 31.3)
+bool prompts(int64_t T, int B, int q_heads, int group, int64_t max_len)
+{
+    return T * group >= (int64_t)B * 64 && T * q_heads >= kPromptWork / max_len;
+}
 
 }  // namespace
 
@@ -539,22 +549,30 @@ uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads,
                                     int64_t max_len)
 {
     const int group = q_heads / kv_heads;
-    if (prompts(T, B, group))
+    if (max_len == 0)
+        return 0;
+    if (prompts(T, B, q_heads, group, max_len))
         return prompt_workspace_floats(T, B, q_heads, kv_heads, head_dim, cus, max_len);
-    // quanta are shared out but where there are blocks for every CU many times
-    // over, more sequences than a worker adds up, more quanta than 31 bits hold,
-    // or sequences so short that a block's own waves are soon done (a second
-    // launch and its parts cost as much as 2000 tokens)
+    // Quanta are shared out but where a workgroup a block does better:
+    // - short sequences: a second launch and its parts cost as much as 1500 tokens
+    //   (one sequence, 2 kv heads of 128 channels: 1024 tokens 9.6 us alone and 11.0
+    //   shared, 2048 14.8 and 11.1);
+    // - longer ones, if there is a block for every CU (64 sequences of 4096 tokens,
+    //   8 kv heads: 51 and 63 us; of 1 .. 4096 34 and 44; of 8192 107 and 120; one of
+    //   8192 among 63 of 512 49 and 21, for which they end at 4096);
+    // - many blocks for every CU (300 sequences of 2304 tokens: 141 and 156);
+    // and where there are more sequences than a worker adds up, or more quanta than
+    // 31 bits hold.
     const int64_t blocks = most_blocks(T, B, group, kRows, true) * kv_heads;
-    if (B > kMostBalanced || blocks >= (int64_t)cus * 16 || max_len <= kAloneTokens ||
-        blocks * (max_len / kQuantum + 1) > INT32_MAX)
+    if (B > kMostBalanced || blocks >= (int64_t)cus * kAloneBlocks ||
+        max_len <= (blocks < cus ? kAloneTokens : 2 * kAloneTokens) || blocks * (max_len / kQuantum + 1) > INT32_MAX)
         return 0;
     return join_floats(workers_of(cus, head_dim), blocks, kRows, head_dim);
 }
 
 hipError_t launch_attention(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
 {
-    if (prompts(a.T, a.B, a.group))
+    if (prompts(a.T, a.B, a.q_heads, a.group, a.max_len))
         return launch_prompt(a, head_dim, dtype, cus, s);
     AttentionParams p = a;
     p.blocks = most_blocks(p.T, p.B, p.group, kRows, p.q_starts != nullptr);

@@ -79,17 +79,43 @@ def widened(d, tokens=4200):
     return dict(d, tables=tables)
 
 
+def headed(d, n):
+    """The same with every kv head and its query heads n times."""
+    return dict(d, q=d["q"].repeat(1, n, 1), cache=d["cache"].repeat(1, n, 1))
+
+
+def ways(d):
+    """(the same case, how often its heads are in it): behind tables as they are, for 4200 tokens, with which work may
+    be split, and where there are rows enough for 2^20 tokens, with which it is as a long prompt's: of few row blocks,
+    shared out, and of more than there are workers."""
+    yield d, 1
+    yield widened(d), 1
+    T, Hq, D = d["q"].shape
+    B, Hk = len(d["lens"]), d["cache"].shape[1]
+    if T * Hq // Hk >= 64 * B:
+        yield widened(d, 1 << 20), 1
+        n = 300 // ((T * (Hq // Hk) // 128 + B) * Hk) + 1
+        yield widened(headed(d, n), 1 << 20), n
+
+
+def check_ways(d, want, single=False, **kw):
+    for case, n in ways(d):
+        got = run(case, single=single, **kw)
+        check(got, tuple(x.repeat(1, n, *[1] * (x.dim() - 2)) for x in want))
+        if n == 1:
+            last = got
+    return last
+
+
 def both(lens, rows, Hq, Hk, D, ps, dt, seed=0, sharp=1.0, width=None, visible=None, **kw):
-    """The definition's result, with short tables and with long ones."""
+    """The definition's result, in all the ways the work is split."""
     d, keys, values = batch(lens, rows, Hq, Hk, D, ps, dt, seed, sharp=sharp, width=width)
     single = all(n == 1 for n in rows)
     want = ref.attention(d["q"], keys, values, lens, d["starts"], visible, **kw)
-    for case in (d, widened(d)):
-        got = run(case, single=single, **kw)
-        check(got, want)
-        if single:
-            again = run(case, **kw)
-            assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    got = check_ways(d, want, single, **kw)
+    if single:
+        again = run(widened(d), **kw)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
     return d, got
 
 
@@ -219,13 +245,15 @@ def test_nan_reaches_who_sees_it(lens, rows, window, width, D, dt):
                               (1, lens[1] - 1, 0, 1), (2, 20, 1, 0), (2, 260, 1, 1), (1, 20, 1, 0)):
         put(d, b, t, kind, D, ps, block)
         (values if kind else keys)[b][t, :, block * 32:block * 32 + 32] = math.nan
-    got = run(d, window=window)
-    out, lse = got[0].cpu().to(F64), got[1].cpu().to(F64)
-    w, l, bound, lbound = ref.attention(d["q"], keys, values, lens, d["starts"], window=window)
-    assert torch.equal(out.isnan(), w.isnan()) and torch.equal(lse.isnan(), l.isnan())
-    assert w.isnan().any() and not w.isnan().all(dim=(1, 2)).all()
-    fine = ~w.isnan()
-    assert ((out - w).abs()[fine] <= bound[fine]).all()
+    want = ref.attention(d["q"], keys, values, lens, d["starts"], window=window)
+    for case, n in ways(d):
+        got = run(case, window=window)
+        out, lse = got[0].cpu().to(F64), got[1].cpu().to(F64)
+        w, l, bound, lbound = (x.repeat(1, n, *[1] * (x.dim() - 2)) for x in want)
+        assert torch.equal(out.isnan(), w.isnan()) and torch.equal(lse.isnan(), l.isnan())
+        assert w.isnan().any() and not w.isnan().all(dim=(1, 2)).all()
+        fine = ~w.isnan()
+        assert ((out - w).abs()[fine] <= bound[fine]).all()
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -252,7 +280,7 @@ def test_what_nobody_sees_may_be_anything(rows, D):
         check(long, ref.attention(d["q"], keys, values, lens, d["starts"], **kw))
         got = run(d, **kw)
         assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
-        check(got, ref.attention(d["q"], keys, values, lens, d["starts"], **kw))
+        check_ways(d, ref.attention(d["q"], keys, values, lens, d["starts"], **kw), **kw)
 
 
 @pytest.mark.parametrize("rows", [(3, 1, 1), (80, 60, 33)])
@@ -272,7 +300,7 @@ def bad_pages(rows, width):
         seen[b][page * ps:(page + 1) * ps] = False
     want = ref.attention(d["q"], keys, values, lens, d["starts"], seen)
     assert (want[0][-1] == 0).all()               # a sequence with no page left
-    check(run(d), want)
+    check_ways(d, want)
 
 
 def test_lengths_and_rows_that_do_not_fit():
@@ -394,7 +422,7 @@ def test_nothing_to_do():
     assert out.shape == (0, 4, 64)
 
 
-@pytest.mark.parametrize("T,B", [(5, 3), (40, 64), (300, 4), (300, 40), (2000, 130)])
+@pytest.mark.parametrize("T,B", [(5, 3), (40, 64), (300, 4), (300, 40), (2000, 130), (2000, 4), (20000, 3)])
 def test_starts_that_fall_where_work_is_shared(T, B):
     """Tables for 4096 tokens, starts to and fro: blocks that two sequences have, or none, and more work than there
     are rows for.  Whatever the rows hold then, nothing is written outside of them and the call ends."""
