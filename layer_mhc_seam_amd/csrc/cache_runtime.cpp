@@ -275,8 +275,9 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
                     "0 < table_width*page_size <= 2^30", kCacheMaxPage);
     if (a->max_len < 0 || a->window < 0 || (a->causal != 0 && a->causal != 1))
         return fail(MHC_SEAM_INVALID_ARG, "max_len and window must not be negative, causal 0 or 1");
-    if (!std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0)
-        return fail(MHC_SEAM_INVALID_ARG, "scale and softcap must be finite, softcap not negative");
+    if (!std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0 ||
+        (a->softcap > 0 && !std::isfinite(a->scale / a->softcap)))
+        return fail(MHC_SEAM_INVALID_ARG, "scale, softcap and their quotient must be finite, softcap not negative");
     if (a->reserved)
         return fail(MHC_SEAM_INVALID_ARG, "reserved fields must be zero");
     if (!a->q_starts && T != a->B)

@@ -1,10 +1,18 @@
 // prompt_kernels.hip -- attention over the 4-bit cache for many query rows a
 // sequence: prompts and chunks of them.
 //
-// The matrix cores bound it, 4 D operations a row and token.  A workgroup holds
-// 128 rows (query rows times heads of a kv head) and goes through the tokens in tiles of 64, once: keys and values are turned from 4 bits into
-// the products' type on their way into LDS, by all waves for all of them, while
-// the tile before is worked on.  A wave's products are 32 x 32 x 16:
+// The matrix cores bound it, 4 D operations a row and token, and the clock under
+// them: 4096 rows of 40 heads over 16384 tokens take 1150 to 1240 us, 0.97 to 1.04
+// PFLOP/s where a large bf16 product reaches 1.44; matrix and vector instructions
+// together are busy for 96% of the cycles, the clock between 1.4 and 2.0 GHz.
+// A workgroup holds 128 rows (query rows times heads of a kv head), 32 a wave (64 a
+// wave, one workgroup a CU: 1551 us for 1323 then), and goes through the tokens in
+// tiles of 64, once: keys and values are turned from 4 bits into the products' type
+// on their way into LDS, by all waves for all of them, while the tile before is
+// worked on (products of 4-bit by 8-bit operands, which would take the codes as they
+// are, sum to 2^-12.9 of the sum of magnitudes only, and are not used).  The order of
+// products, weights and LDS writes is written out: the compiler's own has all
+// products first.  A wave's products are 32 x 32 x 16:
 //   S^T = K Q^T     lane (q, h), q = l % 32, h = l / 32, holds row q of Q, and of
 //                   the result tokens 8 b + 4 h + r, b and r 0 .. 3
 //   O^T += V^T P^T  P is the operand as it stands: k = 16 tokens, of which lane h
@@ -649,9 +657,15 @@ uint64_t prompt_workspace_floats(int64_t T, int B, int q_heads, int kv_heads, in
 {
     const int workers = prompt_workers(cus, head_dim);
     const int64_t blocks = most_blocks(T, B, q_heads / kv_heads, kPromptRows, true) * kv_heads;
-    // tiles are shared out where the blocks leave half of the CUs' places empty
-    // and sequences may be long: joining costs as much as ten tiles
-    if (blocks * 2 > workers || max_len < kSharedTokens)
+    // Tiles are shared out where blocks are few and sequences may be long: joining
+    // costs as much as ten tiles (one sequence, 8 kv heads of 5 heads of 128
+    // channels: 640 rows over 1024 tokens 32 us by blocks, 47 shared, 700 over 2048
+    // 53 and 61, 512 over 4096 95 and 73, over 16384 353 and 193, 2000 over 16384 785
+    // and 660).  More than two blocks for every place of a workgroup fill the chip by
+    // themselves, the longest first (4096 rows over 16384 tokens: 1323 and 1360).
+    // With a share of at least 1, 4 or 12 tiles 64 rows over 4096 tokens of a table of
+    // 65536 take 41, 37 and 46 us.
+    if (blocks > 2 * workers || max_len <= kSharedTokens)
         return 0;
     return join_floats(workers, blocks, kPromptRows, head_dim) + parts_floats(workers);
 }

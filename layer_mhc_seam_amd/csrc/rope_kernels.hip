@@ -6,8 +6,12 @@
 // come from their Taylor series to degrees 9 and 10, whose next terms are below
 // 2^-28 there.  So a position of 2^20 costs no more bits than one of 3.
 //
-// Bytes bound it: each value is read and written once.  A thread keeps the
-// sines and cosines of NP pairs and turns them in several heads.
+// Bytes bound it: each value is read and written once, 16384 tokens of 48 heads of
+// 128 channels inside a product's rows, 403 MB, in 69 us into the same output again
+// and again, 88 into outputs in turn (a copy of as many bytes: 73).  A thread keeps
+// the sines and cosines of NP pairs and turns them in several heads: with two heads a
+// thread instead of eight that takes 106 us; with the next head's loads before this
+// one's stores, or a grid that stays, 87 to 99.
 #include <hip/hip_runtime.h>
 
 #include "half_ops.h"

@@ -139,7 +139,8 @@ def attention_args(T=4, B=4, Hq=8, Hk=2, D=128, ps=64, pages=8, width=4, **kw):
     dict(T=-1), dict(T=1 << 31), dict(B=-1), dict(B=65536), dict(Hq=0), dict(Hq=7), dict(Hk=0), dict(Hq=1),
     dict(Hq=8192), dict(T=1 << 29, q_starts=slot(4)), dict(T=(1 << 31) - (1 << 22), Hq=2, q_starts=slot(4), B=65535), dict(D=80), dict(D=512), dict(dtype=2), dict(ps=8), dict(ps=100), dict(ps=1024), dict(pages=0),
     dict(pages=1 << 31), dict(width=0), dict(width=1 << 26), dict(max_len=-1), dict(window=-1), dict(causal=2),
-    dict(scale=INF), dict(scale=NAN), dict(softcap=-1.0), dict(softcap=NAN), dict(softcap=INF), dict(reserved=3),
+    dict(scale=INF), dict(scale=NAN), dict(softcap=-1.0), dict(softcap=NAN), dict(softcap=INF), dict(scale=1e30, softcap=1e-30),
+    dict(reserved=3),
     dict(T=5), dict(q=None), dict(cache=None), dict(tables=None), dict(lens=None), dict(out=None),
     dict(q=slot(0) + 8), dict(cache=slot(1) + 4), dict(out=slot(5) + 2), dict(tables=slot(2) + 2),
     dict(lens=slot(3) + 1), dict(q_starts=slot(4) + 2), dict(lse=slot(6) + 2), dict(workspace=slot(7) + 4),
