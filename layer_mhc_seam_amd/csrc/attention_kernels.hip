@@ -582,7 +582,7 @@ uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads,
 
 hipError_t launch_attention(const AttentionParams &a, int head_dim, int dtype, int cus, hipStream_t s)
 {
-    if (prompts(a.T, a.B, a.q_heads, a.group, a.max_len))
+    if (prompts(a.T, a.B, a.q_heads, a.group, a.seen))
         return launch_prompt(a, head_dim, dtype, cus, s);
     AttentionParams p = a;
     p.blocks = most_blocks(p.T, p.B, p.group, kRows, p.q_starts != nullptr);

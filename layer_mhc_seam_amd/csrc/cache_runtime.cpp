@@ -303,6 +303,17 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
     if (a->max_len > 0 && a->max_len < max_len)
         max_len = a->max_len;
     const uint64_t floats = attention_workspace_floats(T, a->B, a->q_heads, a->kv_heads, a->head_dim, cus, max_len);
+    // A window leaves a sequence's rows window + n - 1 tokens, which choose the
+    // kernel as sequences of that length would (16 sequences' 5 rows over 4099 tokens,
+    // a window of 1024, 4 kv heads of 256 channels: 18.5 us, shared out 23.1).
+    int64_t seen = max_len;
+    if (a->window > 0 && a->window + T < seen)
+        seen = a->window + T;
+    uint64_t used = attention_workspace_floats(T, a->B, a->q_heads, a->kv_heads, a->head_dim, cus, seen);
+    if (used > floats) {
+        seen = max_len;
+        used = floats;
+    }
     if (floats && (!a->workspace || a->workspace_bytes < 4 * floats))
         return fail(MHC_SEAM_INVALID_ARG, "cache attention needs a workspace of %llu bytes",
                     (unsigned long long)(4 * floats));
@@ -337,7 +348,8 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
     p.q_starts = a->q_starts;
     p.out = (uint16_t *)a->out;
     p.lse = a->lse;
-    p.workspace = floats ? (float *)a->workspace : nullptr;
+    p.workspace = used ? (float *)a->workspace : nullptr;
+    p.seen = seen;
     e = launch_attention(p, a->head_dim, a->dtype, cus, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess)
         return hip_fail(e, "cache attention launch");

@@ -2,7 +2,7 @@
 // sequence: prompts and chunks of them.
 //
 // The matrix cores bound it, 4 D operations a row and token, and the clock under
-// them: 4096 rows of 40 heads over 16384 tokens take 1150 to 1240 us, 0.97 to 1.04
+// them: 4096 rows of 40 heads over 16384 tokens take 1150 to 1350 us, 0.89 to 1.04
 // PFLOP/s where a large bf16 product reaches 1.44; matrix and vector instructions
 // together are busy for 96% of the cycles, the clock between 1.4 and 2.0 GHz.
 // A workgroup holds 128 rows (query rows times heads of a kv head), 32 a wave (64 a

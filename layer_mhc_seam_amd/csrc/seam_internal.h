@@ -174,6 +174,7 @@ hipError_t launch_cache(const CacheParams &p, int head_dim, int dtype, bool writ
 struct AttentionParams {
     CacheLayout c;
     int64_t T, max_len;       // max_len: no more than the tables hold
+    int64_t seen;             // as much of it as a window leaves a sequence's rows
     int64_t q_token, q_head, table_stride;
     int B, q_heads, group;    // group: query heads a kv head
     int causal, window;

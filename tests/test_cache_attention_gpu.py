@@ -168,10 +168,14 @@ def test_prompt_masks(causal, window, softcap, scale, D, dt):
 @pytest.mark.parametrize("dt", [BF, F16])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("lens,rows,window", [([5000], [70], 0), ([100, 3000, 0, 2100], [1, 100, 2, 260], 0),
-                                              ([2500, 2500], [300, 90], 700), ([3000, 1, 40, 700], [70, 1, 40, 300], 0)])
+                                              ([2500, 2500], [300, 90], 700), ([3000, 1, 40, 700], [70, 1, 40, 300], 0),
+                                              ([5000, 40, 3000], [300, 40, 3], 2100)])
 def test_prompt_shares(lens, rows, window, D, dt):
-    """Few blocks of long sequences, whose tiles several workers share."""
-    both(lens, rows, 3, 1, D, 64, dt, window=window, width=80)
+    """Few blocks of long sequences, whose tiles several workers share; heads enough that a window leaves it so."""
+    d, keys, values = batch(lens, rows, 3, 1, D, 64, dt, width=80)
+    want = ref.attention(d["q"], keys, values, lens, d["starts"], window=window)
+    check_ways(d, want, window=window)
+    check(run(headed(d, 12), window=window), tuple(x.repeat(1, 12, *[1] * (x.dim() - 2)) for x in want))
 
 
 @pytest.mark.parametrize("dt", [BF, F16])
