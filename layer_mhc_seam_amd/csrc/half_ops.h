@@ -46,7 +46,6 @@ template <> struct Half<MHC_BF16> {
         return __builtin_bit_cast(u32, bf16x2{(__bf16)a, (__bf16)b});
     }
     static __device__ __forceinline__ float low(u32 w) { return __uint_as_float(w << 16); }
-    static __device__ __forceinline__ float high(u32 w) { return __uint_as_float(w & 0xffff0000u); }
     static __device__ __forceinline__ f32x4 mfma16(const u32x4 &a, const u32x4 &b, const f32x4 &c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
@@ -76,7 +75,6 @@ template <> struct Half<MHC_F16> {
         return __builtin_bit_cast(u32, f16x2{(_Float16)a, (_Float16)b});
     }
     static __device__ __forceinline__ float low(u32 w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }
-    static __device__ __forceinline__ float high(u32 w) { return (float)__builtin_bit_cast(f16x2, w)[1]; }
     static __device__ __forceinline__ f32x4 mfma16(const u32x4 &a, const u32x4 &b, const f32x4 &c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
