@@ -628,7 +628,8 @@ int mhc_cache_read(const mhc_cache_args *args, void *stream);
  *   out = sum_t exp(s_t) v_t / sum_t exp(s_t),   lse = log sum_t exp(s_t)
  * A row that sees nothing has out 0 and lse -inf.  What no row sees may hold
  * anything, NaN too.
- * Scores, sums and the output are held in binary32; products take q and the
+ * Scores, sums and the output are held in binary32, a capped score to 2^-21 of
+ * a cap up to 64, to 2^-19 of itself under a higher one; products take q and the
  * cache's values as they are and exp(s - max) rounded to dtype (with 2^12
  * before it in fp16, whose smallest numbers would end it at 2^-24), which
  * costs what one rounding of the output costs.  Results do not depend on what

@@ -151,7 +151,7 @@ struct Rows {
     int most_lo, least_hi;   // that every row of the block sees
 };
 
-template <int DT, int D, bool CAP> struct Attention {
+template <int DT, int D, int CAP> struct Attention {
     typedef Half<DT> H;
     typedef Softmax<DT> S;
     static constexpr int KC = D / 32;        // products of a score: 8 channels a lane each
@@ -293,8 +293,8 @@ template <int DT, int D, bool CAP> struct Attention {
             for (int i = 0; i < 4; ++i)
                 v[4 * h + i] = s[i];
         }
-        if constexpr (CAP) {
-            cap<8>(P, v);
+        if constexpr (CAP != kNoCap) {
+            cap<8, CAP>(P, v);
         } else {
             const float f = P.scale * kLog2e;
 #pragma unroll
@@ -395,7 +395,7 @@ template <int D> struct Shared {
 
 // BALANCED: the workers share all quanta evenly, and a block that several have
 // parts of is put together by attention_join_kernel.  Otherwise a workgroup a block.
-template <int DT, int D, bool CAP, bool BALANCED>
+template <int DT, int D, int CAP, bool BALANCED>
 __global__ __launch_bounds__(kAttnThreads)
     __attribute__((amdgpu_waves_per_eu(2))) void attention_kernel(const AttentionParams P)
 {
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(kAttnThreads)
 // 72 for 68, 32 of 1 .. 4096 38 for 31); one is slower still there (90, 45).
 int workers_of(int cus, int D) { return cus * (D == 256 ? 2 : 3); }
 
-template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
+template <int DT, int D, int CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
 {
     const int64_t segments = p.blocks * p.c.heads;
     if (p.workspace)
@@ -531,7 +531,10 @@ template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &
 
 template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
 {
-    const hipError_t e = p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
+    const Cap cap = cap_of(p.softcap);
+    const hipError_t e = cap == kNoCap ? launch_cap<DT, D, kNoCap>(p, s)
+                         : cap == kLow ? launch_cap<DT, D, kLow>(p, s)
+                                       : launch_cap<DT, D, kHigh>(p, s);
     if (e != hipSuccess || !p.workspace)
         return e;
     return launch_join<DT, D, kRows>(p, s);

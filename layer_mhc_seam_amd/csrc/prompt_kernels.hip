@@ -63,7 +63,7 @@ template <int D> struct RawValues {
     bool there;
 };
 
-template <int DT, int D, bool CAP> struct Prompt {
+template <int DT, int D, int CAP> struct Prompt {
     typedef Half<DT> H;
     typedef Softmax<DT> S;
     static constexpr int KC = D / 16, DC = D / 32, KU = (D + 127) / 128;
@@ -238,15 +238,20 @@ template <int DT, int D, bool CAP> struct Prompt {
     // lane's row does not see them, and the maximum brought up to them
     __device__ __forceinline__ void settle(int buf, int t, bool edge)
     {
-        if constexpr (CAP) {
-            float v[32];
+        if constexpr (CAP != kNoCap) {
+            // the series leaves no registers for more than eight at once
+            constexpr int N = CAP == kHigh ? 8 : 32;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v[j] = s[j / 16][j % 16];
-            cap<32>(P, v);
+            for (int j0 = 0; j0 < 32; j0 += N) {
+                float v[N];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                s[j / 16][j % 16] = v[j];
+                for (int j = 0; j < N; ++j)
+                    v[j] = s[(j0 + j) / 16][(j0 + j) % 16];
+                cap<N, CAP>(P, v);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    s[(j0 + j) / 16][(j0 + j) % 16] = v[j];
+            }
         }
         u32 there = 0;
 #pragma unroll
@@ -422,7 +427,7 @@ __device__ __forceinline__ Block block_of(const AttentionParams &P, int number)
 // consecutive shares go to one XCD, and a block that several have parts of is
 // put together by a join kernel.  Otherwise a workgroup a block, those of a
 // prompt's last rows, which have the most to do, first.
-template <int DT, int D, bool CAP, bool SHARED>
+template <int DT, int D, int CAP, bool SHARED>
 __global__ __launch_bounds__(64 * kPromptWaves) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 void prompt_kernel(const AttentionParams P)
 {
@@ -487,8 +492,8 @@ void prompt_kernel(const AttentionParams P)
     A_ A(P, L);
     // a negative scale's sign goes to the queries, one of 0 makes them 0: the
     // scores' order is that of their products, and -inf times the factor -inf
-    const u32 sign = CAP || P.scale >= 0 ? 0 : 0x80008000u, keep = CAP || P.scale != 0 ? ~0u : 0;
-    A.factor = CAP ? 1.0f : P.scale != 0 ? fabsf(P.scale) * kLog2e : 1.0f;
+    const u32 sign = CAP != kNoCap || P.scale >= 0 ? 0 : 0x80008000u, keep = CAP != kNoCap || P.scale != 0 ? ~0u : 0;
+    A.factor = CAP != kNoCap ? 1.0f : P.scale != 0 ? fabsf(P.scale) * kLog2e : 1.0f;
     while (at < end) {
         Block k = block_of(P, number);
         while (k.tiles == 0 || at - start >= k.tiles) {
@@ -630,7 +635,7 @@ void prompt_kernel(const AttentionParams P)
 
 int prompt_workers(int cus, int D) { return cus * (D == 256 ? 1 : 2); }
 
-template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
+template <int DT, int D, int CAP> hipError_t launch_cap(const AttentionParams &p, hipStream_t s)
 {
     if (!p.workspace) {
         prompt_kernel<DT, D, CAP, false><<<grid_of(p.blocks * p.c.heads), 64 * kPromptWaves, 0, s>>>(p);
@@ -643,7 +648,10 @@ template <int DT, int D, bool CAP> hipError_t launch_cap(const AttentionParams &
 
 template <int DT, int D> hipError_t launch(const AttentionParams &p, hipStream_t s)
 {
-    return p.softcap > 0 ? launch_cap<DT, D, true>(p, s) : launch_cap<DT, D, false>(p, s);
+    const Cap cap = cap_of(p.softcap);
+    return cap == kNoCap ? launch_cap<DT, D, kNoCap>(p, s)
+           : cap == kLow ? launch_cap<DT, D, kLow>(p, s)
+                         : launch_cap<DT, D, kHigh>(p, s);
 }
 
 template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipStream_t s)

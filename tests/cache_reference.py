@@ -129,9 +129,11 @@ def packed(k, v, order, pages, ps):
     return cache, *held
 
 
-def attention(q, keys, values, lens, q_starts, visible=None, scale=None, causal=True, window=0, softcap=0.0):
+def attention(q, keys, values, lens, q_starts, visible=None, scale=None, causal=True, window=0, softcap=0.0,
+              relative=False):
     """keys[b], values[b] [len, Hkv, D] in binary64 (as many tokens as lens[b] says at least); visible[b] bool [len]
-    or None.  Returns (out, lse, bound, lse_bound): bound is how far the output in q's type may be off."""
+    or None.  Returns (out, lse, bound, lse_bound): bound is how far the output in q's type may be off.  relative: a
+    capped score is off by a part of itself, not of the cap."""
     T, Hq, D = q.shape
     scale = D ** -0.5 if scale is None else scale
     u = torch.finfo(q.dtype).eps / 2
@@ -163,7 +165,11 @@ def attention(q, keys, values, lens, q_starts, visible=None, scale=None, causal=
             off = 2 * (D + 4) * 2.0 ** -24 * (torch.einsum("hd,thd->ht", x.abs(), K.abs()) * abs(scale))
             if softcap:
                 s = softcap * torch.tanh(s / softcap)
-                off = off + softcap * 2.0 ** -21
+                # relative: with h = 2^-24 for a rounding, fewer than 32 of them.  Up to c / 4 tanh's series: 7 with
+                # constants and factors.  Above, 1 - 2 / (e + 1): x is off by 2, 2 |x| log2 e by 2 more, so e by 8 |x|
+                # and exp2's 2, which sum and reciprocal take times e / (e + 1) and add 3: 5.5 at c / 4, times
+                # 2 / (e - 1) = 3.1, less farther on; then 4 with c log2 e
+                off = off + (s.abs() * 2.0 ** -19 if relative else softcap * 2.0 ** -21)
             off = off + 2.0 ** -22 * (s.abs() + 1)
             off = off.amax(1, keepdim=True)                      # [Hq, 1]
             e = torch.softmax(s, 1)

@@ -446,3 +446,17 @@ def test_starts_that_fall_where_work_is_shared(T, B):
     torch.cuda.synchronize()
     assert (guard[:32] == 7.0).all() and (guard[T + 32:] == 7.0).all()
     assert (sums[:32] == 9.0).all() and (sums[T + 32:] == 9.0).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("cap", [5.0, 64.0, 65.0, 1e3, 1e4, 1e5, 1e6, 1e8, 1e30, 3e38])
+@pytest.mark.parametrize("lens,rows", [((300, 41), (1, 1)), ((250, 90), (100, 5)), ((330, 140), (200, 140))])
+def test_capped_scores(lens, rows, cap, dt):
+    """A capped score is good to its own bits, however large the cap: far above the scores it changes nothing."""
+    for D, sharp in ((64, 1.0), (128, 4.0), (256, 30.0)):
+        d, keys, values = batch(lens, rows, 4, 2, D, 16, dt, seed=D, sharp=sharp)
+        want = ref.attention(d["q"], keys, values, lens, d["starts"], softcap=cap, relative=cap > 64)
+        check_ways(d, want, single=max(rows) == 1, softcap=cap)
+        if cap >= 1e30:
+            free = ref.attention(d["q"], keys, values, lens, d["starts"])
+            assert torch.equal(free[0], want[0]) or (free[0] - want[0]).abs().max() < 1e-12
