@@ -149,6 +149,7 @@ template <int D> struct Tile {
 struct Rows {
     int lo, hi;              // tokens that the lane's row sees
     int most_lo, least_hi;   // that every row of the block sees
+    int least_lo, most_hi;   // that some row of it sees
 };
 
 template <int DT, int D, int CAP> struct Attention {
@@ -196,10 +197,9 @@ template <int DT, int D, int CAP> struct Attention {
     __device__ Rows rows_of(const Sequence &s, int i0, int skip)
     {
         Rows w;
-        int none;
         const int i = i0 + (skip + c) / P.group, last = min(i0 + (skip + kRows - 1) / P.group, s.n - 1);
-        row_sees(P, s.len, s.n, i0, &none, &w.least_hi);
-        row_sees(P, s.len, s.n, last, &w.most_lo, &none);
+        row_sees(P, s.len, s.n, i0, &w.least_lo, &w.least_hi);
+        row_sees(P, s.len, s.n, last, &w.most_lo, &w.most_hi);
         row_sees(P, s.len, s.n, i, &w.lo, &w.hi);
         if (i >= s.n)
             w.lo = w.hi = 0;
@@ -248,7 +248,7 @@ template <int DT, int D, int CAP> struct Attention {
     }
 
     // Hides what the lane's row does not see of the 32 tokens at t0
-    __device__ void mask(Tile<D> &x, float v[8], const Rows &rows, int len, Whole table, int t0, int head)
+    __device__ void mask(Tile<D> &x, float v[8], const Rows &rows, Whole table, int t0, int head)
     {
         u32 nan_tokens = 0, seen = 0;
 #pragma unroll
@@ -257,9 +257,9 @@ template <int DT, int D, int CAP> struct Attention {
             const bool sees = x.there[i / 4] && t >= rows.lo && t < rows.hi;
             seen |= (u32)sees << i;
             v[i] = sees ? v[i] : -__builtin_inff();
-            // what no row sees may be anything; a NaN that only some rows see
-            // goes by `nans` to those
-            const bool valid = x.there[i / 4] && t < len;
+            // what no row sees may be anything, infinite too; a NaN that only
+            // some rows see goes by `nans` to those
+            const bool valid = x.there[i / 4] && t >= rows.least_lo && t < rows.most_hi;
 #pragma unroll
             for (int j = 0; j < (D + 127) / 128; ++j)
                 x.v[i][j] = valid ? x.v[i][j] : 0;
@@ -275,7 +275,7 @@ template <int DT, int D, int CAP> struct Attention {
                     nans |= nan_groups<D>(P, table, t0 + 16 * (i / 4) + 4 * g + i % 4, head);
     }
 
-    __device__ __forceinline__ void step(Tile<D> &x, const Rows &rows, int len, Whole table, int t0, int head)
+    __device__ __forceinline__ void step(Tile<D> &x, const Rows &rows, Whole table, int t0, int head)
     {
         float v[8];
 #pragma unroll
@@ -302,7 +302,7 @@ template <int DT, int D, int CAP> struct Attention {
                 v[i] *= f;
         }
         if (!(t0 >= rows.most_lo && t0 + kStep <= rows.least_hi && x.there[0] && x.there[1]))
-            mask(x, v, rows, len, table, t0, head);
+            mask(x, v, rows, table, t0, head);
         const float most =
             fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
         if (__any(most > top + S::kSlack)) {
@@ -375,12 +375,12 @@ template <int DT, int D, int CAP> struct Attention {
         load(a, table, s.len, t, head);
         while (true) {
             load(b, table, s.len, t + kQuantum, head);
-            step(a, rows, s.len, table, t, head);
+            step(a, rows, table, t, head);
             t += kQuantum;
             if (t >= end)
                 break;
             load(a, table, s.len, t + kQuantum, head);
-            step(b, rows, s.len, table, t, head);
+            step(b, rows, table, t, head);
             t += kQuantum;
             if (t >= end)
                 break;

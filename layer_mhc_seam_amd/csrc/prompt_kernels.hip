@@ -162,14 +162,16 @@ template <int DT, int D, int CAP> struct Prompt {
     }
 
     // Where some row sees only some of the tile's tokens (edge) a NaN among its
-    // values is left out and noted; tokens that are not there are 0
-    __device__ __forceinline__ void clean(RawValues<D> &x, int buf, int len, int t, bool edge)
+    // values is left out and noted; tokens that are not there, or outside those
+    // [from, to) that some row sees, are 0
+    __device__ __forceinline__ void clean(RawValues<D> &x, int buf, int from, int to, int t, bool edge)
     {
         u32 odd = 0;
         if (edge || !x.there) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool valid = x.there && t + 16 * wave + value_token() + i < len;
+                const int token = t + 16 * wave + value_token() + i;
+                const bool valid = x.there && token >= from && token < to;
                 const u32 byte = x.scale >> (8 * i) & 255;
                 odd |= (u32)(byte == 255 && valid);
 #pragma unroll
@@ -532,7 +534,7 @@ void prompt_kernel(const AttentionParams P)
             A.load(vals, table, k.len, t, head);
             __syncthreads();             // the block before is done with LDS
             A.put(keys, 0);
-            A.clean(vals, 0, k.len, t, is_edge(t));
+            A.clean(vals, 0, k.least_lo, k.most_hi, t, is_edge(t));
             A.put(vals, 0);
             A.load(keys, table, k.len, t + kTile, head);
             A.put(keys, 1);
@@ -549,7 +551,7 @@ void prompt_kernel(const AttentionParams P)
             while (t + kTile < past) {
                 if (is_edge(t))
                     A.note(buf, table, t, head);
-                A.clean(vals, buf ^ 1, k.len, t + kTile, is_edge(t + kTile));
+                A.clean(vals, buf ^ 1, k.least_lo, k.most_hi, t + kTile, is_edge(t + kTile));
                 f32x16 next[2];
                 A.products_and_weights(next, buf ^ 1);
                 A.values_and_puts(buf, vals, keys);

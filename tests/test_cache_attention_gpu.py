@@ -460,3 +460,25 @@ def test_capped_scores(lens, rows, cap, dt):
         if cap >= 1e30:
             free = ref.attention(d["q"], keys, values, lens, d["starts"])
             assert torch.equal(free[0], want[0]) or (free[0] - want[0]).abs().max() < 1e-12
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [(1, 3, 1, 2), (70, 129, 1, 100)])
+@pytest.mark.parametrize("dt,byte", [(BF, 254), (F16, 254), (F16, 150)])
+def test_what_nobody_sees_may_be_infinite(dt, byte, rows, D):
+    """Codes and scales that are past the type's range everywhere but in the tokens, before a window above all."""
+    lens, ps = [70, 129, 1, 260], 32
+    for kw in ({}, dict(window=40), dict(window=33, causal=False), dict(window=7, softcap=20.0)):
+        d, keys, values = batch(lens, rows, 4, 2, D, ps, dt, seed=2)
+        dirty = torch.full_like(d["cache"], 0x77)            # 6, and 6
+        dirty[:, :, ps * D:] = byte
+        for b, n in enumerate(lens):
+            for t in range(max(0, n - rows[b] + 1 - kw.get("window", n)), n):
+                page, at = int(d["tables"][b, t // ps]), t % ps
+                for kind in range(2):
+                    c = kind * ps * D // 2 + at * D // 2
+                    s = ps * D + kind * ps * D // 32 + torch.arange(D // 32) * ps + at
+                    dirty[page, :, c:c + D // 2] = d["cache"][page, :, c:c + D // 2]
+                    dirty[page, :, s] = d["cache"][page, :, s]
+        d["cache"] = dirty
+        check_ways(d, ref.attention(d["q"], keys, values, lens, d["starts"], **kw), **kw)
