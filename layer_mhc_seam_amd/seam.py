@@ -934,7 +934,8 @@ def cache_attention(q, cache, tables, lens, *, q_starts=None, scale=None, causal
     sees the tokens up to its own (causal) or all, the last `window` of them
     if window > 0; scores are q . k * scale (D ** -0.5), capped by softcap *
     tanh(s / softcap) if softcap > 0.  Rows that see nothing are 0.
-    max_len: no sequence is longer, or is cut there.
+    max_len: no sequence is longer, or is cut there; past what the tables hold
+    it says nothing.
     Returns out [T, Hq, D] in q's type, and with lse the logarithms of the sums
     too (f32 [T, Hq]), by which parts over different tokens can be joined.  out:
     the tensor, or with lse the pair, to write to; rows that belong to no
@@ -952,7 +953,6 @@ def cache_attention(q, cache, tables, lens, *, q_starts=None, scale=None, causal
     T, Hq, D = shape = q.shape
     B, width = tables.shape
     Hk = cache.shape[1]
-    most = 0 if max_len is None else max_len
     _fits(Hq | D | B | width | window)
     index = q.get_device()
     qs = _head_strides("q", q, dt, shape, index)
@@ -975,7 +975,8 @@ def cache_attention(q, cache, tables, lens, *, q_starts=None, scale=None, causal
             out, sums = out
             _need("lse", sums, torch.float32, (T, Hq), index)
         _need("out", out, dt, shape, index)
-    size = cache_attention_workspace(T, B, Hq, Hk, D, _compute_units(index), most or width * ps)
+    most = width * ps if max_len is None else min(max_len, width * ps)
+    size = cache_attention_workspace(T, B, Hq, Hk, D, _compute_units(index), most)
     space = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=q.device) if size else None
     a = CacheAttentionArgs(T, most, pages, *qs, tables.stride(0) if B > 1 else width, B, Hq, Hk, D, ps,
                            width, _types()[1][dt], bool(causal), window,

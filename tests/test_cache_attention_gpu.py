@@ -482,3 +482,18 @@ def test_what_nobody_sees_may_be_infinite(dt, byte, rows, D):
                     dirty[page, :, s] = d["cache"][page, :, s]
         d["cache"] = dirty
         check_ways(d, ref.attention(d["q"], keys, values, lens, d["starts"], **kw), **kw)
+
+
+def test_longest_length_past_the_table():
+    """max_len beyond what the tables hold says nothing new, whatever the workspace of such a length would be."""
+    for B, Hq, Hk, n in ((64, 40, 8, 0), (1, 8, 2, 0), (3, 12, 4, 150)):
+        lens = [200 - b for b in range(B)] if n == 0 else [n + 30, n, n + 7]
+        rows = [1] * B if n == 0 else [n] * B
+        d, keys, values = batch(lens, rows, Hq, Hk, 64, 64, BF, seed=B)
+        d = widened(d, 8192)
+        want = ref.attention(d["q"], keys, values, lens, d["starts"])
+        plain = run(d, single=n == 0)
+        check(plain, want)
+        for most in (8193, 1 << 20, 1 << 29, 1 << 30, (1 << 31) - 1, 1 << 40):
+            got = run(d, single=n == 0, max_len=most)
+            assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
