@@ -689,8 +689,9 @@ int mhc_cache_attention(const mhc_cache_attention_args *args, void *stream);
 /*
  * Bytes of workspace for such a call: a function of T, B, q_heads, kv_heads,
  * head_dim, cu_count (the device's compute units) and max_len (the call's, or
- * what the table holds where that is less or max_len 0) alone; often 0.  Host
- * only.  INVALID_ARG for sizes that the call refuses.
+ * what the table holds where that is less or max_len 0) alone; often 0, and
+ * never less for a longer max_len.  Host only.  INVALID_ARG for sizes that the
+ * call refuses.
  */
 int mhc_cache_attention_workspace(int64_t T, int32_t B, int32_t q_heads, int32_t kv_heads,
                                   int32_t head_dim, int32_t cu_count, int64_t max_len,

@@ -574,11 +574,10 @@ uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads,
     //   8 kv heads: 51 and 63 us; of 1 .. 4096 34 and 44; of 8192 107 and 120; one of
     //   8192 among 63 of 512 49 and 21, for which they end at 4096);
     // - many blocks for every CU (300 sequences of 2304 tokens: 141 and 156);
-    // and where there are more sequences than a worker adds up, or more quanta than
-    // 31 bits hold.
+    // and where there are more sequences than a worker adds up.
     const int64_t blocks = most_blocks(T, B, group, kRows, true) * kv_heads;
     if (B > kMostBalanced || blocks >= (int64_t)cus * kAloneBlocks ||
-        max_len <= (blocks < cus ? kAloneTokens : 2 * kAloneTokens) || blocks * (max_len / kQuantum + 1) > INT32_MAX)
+        max_len <= (blocks < cus ? kAloneTokens : 2 * kAloneTokens))
         return 0;
     return join_floats(workers_of(cus, head_dim), blocks, kRows, head_dim);
 }
@@ -590,6 +589,9 @@ hipError_t launch_attention(const AttentionParams &a, int head_dim, int dtype, i
     AttentionParams p = a;
     p.blocks = most_blocks(p.T, p.B, p.group, kRows, p.q_starts != nullptr);
     p.workers = workers_of(cus, head_dim);
+    // quanta are counted in 31 bits; a window's first token may lie inside one
+    if (p.blocks * p.c.heads * (p.seen / kQuantum + 2) > INT32_MAX)
+        p.workspace = nullptr;
     return dtype == MHC_BF16 ? launch_width<MHC_BF16>(p, head_dim, s) : launch_width<MHC_F16>(p, head_dim, s);
 }
 

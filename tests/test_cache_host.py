@@ -174,6 +174,23 @@ def test_attention_workspace():
         S.cache_attention_workspace(1, 2 ** 32 + 1, 8, 2, 128)
 
 
+def test_attention_workspace_never_falls_with_the_longest_length():
+    """What suffices for a length suffices for shorter ones: so a workspace may be had once, for the longest."""
+    import random
+    r = random.Random(1)
+    cases = [(64, 64, 40, 8, 128, 256), (1, 1, 8, 2, 128, 256), (300, 4, 16, 2, 256, 256)]
+    for _ in range(300):
+        kv, B = r.choice((1, 2, 4, 5, 8, 16, 40)), round(math.exp(r.uniform(0, 8)))
+        cases.append((B * r.choice((1, 1, 2, 5, 40, 300, 1000)), B, kv * r.choice((1, 2, 4, 5, 8, 16)), kv,
+                      r.choice((64, 128, 256)), r.choice((256, 256, 304, 64))))
+    lens = sorted([1 << k for k in range(31)] + [(1 << k) + 1 for k in range(30)]
+                  + [round(math.exp(r.uniform(4, 14))) for _ in range(60)])
+    for case in cases:
+        sizes = [S.cache_attention_workspace(*case, n) for n in lens]
+        assert sizes == sorted(sizes), case
+    assert S.cache_attention_workspace(64, 64, 40, 8, 128) == S.cache_attention_workspace(64, 64, 40, 8, 128, 256, 8192)
+
+
 # --------------------------------------------------------------- binding --
 
 def bf(*shape):
