@@ -1,6 +1,7 @@
 // cache_runtime.cpp -- C ABI of the rotary positions, the 4-bit cache and the
 // attention over it.  Argument rules only; each call is checked in full before
-// any device call is made.
+// any device call is made, but for the attention's workspace, whose size goes by
+// the device's compute units and which is checked before the launch.
 
 #include <cmath>
 #include <cstdint>
@@ -295,6 +296,14 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
         return fail(MHC_SEAM_INVALID_ARG, "q's strides are positive multiples of 8 that keep heads and tokens apart");
     if (a->B > 1 && (a->table_stride < a->table_width || a->table_stride >= kMaxElements))
         return fail(MHC_SEAM_INVALID_ARG, "table_stride must be table_width at least");
+    const Range ins[5] = {q.range(),
+                          {a->cache, a->pages * a->kv_heads * (int64_t)cache_page_bytes(a->page_size, a->head_dim)},
+                          {a->tables, 4 * ((a->B - 1) * a->table_stride + a->table_width)},
+                          {a->lens, 4 * (int64_t)a->B},
+                          {a->q_starts, 4 * (int64_t)(a->B + 1)}};
+    const Range out{a->out, 2 * T * a->q_heads * D}, lse{a->lse, 4 * T * a->q_heads};
+    if (clash({out, lse}, {ins[0], ins[1], ins[2], ins[3], ins[4]}))
+        return fail(MHC_SEAM_INVALID_ARG, "an output overlaps an input or the other output");
     int cus = 0;
     hipError_t e = compute_units(&cus);
     if (e != hipSuccess)
@@ -317,16 +326,9 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
     if (floats && (!a->workspace || a->workspace_bytes < 4 * floats))
         return fail(MHC_SEAM_INVALID_ARG, "cache attention needs a workspace of %llu bytes",
                     (unsigned long long)(4 * floats));
-    const Range ins[5] = {q.range(),
-                          {a->cache, a->pages * a->kv_heads * (int64_t)cache_page_bytes(a->page_size, a->head_dim)},
-                          {a->tables, 4 * ((a->B - 1) * a->table_stride + a->table_width)},
-                          {a->lens, 4 * (int64_t)a->B},
-                          {a->q_starts, 4 * (int64_t)(a->B + 1)}};
-    if (clash({{a->out, 2 * T * a->q_heads * D},
-               {a->lse, 4 * T * a->q_heads},
-               {floats ? a->workspace : nullptr, 4 * (int64_t)floats}},
-              {ins[0], ins[1], ins[2], ins[3], ins[4]}))
-        return fail(MHC_SEAM_INVALID_ARG, "an output or the workspace overlaps an input or another output");
+    const Range space{floats ? a->workspace : nullptr, 4 * (int64_t)floats};
+    if (clash({space}, {ins[0], ins[1], ins[2], ins[3], ins[4], out, lse}))
+        return fail(MHC_SEAM_INVALID_ARG, "the workspace overlaps an input or an output");
     AttentionParams p{};
     p.c = cache_layout(a->pages, a->kv_heads, a->page_size);
     p.T = T;

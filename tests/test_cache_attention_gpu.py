@@ -497,3 +497,37 @@ def test_longest_length_past_the_table():
         for most in (8193, 1 << 20, 1 << 29, 1 << 30, (1 << 31) - 1, 1 << 40):
             got = run(d, single=n == 0, max_len=most)
             assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+
+
+@pytest.mark.parametrize("rows", [1, 400])
+def test_workspace_refusals(rows):
+    """A workspace that is missing, too small, or over what the call reads or writes: refused, and nothing is done."""
+    import ctypes
+    from layer_mhc_seam_amd import seam as S
+    B, Hq, Hk, D, ps, width = 2, 8, 2, 128, 64, 80
+    T = B * rows
+    size = S.cache_attention_workspace(T, B, Hq, Hk, D, S._compute_units(0), width * ps)
+    assert size > 0
+    q = torch.randn(T, Hq, D).to(BF).cuda()
+    cache = S.kv_cache(8, Hk, D, ps)
+    tables, lens = torch.zeros(B, width, dtype=torch.int32).cuda(), torch.full((B,), 256, dtype=torch.int32).cuda()
+    starts = torch.arange(0, T + 1, rows, dtype=torch.int32).cuda()
+    out, lse = torch.full_like(q, 3.0), torch.full((T, Hq), 4.0).cuda()
+    space = torch.empty(size, dtype=torch.uint8).cuda()
+
+    def call(workspace, nbytes):
+        a = S.CacheAttentionArgs(T, 0, 8, Hq * D, D, width, B, Hq, Hk, D, ps, width, 0, 1, 0, 0.1, 0.0, 0, q.data_ptr(),
+                                 cache.data_ptr(), tables.data_ptr(), lens.data_ptr(), starts.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), workspace, nbytes)
+        return S.lib().mhc_cache_attention(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+
+    for t in (q, cache, tables, lens, starts, out, lse):
+        assert call(t.data_ptr(), size) == S.INVALID_ARG
+        # ends inside the tensor, by 16 bytes
+        assert call((t.data_ptr() + 15) // 16 * 16 - size // 16 * 16 - (16 if size % 16 else 0) + 16, size) == S.INVALID_ARG
+    assert call(None, size) == call(space.data_ptr(), size - 1) == call(space.data_ptr() + 4, size) == S.INVALID_ARG
+    torch.cuda.synchronize()
+    assert (out == 3.0).all() and (lse == 4.0).all()
+    assert call(space.data_ptr(), size) == S.OK
+    torch.cuda.synchronize()
+    assert not (out == 3.0).any() and not (lse == 4.0).any()

@@ -151,6 +151,18 @@ def test_attention_refuses(kw):
     assert message()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(out=slot(0)), dict(out=slot(0) + 4 * 2048 - 16), dict(out=slot(1) + 16 * PAGE - 16), dict(out=slot(2)),
+    dict(out=slot(3)), dict(out=slot(3) - 4 * 2048 + 16), dict(q_starts=slot(4), out=slot(4)),
+    dict(q_starts=slot(4), lse=slot(4) + 16), dict(lse=slot(0)), dict(lse=slot(1) + 16 * PAGE - 4),
+    dict(lse=slot(2) + 60), dict(lse=slot(3) + 12), dict(lse=slot(5) + 4 * 2048 - 4), dict(lse=slot(5) - 124),
+])
+def test_attention_refuses_overlaps(kw):
+    """out, 4 rows of 8 heads of 128 channels, and lse over the inputs and each other, by an element."""
+    assert S.lib().mhc_cache_attention(ctypes.byref(attention_args(**kw)), None) == S.INVALID_ARG
+    assert "overlaps" in message()
+
+
 def test_attention_nothing_to_do():
     call = S.lib().mhc_cache_attention
     assert call(ctypes.byref(attention_args(T=0, B=0, q=None, out=None)), None) == S.OK
