@@ -27,21 +27,21 @@ struct Rows {
     int64_t row() const { return (heads - 1) * head + D; }                 // of one token, end to end
     int64_t extent() const { return T > 0 ? (T - 1) * token + row() : 0; }
     Range range() const { return {p, 2 * extent()}; }
-    // Heads apart from each other inside a token, or tokens apart inside a head
+    // Strides above 0 and sizes whose products stay in 64 bits
+    bool small() const
+    {
+        return token > 0 && head > 0 && token < kMaxElements && head < kMaxElements && T <= INT32_MAX &&
+               (T <= 1 || token <= (kMaxElements - 1) / T) && head <= (kMaxElements - 1) / heads &&
+               extent() < kMaxElements;
+    }
+    // And heads apart from each other inside a token, or tokens apart inside a head
     bool apart() const
     {
-        if (token < 1 || head < 1)
+        if (!small())
             return false;
         const bool tokens_outside = (heads == 1 || head >= D) && (T == 1 || token >= row());
         const bool heads_outside = (T == 1 || token >= D) && (heads == 1 || head >= (T - 1) * token + D);
         return tokens_outside || heads_outside;
-    }
-    // Sizes whose products stay in 64 bits
-    bool small() const
-    {
-        return token < kMaxElements && head < kMaxElements && T <= INT32_MAX &&
-               (T <= 1 || token <= (kMaxElements - 1) / T) && head <= (kMaxElements - 1) / heads &&
-               extent() < kMaxElements;
     }
     bool same(const Rows &o) const { return p == o.p && token == o.token && head == o.head; }
 };
@@ -91,7 +91,7 @@ int check_cache(const mhc_cache_args *a, bool write)
     const Rows k{a->k, a->T, a->heads, a->head_dim, a->k_token, a->k_head};
     const Rows v{a->v, a->T, a->heads, a->head_dim, a->v_token, a->v_head};
     for (const Rows &x : {k, v})
-        if (x.p && (!x.apart() || !x.small() || x.token % 8 || x.head % 8))
+        if (x.p && (!x.apart() || x.token % 8 || x.head % 8))
             return fail(MHC_SEAM_INVALID_ARG,
                         "strides of k and v are positive multiples of 8 that keep heads and tokens apart");
     const Range cache{a->cache, a->pages * a->heads * (int64_t)cache_page_bytes(a->page_size, a->head_dim)};
@@ -184,7 +184,7 @@ int mhc_rope(const mhc_rope_args *a, void *stream)
     const Range others[2] = {{a->positions, (int64_t)a->position_bytes * ((a->axes - 1) * a->position_axis + T)},
                              {a->inv_freq, 2 * (int64_t)a->rotary}};
     for (int i = 0; i < tensors; ++i) {
-        if (!in[i].apart() || !in[i].small() || !out[i].apart() || !out[i].small())
+        if (!in[i].apart() || !out[i].apart())
             return fail(MHC_SEAM_INVALID_ARG, "rope's strides are positive and keep heads and tokens apart");
         in_place = in_place && in[i].same(out[i]);
     }
@@ -292,7 +292,7 @@ int mhc_cache_attention(const mhc_cache_attention_args *a, void *stream)
         return fail(MHC_SEAM_INVALID_ARG,
                     "q, cache, out and workspace must be 16-byte aligned, the others to their elements");
     const Rows q{a->q, T, a->q_heads, D, a->q_token, a->q_head};
-    if (!q.apart() || !q.small() || q.token % 8 || q.head % 8)
+    if (!q.apart() || q.token % 8 || q.head % 8)
         return fail(MHC_SEAM_INVALID_ARG, "q's strides are positive multiples of 8 that keep heads and tokens apart");
     if (a->B > 1 && (a->table_stride < a->table_width || a->table_stride >= kMaxElements))
         return fail(MHC_SEAM_INVALID_ARG, "table_stride must be table_width at least");

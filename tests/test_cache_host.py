@@ -45,6 +45,18 @@ def test_layout_addresses(tmp_path):
     assert got.returncode == 0 and got.stdout == "ok\n", got.stdout + got.stderr
 
 
+def test_checks_do_not_overflow(tmp_path):
+    """Sizes and strides at the ends of their types are refused before they are multiplied."""
+    exe = tmp_path / "checks"
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    trap = [f for x in ("-fsanitize=signed-integer-overflow", "-fsanitize-trap=signed-integer-overflow")
+            for f in ("-Xarch_host", x)]
+    subprocess.run([hipcc, "--offload-arch=gfx950", "-std=c++17", "-O1", *trap, "-x", "hip",
+                    os.path.join(HERE, "cache_arguments_check.cpp"), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert got.returncode == 0 and got.stdout == "ok\n", got.stdout + got.stderr
+
+
 # ------------------------------------------------------------------ rope --
 
 def rope_args(T=4, Hq=8, Hk=2, D=128, R=128, **kw):
