@@ -532,7 +532,7 @@ int mhc_route(const mhc_route_args *args, void *stream);
  * and k of a loss, given that with regard to the outputs.  Channels from
  * `rotary` on are copied.  theta is taken in binary64 and whole turns are
  * left out there, so far positions lose nothing: sine and cosine are within
- * 2^-22 (plus |p inv_freq| 2^-52) of the real angle's.  The rest is binary32,
+ * 2^-22 (plus |p inv_freq| 2^-51) of the real angle's.  The rest is binary32,
  * rounded once.
  *   q, k        dtype (MHC_BF16 or MHC_F16); a token's heads q_head apart, its
  *               channels dense, tokens q_token apart (elements), and so on: a

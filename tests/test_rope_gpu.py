@@ -187,3 +187,29 @@ def test_rope_refuses_on_the_device():
                  lambda: S.rope(q, None, pos, f, scale=float("inf")), lambda: S.rope(q, None, pos, f, scale=float("nan"))):
         with pytest.raises(S.SeamError):
             call()
+
+
+@pytest.mark.parametrize("start", [(1 << 32) + 7, -(1 << 33), (1 << 40) + 3, -(1 << 40)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_positions_past_32_bits(start, interleaved):
+    """Turns by the whole of a long position, each against the definition: an angle is off by 2^-51 of itself (three
+    roundings of 2^-53), which moves an output by as much of its pair's size."""
+    from layer_mhc_seam_amd import seam as S
+    g = torch.Generator().manual_seed(7)
+    T, D = 33, 128
+    q = torch.randn(T, 2, D, generator=g).to(F16)
+    pos = start + torch.arange(T)
+    f = (freqs(64) * 2 ** 10).round().clamp(min=1) / 2 ** 10       # their products with positions are exact
+    got = S.rope(q.cuda(), None, pos.cuda(), f.cuda(), interleaved=interleaved)[0].cpu()
+    want = ref.rope(q, pos, f, interleaved=interleaved)
+    a = q.to(F64).abs()
+    if interleaved:
+        size = (a[..., 0::2] + a[..., 1::2]).repeat_interleave(2, -1)
+        angle = (pos[:, None] * f.to(F64)).repeat_interleave(2, -1)
+    else:
+        size = (a[..., :64] + a[..., 64:]).repeat(1, 1, 2)
+        angle = (pos[:, None] * f.to(F64)).repeat(1, 2)
+    bound = 2.0 ** -11 * want.abs() + size * (2.0 ** -20 + angle.abs()[:, None] * 2.0 ** -51) + 2.0 ** -14
+    assert ((got.to(F64) - want).abs() <= bound).all()
+    short = S.rope(q.cuda(), None, (pos % (1 << 32)).cuda(), f.cuda(), interleaved=interleaved)[0].cpu()
+    assert ((got - short).abs().amax((1, 2)) > 0.1).all()          # not their low 32 bits
