@@ -192,3 +192,27 @@ def test_device_refusals():
     for call in (lambda: S.cache_write(c, y, y, s), lambda: S.cache_read(c, s, 64, out=(x, x))):
         with pytest.raises(S.SeamError):
             call()
+
+
+@pytest.mark.parametrize("H,D", [(1, 64), (5, 128), (3, 256)])
+def test_keys_or_values_alone(H, D):
+    """The C entry reads only what it is given a place for; what lies where the other would go stays."""
+    import ctypes
+    from layer_mhc_seam_amd import seam as S
+    g = torch.Generator().manual_seed(D)
+    T, ps, pages = 70, 16, 6
+    x = torch.randn(2, T, H, D, generator=g).to(BF).cuda()
+    slots = torch.randperm(pages * ps, generator=g)[:T]
+    slots[::9] = -1
+    slots = slots.cuda()
+    c = S.cache_write(S.kv_cache(pages, H, D, ps), x[0], x[1], slots)
+    want = S.cache_read(c, slots, D)
+    for kind in range(2):
+        out = torch.full((2, T, H, D), 7.0, dtype=BF).cuda()
+        at = [out[kind].data_ptr() if i == kind else None for i in range(2)]
+        for other in ((0, 0), (H * D, D)):              # the absent one's strides say nothing
+            strides = [(H * D, D) if i == kind else other for i in range(2)]
+            a = S.CacheArgs(T, pages, ps, H, D, 0, 8, 0, *strides[0], *strides[1], c.data_ptr(), slots.data_ptr(), *at)
+            assert S.lib().mhc_cache_read(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == S.OK
+        torch.cuda.synchronize()
+        assert torch.equal(out[kind], want[kind]) and (out[1 - kind] == 7.0).all()

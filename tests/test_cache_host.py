@@ -276,6 +276,16 @@ def test_kv_cache():
     assert S._cache_sizes.__name__ and 48 * 136 % (128 + 8) == 0
 
 
+def test_pages_of_a_cache():
+    for pages, H, D, ps in ((3, 2, 128, 48), (1, 1, 64, 16), (7, 5, 256, 512)):
+        shape = S.kv_cache(pages, H, D, ps, device="cpu").shape
+        assert S._pages_of(shape, H, D) == (pages, ps)
+        for bad in ((shape, H + 1, D), (shape[:2], H, D), ((pages, H, shape[2] + 1), H, D), ((pages, H, 0), H, D),
+                    ((pages, H, shape[2] + D + D // 16), H, D), (shape, H, 0)):
+            with pytest.raises(ValueError, match="cache"):
+                S._pages_of(*bad)
+
+
 # ------------------------------------------------------ plain definitions --
 
 def test_groups():
