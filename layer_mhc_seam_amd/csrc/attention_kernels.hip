@@ -550,7 +550,10 @@ template <int DT> hipError_t launch_width(const AttentionParams &p, int D, hipSt
 // rows and 162 by 128, at 80 243 and 213), and work enough for its tiles of 128
 // rows to fill the chip, rows times heads times tokens (8 kv heads, 5 heads each: 64
 // rows over 1024 tokens 11 and 29 us, 512 31.3 and 30.8; 64 over 4096 30 and 37, 256
-// 59 and 57; 32 over 16384 40.7 and 40.4; 8 times 64 over 1024 30.8 and 31.3)
+// 59 and 57; 32 over 16384 40.7 and 40.4; 8 times 64 over 1024 30.8 and 31.3).  One
+// kernel for the whole call: single rows beside a prompt fill a block of 128 rows with
+// their heads (63 of them beside 2048 rows, each over 8192 tokens, 703 us; the two as
+// calls of their own 370 and 105).
 bool prompts(int64_t T, int B, int q_heads, int group, int64_t max_len)
 {
     return T * group >= (int64_t)B * 64 && T * q_heads >= kPromptWork / max_len;
@@ -573,7 +576,11 @@ uint64_t attention_workspace_floats(int64_t T, int B, int q_heads, int kv_heads,
     // - longer ones, if there is a block for every CU (64 sequences of 4096 tokens,
     //   8 kv heads: 51 and 63 us; of 1 .. 4096 34 and 44; of 8192 107 and 120; one of
     //   8192 among 63 of 512 49 and 21, for which they end at 4096);
-    // - many blocks for every CU (300 sequences of 2304 tokens: 141 and 156);
+    // - many blocks for every CU (300 sequences of 2304 tokens: 141 and 156; 40 heads on
+    //   8, 256 of 5000 tokens 221 and 254, of 1 .. 8192 212 and 225).  That holds for
+    //   lengths alike: of 512 .. 65536, even over their logarithm, 732 and 582, and one
+    //   long sequence among 255 of 512 is one workgroup's way through it, one of 8192
+    //   71 and 50, of 32768 195 and 55, of 131072 699 and 73;
     // and where there are more sequences than a worker adds up.
     const int64_t blocks = most_blocks(T, B, group, kRows, true) * kv_heads;
     if (B > kMostBalanced || blocks >= (int64_t)cus * kAloneBlocks ||
